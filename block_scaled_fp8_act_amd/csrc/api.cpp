@@ -523,4 +523,181 @@ dsfp8_status dsfp8_moe_combine(const void* yr, int64_t R, int64_t ldy, const int
   return launched(dsfp8::launch_combine(a, stream));
 }
 
+// ---- int8 ------------------------------------------------------------------------------
+
+namespace {
+
+// The largest K for which |sum of K products of int8 values| < 2^31.
+constexpr int64_t kMaxI8K = 131071;
+
+inline int64_t pad16(int64_t n) { return (n + 15) / 16 * 16; }
+
+dsfp8_status row_quant_args(const void* x, bool f32, int64_t ldx, const void* u, int64_t ldu, int64_t M, int64_t K,
+                            void* y, int64_t ldy, float* s, dsfp8::RowQuantArgs& a) {
+  DSFP8_TRY(check_mat(x, M, K, ldx, f32 ? 4 : 2));
+  if (u != nullptr) DSFP8_TRY(check_mat(u, M, K, ldu, 2));
+  DSFP8_TRY(check_mat(y, M, K, ldy, 1));
+  DSFP8_TRY(check_mat(s, M, 1, 1, 4));
+  a = dsfp8::RowQuantArgs{};
+  a.x = x;
+  a.f32 = f32;
+  a.ldx = ldx;
+  a.u = static_cast<const uint16_t*>(u);
+  a.ldu = ldu;
+  a.M = M;
+  a.K = K;
+  a.y = static_cast<int8_t*>(y);
+  a.ldy = ldy;
+  a.s = s;
+  return DSFP8_OK;
+}
+
+dsfp8_status gemm_i8_args(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb, const float* b_s,
+                          void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, dsfp8::GemmI8Args& a) {
+  if (!dim_ok(M) || !dim_ok(N) || K < 0 || K > kMaxI8K) return DSFP8_ERR_SHAPE;
+  DSFP8_TRY(check_mat(A, M, K, lda, 1));
+  DSFP8_TRY(check_mat(a_s, M, 1, 1, 4));
+  DSFP8_TRY(check_mat(B, N, K, ldb, 1));
+  DSFP8_TRY(check_mat(b_s, N, 1, 1, 4));
+  DSFP8_TRY(check_mat(C, M, N, ldc, 2));
+  a = dsfp8::GemmI8Args{};
+  a.A = static_cast<const int8_t*>(A);
+  a.lda = lda;
+  a.a_s = a_s;
+  a.B = static_cast<const int8_t*>(B);
+  a.ldb = ldb;
+  a.b_s = b_s;
+  a.C = static_cast<uint16_t*>(C);
+  a.ldc = ldc;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  return DSFP8_OK;
+}
+
+// Quantise the rows of x (gated: of SiLU(x) * u) into the workspace, then the
+// product: codes [M, pad16(K)], then scales [M].
+dsfp8_status linear_i8(const void* x, int64_t ldx, const void* u, int64_t ldu, const void* B, int64_t ldb,
+                       const float* b_s, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(N) || K < 0 || K > kMaxI8K) return DSFP8_ERR_SHAPE;
+  DSFP8_TRY(check_mat(x, M, K, ldx, 2));
+  if (u != nullptr) DSFP8_TRY(check_mat(u, M, K, ldu, 2));
+  if (workspace_bytes < dsfp8_linear_i8_workspace_bytes(M, K)) return DSFP8_ERR_WORKSPACE;
+  if (workspace == nullptr && M > 0) return DSFP8_ERR_NULL;
+  if (!al(workspace, 16)) return DSFP8_ERR_ALIGN;
+  const int64_t ldy = pad16(K);
+  int8_t* y = static_cast<int8_t*>(workspace);
+  float* s = reinterpret_cast<float*>(y + M * ldy);
+  dsfp8::GemmI8Args g;
+  DSFP8_TRY(gemm_i8_args(y, ldy, s, B, ldb, b_s, C, ldc, M, N, K, g));
+  dsfp8::RowQuantArgs q;
+  DSFP8_TRY(row_quant_args(x, false, ldx, u, ldu, M, K, y, ldy, s, q));
+  if (M == 0 || N == 0) return DSFP8_OK;
+  const dsfp8_status st = launched(dsfp8::launch_row_quant_i8(q, stream));
+  return st == DSFP8_OK ? launched(dsfp8::launch_gemm_i8(g, stream)) : st;
+}
+
+}  // namespace
+
+dsfp8_status dsfp8_row_quant_i8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, void* y, int64_t ldy,
+                                float* s, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
+  if (dtype != DSFP8_DTYPE_F32 && dtype != DSFP8_DTYPE_BF16) return DSFP8_ERR_DTYPE;
+  dsfp8::RowQuantArgs a;
+  DSFP8_TRY(row_quant_args(x, dtype == DSFP8_DTYPE_F32, ldx, nullptr, 0, M, K, y, ldy, s, a));
+  return launched(dsfp8::launch_row_quant_i8(a, stream));
+}
+
+dsfp8_status dsfp8_silu_mul_row_quant_i8(const void* g, int64_t ldg, const void* u, int64_t ldu, int64_t M, int64_t I,
+                                         void* y, int64_t ldy, float* s, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(I)) return DSFP8_ERR_SHAPE;
+  if (u == nullptr && M > 0 && I > 0) return DSFP8_ERR_NULL;
+  dsfp8::RowQuantArgs a;
+  DSFP8_TRY(row_quant_args(g, false, ldg, u, ldu, M, I, y, ldy, s, a));
+  return launched(dsfp8::launch_row_quant_i8(a, stream));
+}
+
+dsfp8_status dsfp8_gemm_i8(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb,
+                           const float* b_s, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                           hipStream_t stream) {
+  dsfp8::GemmI8Args a;
+  DSFP8_TRY(gemm_i8_args(A, lda, a_s, B, ldb, b_s, C, ldc, M, N, K, a));
+  return launched(dsfp8::launch_gemm_i8(a, stream));
+}
+
+size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t K) {
+  if (!dim_ok(M) || K < 0 || K > kMaxI8K) return 0;
+  return (size_t)(M * pad16(K) + 4 * M);
+}
+
+dsfp8_status dsfp8_linear_i8(const void* x, int64_t ldx, const void* B, int64_t ldb, const float* b_s, void* C,
+                             int64_t ldc, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  return linear_i8(x, ldx, nullptr, 0, B, ldb, b_s, C, ldc, M, N, K, workspace, workspace_bytes, stream);
+}
+
+dsfp8_status dsfp8_silu_mul_linear_i8(const void* g, int64_t ldg, const void* u, int64_t ldu, const void* B,
+                                      int64_t ldb, const float* b_s, void* C, int64_t ldc, int64_t M, int64_t N,
+                                      int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (u == nullptr && M > 0 && K > 0) return DSFP8_ERR_NULL;
+  return linear_i8(g, ldg, u, ldu, B, ldb, b_s, C, ldc, M, N, K, workspace, workspace_bytes, stream);
+}
+
+// ---- routed experts for a few tokens ----------------------------------------------------
+
+size_t dsfp8_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) {
+  if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16 || !dim_ok(F)) return 0;
+  return dsfp8::moe_few_workspace_bytes(T, k, F);
+}
+
+dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx, const void* W13, int64_t ldw13, const float* s13,
+                           int64_t lds13, const void* W2, int64_t ldw2, const float* s2, int64_t lds2, int weight_fmt,
+                           const int32_t* indices, int64_t ldi, const void* weights, int64_t ldwt, int64_t T,
+                           int64_t k, int64_t E, int64_t D, int64_t F, void* out, int64_t ldo, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  static_assert(DSFP8_MOE_FEW_MAX_TOKENS == dsfp8::kMoeFewTokens, "header and library agree");
+  if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16 || E < 1 || E > kMaxExperts) return DSFP8_ERR_SHAPE;
+  if (!dim_ok(D) || !dim_ok(F) || !dim_ok(2 * F)) return DSFP8_ERR_SHAPE;
+  if (weight_fmt != DSFP8_WEIGHT_E4M3 && weight_fmt != DSFP8_WEIGHT_I8) return DSFP8_ERR_DTYPE;
+  const bool i8 = weight_fmt == DSFP8_WEIGHT_I8;
+  DSFP8_TRY(check_mat(x, T, D, ldx, 2));
+  DSFP8_TRY(check_mat(W13, E * 2 * F, D, ldw13, 1));
+  DSFP8_TRY(check_mat(W2, E * D, F, ldw2, 1));
+  DSFP8_TRY(i8 ? check_mat(s13, E, 2 * F, lds13, 4) : check_mat(s13, E * nblk(2 * F), nblk(D), lds13, 4));
+  DSFP8_TRY(i8 ? check_mat(s2, E, D, lds2, 4) : check_mat(s2, E * nblk(D), nblk(F), lds2, 4));
+  DSFP8_TRY(check_mat(indices, T, k, ldi, 4));
+  DSFP8_TRY(check_mat(weights, T, k, ldwt, 2));
+  DSFP8_TRY(check_mat(out, T, D, ldo, 2));
+  if (workspace_bytes < dsfp8_moe_few_workspace_bytes(T, k, F)) return DSFP8_ERR_WORKSPACE;
+  if (workspace == nullptr && T > 0) return DSFP8_ERR_NULL;
+  if (!al(workspace, 16)) return DSFP8_ERR_ALIGN;
+  if (T == 0 || D == 0) return DSFP8_OK;
+  dsfp8::MoeFewArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.w13 = static_cast<const uint8_t*>(W13);
+  a.ldw13 = ldw13;
+  a.s13 = s13;
+  a.lds13 = lds13;
+  a.w2 = static_cast<const uint8_t*>(W2);
+  a.ldw2 = ldw2;
+  a.s2 = s2;
+  a.lds2 = lds2;
+  a.i8 = i8;
+  a.indices = indices;
+  a.ldi = ldi;
+  a.weights = static_cast<const uint16_t*>(weights);
+  a.ldwt = ldwt;
+  a.T = (int)T;
+  a.k = (int)k;
+  a.E = E;
+  a.D = D;
+  a.F = F;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  a.work = workspace;
+  return launched(dsfp8::launch_moe_few(a, stream));
+}
+
 }  // extern "C"

@@ -123,6 +123,61 @@ struct GemmArgs {
   bool q_ue8m0;
 };
 
+// int8 quantisation of rows, one scale per row.
+struct RowQuantArgs {
+  const void* x;       // fp32 or bf16 input (bf16 gate input when u != nullptr)
+  bool f32;
+  int64_t ldx;
+  const uint16_t* u;   // bf16 up-projection input of the gated form, or nullptr
+  int64_t ldu;
+  int64_t M, K;
+  int8_t* y;
+  int64_t ldy;
+  float* s;            // [M]
+};
+
+struct GemmI8Args {
+  const int8_t* A;
+  int64_t lda;
+  const float* a_s;    // [M]
+  const int8_t* B;
+  int64_t ldb;
+  const float* b_s;    // [N]
+  uint16_t* C;
+  int64_t ldc;
+  int64_t M, N, K;
+};
+
+// A routed-expert layer for a few tokens.
+constexpr int kMoeFewTokens = 64;
+struct MoeFewArgs {
+  const uint16_t* x;        // bf16 [T, D]
+  int64_t ldx;
+  const uint8_t* w13;       // [E, 2F, D]
+  int64_t ldw13;
+  const float* s13;
+  int64_t lds13;
+  const uint8_t* w2;        // [E, D, F]
+  int64_t ldw2;
+  const float* s2;
+  int64_t lds2;
+  bool i8;                  // int8 with row scales, else e4m3 with block scales
+  const int32_t* indices;   // [T, k]
+  int64_t ldi;
+  const uint16_t* weights;  // bf16 [T, k]
+  int64_t ldwt;
+  int T, k;
+  int64_t E, D, F;
+  uint16_t* out;            // bf16 [T, D]
+  int64_t ldo;
+  void* work;
+};
+
+hipError_t launch_row_quant_i8(const RowQuantArgs& a, hipStream_t stream);
+hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream);
+hipError_t launch_moe_few(const MoeFewArgs& a, hipStream_t stream);
+size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F);
+
 hipError_t launch_act_quant(const ActQuantArgs& a, hipStream_t stream);
 // Gated products: false if the operands do not fit the direct-to-LDS pipeline
 // the gated epilogue is built on (nothing launched).

@@ -18,6 +18,7 @@
  * Number formats
  *   e4m3  OCP FP8 E4M3 "fn" (bias 7, max +-448, no infinity, NaN = S.1111.111),
  *         i.e. torch.float8_e4m3fn ([DS] item 10).  Stored as one byte.
+ *   int8  two's complement, one byte; quantised values lie in [-127, 127].
  *   bf16  bfloat16, stored as two bytes.
  *   Scales are IEEE fp32.
  *
@@ -61,7 +62,7 @@
 extern "C" {
 #endif
 
-#define DSFP8_ABI_VERSION 6
+#define DSFP8_ABI_VERSION 7
 #define DSFP8_BLOCK 128
 
 typedef int dsfp8_status;
@@ -86,8 +87,12 @@ enum {
  * stored as fp32. */
 enum { DSFP8_SCALE_FP32 = 0, DSFP8_SCALE_UE8M0 = 1 };
 
-/* Element types accepted by dsfp8_weight_quant. */
+/* Element types accepted by dsfp8_weight_quant and dsfp8_row_quant_i8. */
 enum { DSFP8_DTYPE_F32 = 0, DSFP8_DTYPE_BF16 = 1 };
+
+/* Stored weight formats accepted by dsfp8_moe_few: e4m3 with one scale per
+ * 128x128 block, or int8 with one scale per row (output channel). */
+enum { DSFP8_WEIGHT_E4M3 = 0, DSFP8_WEIGHT_I8 = 1 };
 
 /* Library ABI version (DSFP8_ABI_VERSION of the build). */
 int dsfp8_abi_version(void);
@@ -430,6 +435,129 @@ dsfp8_status dsfp8_moe_combine(const void* yr, int64_t R, int64_t ldy,
                                const int32_t* indices, int64_t ldi, const void* weights, int64_t ldw,
                                const int32_t* token_rows, int64_t T, int64_t k, int64_t D,
                                void* out, int64_t ldo, hipStream_t stream);
+
+/*
+ * Row quantisation to int8, one scale per row: a row is a token of an
+ * activation matrix or an output channel of a weight.
+ *   a      = max(max_k |x[m, k]|, 2^-100)
+ *   s[m]   = a / 127                       (fp32 division)
+ *   y[m,k] = rne(x[m,k] * (127 / a))       (fp32 division and product, each
+ *                                           rounded once; rne to an integer)
+ * so x[m,k] ~= y[m,k] * s[m], |y| <= 127, and a row of zeros gives zeros.
+ * A NaN or infinity anywhere in a row makes s[m] NaN or infinite (the row's
+ * codes are then unspecified), so that products of that row show it and no
+ * other row changes.
+ *
+ *   x      fp32 or bf16 (dtype) [M, K], row stride ldx  (device, read)
+ *   y      int8 [M, K], row stride ldy                  (device, written)
+ *   s      fp32 [M]                                     (device, written)
+ * With K = 0 every s[m] is that of a row of zeros.
+ * Errors: DTYPE, NULL, SHAPE, LD, ALIGN, LAUNCH.
+ */
+dsfp8_status dsfp8_row_quant_i8(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx,
+                                void* y, int64_t ldy, float* s, hipStream_t stream);
+
+/*
+ * The same of x[m,i] = SiLU(g[m,i]) * u[m,i], SiLU(v) = v / (1 + e^-v),
+ * evaluated in fp32 and not rounded in between (the hardware's exponential
+ * and reciprocal, each within a few fp32 ulp).
+ *   g, u   bf16 [M, I], row strides ldg, ldu (device, read; may be the halves
+ *          of one [M, 2I] product)
+ * Errors: as dsfp8_row_quant_i8.
+ */
+dsfp8_status dsfp8_silu_mul_row_quant_i8(const void* g, int64_t ldg, const void* u, int64_t ldu,
+                                         int64_t M, int64_t I, void* y, int64_t ldy, float* s,
+                                         hipStream_t stream);
+
+/*
+ * Product of int8 matrices with a scale for each row of A (token) and each
+ * row of B (output channel):
+ *   C[m, n] = bf16( fp32(sum_k A[m,k] B[n,k]) * (a_s[m] * b_s[n]) )
+ * The sum is exact (32-bit integers), so the result does not depend on the
+ * order of accumulation.
+ *
+ *   A      int8 [M, K], row stride lda                  (device, read)
+ *   a_s    fp32 [M]                                     (device, read)
+ *   B      int8 [N, K], row stride ldb (the weight)     (device, read)
+ *   b_s    fp32 [N]                                     (device, read)
+ *   C      bf16 [M, N], row stride ldc                  (device, written)
+ * K <= 131071, the largest for which no sum of int8 products (-128 included)
+ * leaves 32 bits.  K = 0 writes zeros.
+ * Errors: NULL, SHAPE, LD, ALIGN, LAUNCH.
+ */
+dsfp8_status dsfp8_gemm_i8(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb,
+                           const float* b_s, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                           hipStream_t stream);
+
+/*
+ * int8 linear layer on bf16 rows, linear() of [AG] 6.3 with int8 operands:
+ * dsfp8_gemm_i8 of dsfp8_row_quant_i8(x) with the weight (B, b_s); and the
+ * gated form on x = SiLU(g) * u, dsfp8_gemm_i8 of
+ * dsfp8_silu_mul_row_quant_i8(g, u): the down-projection w2(SiLU(w1 x) * w3 x)
+ * of [AG] 1.2.
+ *
+ *   x (g, u)  bf16 [M, K], row stride ldx (ldg, ldu)    (device, read)
+ *   B, b_s, C  as for dsfp8_gemm_i8
+ *   workspace  at least dsfp8_linear_i8_workspace_bytes(M, K) bytes, 16-byte
+ *            aligned (scratch: the codes and scales of x; needs no
+ *            initialisation)                            (device, scratch)
+ * Errors: NULL, SHAPE, LD, ALIGN, WORKSPACE, LAUNCH.
+ */
+dsfp8_status dsfp8_linear_i8(const void* x, int64_t ldx, const void* B, int64_t ldb, const float* b_s,
+                             void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+dsfp8_status dsfp8_silu_mul_linear_i8(const void* g, int64_t ldg, const void* u, int64_t ldu,
+                                      const void* B, int64_t ldb, const float* b_s,
+                                      void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t K);
+
+/*
+ * A whole routed-expert layer for a few tokens ([AG] 6.4 / 8.4 with the
+ * expert of 1.2): for every token t and slot j whose expert e = indices[t, j]
+ * lies in [0, E),
+ *   g = W1[e] x[t],  u = W3[e] x[t],  h = SiLU(g) * u
+ *   out[t] = bf16( sum over j of weights[t, j] * (W2[e] h) )
+ * in two kernels, from the gate's choice to the combined output.  Only the
+ * weights of experts that some token chose are read.  Weights are the stored
+ * values times their scales, activations are not quantised (they are not what
+ * such a layer waits for): every sum is fp32, h is carried with 16
+ * significant bits, and the output is rounded once.  The result of a token
+ * depends on that token alone, repeated calls give the same bytes, and a
+ * token none of whose experts lie in [0, E) (an expert-parallel rank's
+ * indices are relative to its first expert) gets zeros.  A token may name an
+ * expert more than once; its weights add up.
+ *
+ *   x        bf16 [T, D], row stride ldx                    (device, read)
+ *   W13      [E, 2F, D]: w1 in rows 0..F-1 of each expert, w3 in rows
+ *            F..2F-1; row stride ldw13, expert stride 2F*ldw13 (device, read)
+ *   W2       [E, D, F]: row stride ldw2, expert stride D*ldw2  (device, read)
+ *   s13, s2  scales, fp32                                   (device, read):
+ *            weight_fmt E4M3: [E, KB(2F), KB(D)] and [E, KB(D), KB(F)] (the
+ *            128x128 blocks of each expert's stacked [2F, D] and [D, F]),
+ *            row strides lds13, lds2, expert strides KB(2F)*lds13, KB(D)*lds2;
+ *            weight_fmt I8: [E, 2F] and [E, D], expert strides lds13, lds2
+ *   indices  int32 [T, k], row stride ldi                   (device, read)
+ *   weights  bf16 [T, k], row stride ldwt                   (device, read)
+ *   out      bf16 [T, D], row stride ldo                    (device, written)
+ *   workspace  at least dsfp8_moe_few_workspace_bytes(T, k, F) bytes, 16-byte
+ *            aligned; needs no initialisation               (device, scratch)
+ * Limits: T <= DSFP8_MOE_FEW_MAX_TOKENS (more tokens: dsfp8_moe_route and the
+ * grouped products), 1 <= k <= 16, 1 <= E <= 65536.  F = 0 writes zeros.
+ * Errors: DTYPE (unknown weight_fmt), NULL, SHAPE, LD, ALIGN, WORKSPACE, LAUNCH.
+ */
+#define DSFP8_MOE_FEW_MAX_TOKENS 64
+dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx,
+                           const void* W13, int64_t ldw13, const float* s13, int64_t lds13,
+                           const void* W2, int64_t ldw2, const float* s2, int64_t lds2, int weight_fmt,
+                           const int32_t* indices, int64_t ldi, const void* weights, int64_t ldwt,
+                           int64_t T, int64_t k, int64_t E, int64_t D, int64_t F,
+                           void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+size_t dsfp8_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F);
 
 #ifdef __cplusplus
 }
