@@ -12,6 +12,7 @@
 // so nothing depends on their order.
 #include "device.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace dsfp8 {
 namespace {
@@ -75,6 +76,207 @@ __device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t k, int64_t K,
 }
 
 __device__ __forceinline__ int chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// ---- 16-byte aligned operands: tiles fed by direct-to-LDS loads ----------------------
+//
+// BM x BN tiles, each wave WM x WN of it, as in the block-scaled products: a
+// ring of STAGES K-blocks of 128 bytes per row, filled by buffer_load ... lds
+// (rows past the matrix and chunks past K read as zero through the
+// descriptor), one barrier per K-block, the loads of a later K-block issued
+// between the MFMAs of the current one.  Nothing is rescaled inside the K
+// loop, so the accumulators stay where the matrix instruction leaves them.
+// The weight fragment is the instruction's first operand, so a lane's results
+// are runs of four columns of one row.
+
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
+struct I8Cfg {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
+  static constexpr int NW = WAVES_M * WAVES_N;
+  static constexpr int kThreads = 64 * NW;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+  static constexpr int TM = WM / 32, TN = WN / 32;
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LOADS = A_INSTR + B_INSTR;
+  static constexpr int CS = WN + 8;  // staged C row, in bf16 elements
+  static constexpr int C_BYTES = NW * WM * CS * 2;
+  static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > C_BYTES ? STAGES * STAGE_BYTES : C_BYTES;
+  static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole 1 KB segments per wave");
+  static_assert(WM % 32 == 0 && WN % 32 == 0, "32x32 subtiles");
+  static_assert(LOADS * (STAGES - 2) < 64 && LOADS <= 10, "vmcnt range, packed chunk indices");
+};
+
+template <class CF>
+struct I8Loader {
+  i32x4 rsA, rsB;
+  uint32_t off[CF::LOADS];
+  uint32_t kc;  // logical chunk (0..7) of load n at bits 3n
+  uint32_t lds0;
+  uint32_t K;
+  int wave;
+
+  __device__ __forceinline__ void init(const GemmI8Args& p, int64_t m0, int64_t n0, uint8_t* smem) {
+    const int lane = lane_id();
+    wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    K = (uint32_t)p.K;
+    const int64_t ra = p.M - m0 < CF::BM ? p.M - m0 : CF::BM, rb = p.N - n0 < CF::BN ? p.N - n0 : CF::BN;
+    rsA = make_rsrc(p.A + m0 * p.lda, (uint32_t)((ra - 1) * p.lda + p.K));
+    rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
+    kc = 0;
+#pragma unroll
+    for (int n = 0; n < CF::LOADS; ++n) {
+      const bool a = n < CF::A_INSTR;
+      const int r = (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ swz_key(r);
+      off[n] = r < (a ? ra : rb) ? (uint32_t)(r * (a ? p.lda : p.ldb) + c * 16) : kOob;
+      kc |= (uint32_t)c << (3 * n);
+    }
+    lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem));
+  }
+
+  template <bool KFULL>
+  __device__ __forceinline__ void issue(int n, int kb, int stage) const {
+    const bool a = n < CF::A_INSTR;
+    const uint32_t kbyte = (uint32_t)kb * BK;
+    const bool in = KFULL || kbyte + ((kc >> (3 * n)) & 7u) * 16u < K;
+    const uint32_t at = lds0 + (uint32_t)(stage * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) +
+                                          (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 1024);
+    dma_b128(a ? rsA : rsB, at, in ? off[n] : kOob, kbyte);
+  }
+};
+
+// The K loop of one tile; K-blocks 0 .. STAGES - 2 are already on their way.
+template <class CF, bool KFULL>
+__device__ __forceinline__ void i8_k_loop(const I8Loader<CF>& ld, int nkb, const uint8_t* smem,
+                                          v16i (&acc)[CF::TM][CF::TN]) {
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
+  // Operand row r of a 32-row slice: lane r and lane r + 32 hold the two
+  // 16-byte halves of each 32 bytes of K.
+  const int fr = lane & 31, fg = lane >> 5;
+  uint32_t lf[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) lf[h] = (uint32_t)(fr * BK + (((2 * h + fg) ^ swz_key(fr)) << 4));
+#pragma unroll
+  for (int i = 0; i < CF::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < CF::TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  constexpr int STEPS = 4 * CF::TM;
+  constexpr int PER = (CF::LOADS + STEPS - 1) / STEPS;
+  for (int kb = 0; kb < nkb; ++kb) {
+    if (CF::STAGES > 2 && kb + 1 < nkb) wait_vmcnt<CF::LOADS * (CF::STAGES - 2)>();
+    else wait_vmcnt<0>();
+    __syncthreads();
+    const int kn = kb + CF::STAGES - 1, slot = kn % CF::STAGES;
+    const uint8_t* at = smem + (kb % CF::STAGES) * CF::STAGE_BYTES + wm * CF::WM * BK;
+    const uint8_t* bt = smem + (kb % CF::STAGES) * CF::STAGE_BYTES + CF::A_BYTES + wn * CF::WN * BK;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      v4i fb[CF::TN];
+#pragma unroll
+      for (int j = 0; j < CF::TN; ++j) fb[j] = *reinterpret_cast<const v4i*>(bt + j * 32 * BK + lf[h]);
+#pragma unroll
+      for (int i = 0; i < CF::TM; ++i) {
+        const v4i fa = *reinterpret_cast<const v4i*>(at + i * 32 * BK + lf[h]);
+#pragma unroll
+        for (int j = 0; j < CF::TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa, acc[i][j], 0, 0, 0);
+        if (kn < nkb) {
+#pragma unroll
+          for (int n = (h * CF::TM + i) * PER; n < (h * CF::TM + i + 1) * PER && n < CF::LOADS; ++n)
+            ld.template issue<KFULL>(n, kn, slot);
+        }
+      }
+    }
+  }
+}
+
+// Scale, round to bf16, stage in LDS (every wave is done with the ring) and
+// store rows with 16-byte writes where the output allows.
+template <class CF>
+__device__ __forceinline__ void i8_store(const GemmI8Args& p, int64_t m0, int64_t n0,
+                                         const v16i (&acc)[CF::TM][CF::TN], uint8_t* smem) {
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
+  const int fr = lane & 31, fg = lane >> 5;
+  const int64_t row0 = m0 + wm * CF::WM, col0 = n0 + wn * CF::WN;
+  uint16_t* st = reinterpret_cast<uint16_t*>(smem) + wave * CF::WM * CF::CS;
+  // lane (fr, fg), value 4q + v of subtile (i, j): row 32i + fr, column 32j + 8q + 4fg + v
+  float as[CF::TM];
+#pragma unroll
+  for (int i = 0; i < CF::TM; ++i) {
+    const int64_t r = row0 + 32 * i + fr;
+    as[i] = p.a_s[r < p.M ? r : p.M - 1];
+  }
+#pragma unroll
+  for (int j = 0; j < CF::TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float bs[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t c = col0 + 32 * j + 8 * q + 4 * fg + v;
+        bs[v] = p.b_s[c < p.N ? c : p.N - 1];
+      }
+#pragma unroll
+      for (int i = 0; i < CF::TM; ++i) {
+        float y[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] = (float)acc[i][j][4 * q + v] * (as[i] * bs[v]);
+        *reinterpret_cast<uint2*>(st + (32 * i + fr) * CF::CS + 32 * j + 8 * q + 4 * fg) =
+            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      }
+    }
+  __builtin_amdgcn_wave_barrier();
+  const bool vec = (reinterpret_cast<uintptr_t>(p.C) & 15) == 0 && p.ldc % 8 == 0;
+  constexpr int CPR = CF::WN / 8, IT = CF::WM * CPR / 64;
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int c = lane + 64 * it;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(st + (c / CPR) * CF::CS + (c % CPR) * 8);
+    const int64_t row = row0 + c / CPR, col = col0 + (c % CPR) * 8;
+    if (row >= p.M || col >= p.N) continue;
+    uint16_t* dst = p.C + row * p.ldc + col;
+    if (vec && col + 8 <= p.N) {
+      *reinterpret_cast<u32x4*>(dst) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int e = 0; e < 8 && col + e < p.N; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+template <class CF, bool KFULL>
+__global__ __launch_bounds__(CF::kThreads) void gemm_i8_kernel(GemmI8Args p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS_BYTES];
+  const int64_t tiles_m = (p.M + CF::BM - 1) / CF::BM, tiles_n = (p.N + CF::BN - 1) / CF::BN;
+  const int nkb = (int)((p.K + BK - 1) / BK);
+  for (int64_t pid = blockIdx.x; pid < tiles_m * tiles_n; pid += gridDim.x) {
+    int64_t tm, tn;
+    tile_of(pid, tiles_m, tiles_n, tm, tn);
+    I8Loader<CF> ld;
+    ld.init(p, tm * CF::BM, tn * CF::BN, smem);
+    for (int s = 0; s < CF::STAGES - 1 && s < nkb; ++s)
+#pragma unroll
+      for (int n = 0; n < CF::LOADS; ++n) ld.template issue<KFULL>(n, s, s);
+    v16i acc[CF::TM][CF::TN];
+    i8_k_loop<CF, KFULL>(ld, nkb, smem, acc);
+    __syncthreads();
+    i8_store<CF>(p, tm * CF::BM, tn * CF::BN, acc, smem);
+    __syncthreads();
+  }
+}
+
+using I8Big = I8Cfg<256, 256, 2, 4, 2>;
+using I8Mid = I8Cfg<128, 128, 2, 2, 2>;
+using I8Small = I8Cfg<64, 64, 2, 2, 2>;
+
+// ---- any alignment ---------------------------------------------------------------------
 
 // 64x64 tiles, 4 waves of 32x32, any alignment: 16-byte chunks through
 // registers into LDS.
@@ -143,8 +345,35 @@ hipError_t launch_row_quant_i8(const RowQuantArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+namespace {
+
+inline bool aligned16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0; }
+
+template <class CF>
+int64_t tiles(const GemmI8Args& a) {
+  return ((a.M + CF::BM - 1) / CF::BM) * ((a.N + CF::BN - 1) / CF::BN);
+}
+
+template <class CF>
+hipError_t launch_tiles(const GemmI8Args& a, hipStream_t stream) {
+  const int64_t t = tiles<CF>(a);
+  const dim3 grid((unsigned)(t < (1 << 20) ? t : (1 << 20)));
+  if (a.K % BK == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, true>), grid, dim3(CF::kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((gemm_i8_kernel<CF, false>), grid, dim3(CF::kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
+  const bool span = a.lda < (1 << 23) && a.ldb < (1 << 23);  // a tile's rows within 31-bit offsets
+  if (a.K > 0 && a.K % 16 == 0 && aligned16(a.A, a.lda) && aligned16(a.B, a.ldb) && span) {
+    const int cus = device_cu_count();
+    if (tiles<I8Big>(a) >= cus) return launch_tiles<I8Big>(a, stream);
+    if (tiles<I8Mid>(a) >= cus) return launch_tiles<I8Mid>(a, stream);
+    return launch_tiles<I8Small>(a, stream);
+  }
   const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
   hipLaunchKernelGGL(gemm_i8_any_kernel, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
