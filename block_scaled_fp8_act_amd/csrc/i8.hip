@@ -18,46 +18,176 @@ namespace dsfp8 {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));  // an access at any address
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr float kAmaxFloor = 0x1p-100f;  // 127 / a and a / 127 stay normal
 
 // ---- row quantisation ----------------------------------------------------------------
 
-// Input element k of row m as fp32.
-struct RowSrc {
-  const RowQuantArgs& a;
-  int64_t m;
-  __device__ __forceinline__ float operator()(int64_t k) const {
-    if (a.f32) return static_cast<const float*>(a.x)[m * a.ldx + k];
-    const float g = bf16_lo(static_cast<const uint16_t*>(a.x)[m * a.ldx + k]);
-    if (a.u == nullptr) return g;
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * bf16_lo(a.u[m * a.ldu + k]);
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+
+enum Src { kBf16, kF32, kGated };
+
+// SiLU(g) * u in fp32.
+__device__ __forceinline__ float gate(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Eight consecutive input elements as loaded, and as fp32 values.
+template <Src SRC>
+struct Chunk {
+  u32x4 r[SRC == kBf16 ? 1 : 2];
+
+  // Elements k .. k + 7 of row m, all of them in the row; zeros if not `on`.
+  __device__ __forceinline__ void load(const RowQuantArgs& a, int64_t m, int64_t k, bool on) {
+#pragma unroll
+    for (auto& w : r) w = u32x4{0u, 0u, 0u, 0u};
+    if (!on) return;
+    if constexpr (SRC == kF32) {
+      const float* src = static_cast<const float*>(a.x) + m * a.ldx + k;
+      r[0] = *reinterpret_cast<const u32x4u*>(src);
+      r[1] = *reinterpret_cast<const u32x4u*>(src + 4);
+    } else {
+      r[0] = *reinterpret_cast<const u32x4u*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + k);
+      if constexpr (SRC == kGated) r[1] = *reinterpret_cast<const u32x4u*>(a.u + m * a.ldu + k);
+    }
+  }
+
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (SRC == kF32) {
+        v[i] = __uint_as_float(r[0][i]);
+        v[4 + i] = __uint_as_float(r[1][i]);
+      } else {
+        v[2 * i] = bf16_lo(r[0][i]);
+        v[2 * i + 1] = bf16_hi(r[0][i]);
+        if constexpr (SRC == kGated) {
+          v[2 * i] = gate(v[2 * i], bf16_lo(r[1][i]));
+          v[2 * i + 1] = gate(v[2 * i + 1], bf16_hi(r[1][i]));
+        }
+      }
+    }
+  }
+
+  // Keep the gate's result in place of its inputs.
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i >> 2][i & 3] = __float_as_uint(v[i]);
   }
 };
 
-__global__ __launch_bounds__(256) void row_quant_kernel(RowQuantArgs a) {
-  __shared__ uint32_t red[256];
-  const RowSrc x{a, (int64_t)blockIdx.x};
-  uint32_t top = __float_as_uint(kAmaxFloor);
-  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
-    const uint32_t b = __float_as_uint(x(k)) & 0x7fffffffu;
+// The largest |v| as a bit pattern (NaN > infinity > finite).
+__device__ __forceinline__ uint32_t max_abs(const float (&v)[8], uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
     top = b > top ? b : top;
   }
-  red[threadIdx.x] = top;
-  __syncthreads();
-  for (int d = 128; d > 0; d >>= 1) {
-    if ((int)threadIdx.x < d && red[threadIdx.x + d] > red[threadIdx.x]) red[threadIdx.x] = red[threadIdx.x + d];
-    __syncthreads();
+  return top;
+}
+
+__device__ __forceinline__ uint32_t max_u32_wave(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
+    v = o > v ? o : v;
   }
-  const float amax = __uint_as_float(red[0]);
-  const float inv = 127.0f / amax;
-  // Adding 1.5 * 2^23 rounds to an integer (nearest even) and leaves it in
-  // the low bits as two's complement.
-  for (int64_t k = threadIdx.x; k < a.K; k += 256)
-    a.y[x.m * a.ldy + k] = (int8_t)__float_as_uint(x(k) * inv + 0x1.8p23f);
-  if (threadIdx.x == 0) a.s[x.m] = amax / 127.0f;
+  return v;
+}
+
+// Eight codes.  Adding 1.5 * 2^23 rounds a product to an integer (nearest
+// even) and leaves it in the low bits as two's complement.
+__device__ __forceinline__ u32x2u codes8(const float (&v)[8], float inv) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(v[i] * inv + 0x1.8p23f);
+  u32x2u r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    r[h] = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u) |
+           __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000c0cu);
+  return r;
+}
+
+// TPR threads per row, NC chunks of 8 elements per thread: the row stays in
+// registers between the maximum and the codes, so it is read once (NC = 0: a
+// longer row is read twice).  A row's last chunk starts at K - 8: where it
+// overlaps the one before, the same codes are written twice.  K >= 8.
+template <Src SRC, int TPR, int NC>
+__global__ __launch_bounds__(256) void row_quant_kernel(RowQuantArgs a) {
+  constexpr int RPB = 256 / TPR;
+  constexpr int N = NC > 0 ? NC : 4;
+  constexpr Src kHeld = SRC == kGated ? kF32 : SRC;  // what a held chunk contains
+  __shared__ uint32_t red[4];
+  const int t = threadIdx.x % TPR;
+  const int nch = (int)((a.K + 7) >> 3);
+  const int passes = NC > 0 ? 1 : (nch + N * TPR - 1) / (N * TPR);
+  auto at = [&](int c) { return c < nch - 1 ? 8 * (int64_t)c : a.K - 8; };
+  for (int64_t m = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; m < a.M; m += (int64_t)gridDim.x * RPB) {
+    Chunk<kHeld> held[N];
+    uint32_t top = __float_as_uint(kAmaxFloor);
+    auto fetch = [&](int p) __attribute__((always_inline)) {
+      Chunk<SRC> in[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = t + TPR * (i + N * p);
+        in[i].load(a, m, at(c), c < nch);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float v[8];
+        in[i].values(v);
+        top = max_abs(v, top);
+        if constexpr (SRC == kGated) held[i].set(v);
+        else held[i] = in[i];
+      }
+    };
+    for (int p = 0; p < passes; ++p) fetch(p);
+    top = max_u32_wave(top);
+    if constexpr (TPR == 256) {
+      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = red[w] > top ? red[w] : top;
+      __syncthreads();
+    }
+    const float amax = __uint_as_float(top);
+    const float inv = 127.0f / amax;
+    for (int p = 0; p < passes; ++p) {
+      if constexpr (NC == 0) fetch(p);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = t + TPR * (i + N * p);
+        float v[8];
+        held[i].values(v);
+        if (c < nch) *reinterpret_cast<u32x2u*>(a.y + m * a.ldy + at(c)) = codes8(v, inv);
+      }
+    }
+    if (t == 0) a.s[m] = amax / 127.0f;
+  }
+}
+
+// Rows of fewer than 8 elements: one thread each.
+__global__ __launch_bounds__(256) void row_quant_short_kernel(RowQuantArgs a) {
+  for (int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x; m < a.M; m += (int64_t)gridDim.x * 256) {
+    float v[8];
+    for (int k = 0; k < 8; ++k) {
+      v[k] = 0.0f;
+      if (k >= a.K) continue;
+      if (a.f32) {
+        v[k] = static_cast<const float*>(a.x)[m * a.ldx + k];
+      } else {
+        v[k] = bf16_lo(static_cast<const uint16_t*>(a.x)[m * a.ldx + k]);
+        if (a.u != nullptr) v[k] = gate(v[k], bf16_lo(a.u[m * a.ldu + k]));
+      }
+    }
+    const float amax = __uint_as_float(max_abs(v, __float_as_uint(kAmaxFloor)));
+    const u32x2u c = codes8(v, 127.0f / amax);
+    for (int k = 0; k < a.K; ++k) a.y[m * a.ldy + k] = (int8_t)(c[k >> 2] >> (8 * (k & 3)));
+    a.s[m] = amax / 127.0f;
+  }
 }
 
 // ---- product ---------------------------------------------------------------------------
@@ -339,10 +469,33 @@ __global__ __launch_bounds__(256) void gemm_i8_any_kernel(GemmI8Args p) {
 
 }  // namespace
 
+namespace {
+
+template <class Kernel>
+hipError_t launch_rows(Kernel kernel, int rows_per_block, const RowQuantArgs& a, hipStream_t stream) {
+  const int64_t blocks = (a.M + rows_per_block - 1) / rows_per_block;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < (1 << 22) ? blocks : (1 << 22))), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <Src SRC>
+hipError_t launch_quant(const RowQuantArgs& a, hipStream_t stream) {
+  if (a.K <= 512) return launch_rows(row_quant_kernel<SRC, 64, 1>, 4, a, stream);
+  if (a.K <= 1024) return launch_rows(row_quant_kernel<SRC, 64, 2>, 4, a, stream);
+  if (a.K <= 2048) return launch_rows(row_quant_kernel<SRC, 256, 1>, 1, a, stream);
+  if (a.K <= 4096) return launch_rows(row_quant_kernel<SRC, 256, 2>, 1, a, stream);
+  if (a.K <= 8192) return launch_rows(row_quant_kernel<SRC, 256, 4>, 1, a, stream);
+  if (a.K <= 20480) return launch_rows(row_quant_kernel<SRC, 256, 10>, 1, a, stream);
+  return launch_rows(row_quant_kernel<SRC, 256, 0>, 1, a, stream);
+}
+
+}  // namespace
+
 hipError_t launch_row_quant_i8(const RowQuantArgs& a, hipStream_t stream) {
   if (a.M == 0) return hipSuccess;
-  hipLaunchKernelGGL(row_quant_kernel, dim3((unsigned)a.M), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  if (a.K < 8) return launch_rows(row_quant_short_kernel, 256, a, stream);
+  if (a.f32) return launch_quant<kF32>(a, stream);
+  return a.u != nullptr ? launch_quant<kGated>(a, stream) : launch_quant<kBf16>(a, stream);
 }
 
 namespace {
