@@ -594,6 +594,7 @@ dsfp8_status linear_i8(const void* x, int64_t ldx, const void* u, int64_t ldu, c
   dsfp8::RowQuantArgs q;
   DSFP8_TRY(row_quant_args(x, false, ldx, u, ldu, M, K, y, ldy, s, q));
   if (M == 0 || N == 0) return DSFP8_OK;
+  if (dsfp8::linear_i8_fused(g, q)) return launched(dsfp8::launch_linear_i8_fused(g, q, stream));
   const dsfp8_status st = launched(dsfp8::launch_row_quant_i8(q, stream));
   return st == DSFP8_OK ? launched(dsfp8::launch_gemm_i8(g, stream)) : st;
 }

@@ -10,6 +10,8 @@
 //
 // Product: C = bf16((sum_k A B) * (a_s * b_s)).  The integer sums are exact,
 // so nothing depends on their order.
+#include <type_traits>
+
 #include "device.h"
 #include "launch.h"
 #include "tile.h"
@@ -406,6 +408,220 @@ using I8Big = I8Cfg<256, 256, 2, 4, 2>;
 using I8Mid = I8Cfg<128, 128, 2, 2, 2>;
 using I8Small = I8Cfg<64, 64, 2, 2, 2>;
 
+// ---- few output tiles: K split over the waves of a workgroup ---------------------------
+//
+// A workgroup owns a 16 FM x 16 FN tile; its W waves take the K-blocks in turn
+// (wave w: w, w + W, ...), each through a ring of D LDS slots of its own that
+// hold one K-block of the tile's rows, so no wave waits for another until the
+// sums are added up at the end, by integer additions in LDS, whose order does
+// not matter.  All of a wave's first D K-blocks are in flight at once.
+//
+// FUSED: the activations come as the quantiser's input and every workgroup
+// quantises all M <= 16 rows of it itself, while its first weights are on
+// their way; the codes stay in LDS (rows of code_ld bytes after the ring).
+// HALF (FN = 1): 8 columns per workgroup, so that a narrow product reaches
+// more CUs.
+
+constexpr int kSplitWaves = 8;
+constexpr int kFusedCodes = 16384;  // most codes (M * K) of a fused launch, which keeps two workgroups per CU
+
+template <int FM, int FN, int D, bool FUSED, bool HALF>
+struct SplitCfg {
+  static constexpr int TM = 16 * FM, TN = HALF ? 8 : 16 * FN;
+  static constexpr int AROWS = FUSED ? 0 : TM;
+  static constexpr int SLOT = (AROWS + TN) * BK;
+  static constexpr int LOADS = SLOT / 1024;  // 8 rows per load
+  static constexpr int RING = kSplitWaves * D * SLOT;
+  static constexpr int SUM = TM * 16 * FN * 4;
+  static constexpr int LDS = RING > SUM ? RING : SUM;
+  static constexpr int CODES = FUSED ? kFusedCodes + 16 * (BK - 16 + 16) : 0;
+};
+
+template <class SRC_TAG, int FM, int FN, int D, bool HALF>
+__global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8Args p, RowQuantArgs x, int code_ld) {
+  constexpr bool FUSED = !std::is_void<SRC_TAG>::value;
+  using CF = SplitCfg<FM, FN, D, FUSED, HALF>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS + CF::CODES];
+  __shared__ uint32_t row_top[16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int fr = lane & 15, fg = lane >> 4;
+  const uint32_t tiles_n = (uint32_t)((p.N + CF::TN - 1) / CF::TN);
+  const int64_t m0 = FUSED ? 0 : (int64_t)(blockIdx.x / tiles_n) * CF::TM;
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * CF::TN;
+  const int nkb = (int)((p.K + BK - 1) / BK);
+  const uint32_t K = (uint32_t)p.K;
+  const int64_t ra = p.M - m0 < CF::TM ? p.M - m0 : CF::TM, rb = p.N - n0 < CF::TN ? p.N - n0 : CF::TN;
+  const i32x4 rsA = make_rsrc(p.A + (FUSED ? 0 : m0 * p.lda), FUSED ? 0u : (uint32_t)((ra - 1) * p.lda + p.K));
+  const i32x4 rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
+  uint32_t off[CF::LOADS], kc = 0;
+#pragma unroll
+  for (int n = 0; n < CF::LOADS; ++n) {
+    const bool a = 8 * n < CF::AROWS;
+    const int r = 8 * n - (a ? 0 : CF::AROWS) + (lane >> 3);
+    const int c = (lane & 7) ^ swz_key(r);
+    off[n] = r < (a ? ra : rb) ? (uint32_t)(r * (a ? p.lda : p.ldb) + c * 16) : kOob;
+    kc |= (uint32_t)c << (3 * (n & 1));  // the chunk depends on the row modulo 16 alone
+  }
+  const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem)) + (uint32_t)(wave * D * CF::SLOT);
+  auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < CF::LOADS; ++n) {
+      const uint32_t kbyte = (uint32_t)kb * BK;
+      const bool in = kbyte + ((kc >> (3 * (n & 1))) & 7u) * 16u < K;
+      dma_b128(8 * n < CF::AROWS ? rsA : rsB, lds0 + (uint32_t)(slot * CF::SLOT + n * 1024), in ? off[n] : kOob, kbyte);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (wave + d * kSplitWaves < nkb) issue(wave + d * kSplitWaves, d);
+
+  uint8_t* codes = smem + CF::LDS;
+  if constexpr (FUSED) {
+    // Units of 64 chunks of one row, dealt to the waves in turn; held in
+    // registers between the row's maximum and its codes.
+    constexpr Src SRC = SRC_TAG::value;
+    constexpr Src kHeld = SRC == kGated ? kF32 : SRC;
+    const int nch = (int)((x.K + 7) >> 3), segs = (nch + 63) >> 6, units = (int)p.M * segs;
+    if (threadIdx.x < 16) row_top[threadIdx.x] = __float_as_uint(kAmaxFloor);
+    __syncthreads();
+    constexpr int HOLD = 4;
+    Chunk<kHeld> held[HOLD];
+    auto place = [&](int u, int& m, int& c) { m = u / segs, c = (u - m * segs) * 64 + lane; };
+    auto at = [&](int c) { return c < nch - 1 ? 8 * c : (int)x.K - 8; };
+    auto fetch = [&](int u0) __attribute__((always_inline)) {
+      Chunk<SRC> in[HOLD];
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        int m, c;
+        place(u0 + i * kSplitWaves, m, c);
+        in[i].load(x, m, at(c), u0 + i * kSplitWaves < units && c < nch);
+      }
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        if constexpr (SRC == kGated) {
+          float v[8];
+          in[i].values(v);
+          held[i].set(v);
+        } else {
+          held[i] = in[i];
+        }
+      }
+    };
+    const bool once = units <= HOLD * kSplitWaves;
+    for (int u0 = wave; u0 < units; u0 += HOLD * kSplitWaves) {
+      fetch(u0);
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        const int u = u0 + i * kSplitWaves;
+        if (u >= units) continue;
+        float v[8];
+        held[i].values(v);
+        const uint32_t top = max_u32_wave(max_abs(v, 0u));
+        if (lane == 0) atomicMax(&row_top[u / segs], top);
+      }
+    }
+    // Zero the codes between the row's end and its last K-block's: their
+    // weights read as zero, but the codes must be defined.
+    const int pad = nkb * BK - (int)x.K;
+    for (int i = threadIdx.x; i < (int)p.M * pad; i += 64 * kSplitWaves)
+      codes[(i / pad) * code_ld + x.K + i % pad] = 0;
+    __syncthreads();
+    for (int u0 = wave; u0 < units; u0 += HOLD * kSplitWaves) {
+      if (!once) fetch(u0);
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        const int u = u0 + i * kSplitWaves;
+        if (u >= units) continue;
+        int m, c;
+        place(u, m, c);
+        float v[8];
+        held[i].values(v);
+        if (c < nch)
+          *reinterpret_cast<u32x2u*>(codes + m * code_ld + at(c)) = codes8(v, 127.0f / __uint_as_float(row_top[m]));
+      }
+    }
+    __syncthreads();
+  }
+
+  v4i acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  const uint8_t* ring = smem + wave * D * CF::SLOT;
+  for (int kb = wave, slot = 0; kb < nkb; kb += kSplitWaves) {
+    // loads of the later K-blocks in flight behind this one's
+    const int left = (nkb - 1 - kb) / kSplitWaves;
+    if (D >= 4 && left >= 3) wait_vmcnt<CF::LOADS * (D >= 4 ? 3 : 0)>();
+    else if (D >= 3 && left >= 2) wait_vmcnt<CF::LOADS * (D >= 3 ? 2 : 0)>();
+    else if (D >= 2 && left >= 1) wait_vmcnt<CF::LOADS * (D >= 2 ? 1 : 0)>();
+    else wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    const uint8_t* at = ring + slot * CF::SLOT;
+    const uint8_t* bt = at + CF::AROWS * BK;
+    v4i fa[FM][2], fb[FN][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        fb[j][h] = *reinterpret_cast<const v4i*>(bt + swz(HALF ? fr & 7 : 16 * j + fr, 4 * h + fg));
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if constexpr (FUSED) {
+          const int r = fr < (int)p.M ? fr : 0;
+          fa[i][h] = *reinterpret_cast<const v4i*>(codes + r * code_ld + kb * BK + 64 * h + 16 * fg);
+        } else {
+          fa[i][h] = *reinterpret_cast<const v4i*>(at + swz(16 * i + fr, 4 * h + fg));
+        }
+      }
+    }
+    // the slot is free once its fragments have arrived
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (kb + D * kSplitWaves < nkb) issue(kb + D * kSplitWaves, slot);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j][h], fa[i][h], acc[i][j], 0, 0, 0);
+    slot = slot + 1 == D ? 0 : slot + 1;
+  }
+  __syncthreads();
+  // sum[subtile][v][lane] over the waves
+  int* sum = reinterpret_cast<int*>(smem);
+  for (int i = threadIdx.x; i < FM * FN * 256; i += 64 * kSplitWaves) sum[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) atomicAdd(&sum[((i * FN + j) * 4 + v) * 64 + lane], acc[i][j][v]);
+  __syncthreads();
+  constexpr int CPR = CF::TN / 4;  // runs of four columns per row
+  const bool vec = (reinterpret_cast<uintptr_t>(p.C) & 7) == 0 && p.ldc % 4 == 0;
+  for (int q = threadIdx.x; q < CF::TM * CPR; q += 64 * kSplitWaves) {
+    const int r = q / CPR, c4 = q % CPR;
+    const int64_t row = m0 + r, col = n0 + 4 * c4;
+    if (row >= p.M || col >= p.N) continue;
+    const int* src = sum + (((r >> 4) * FN + (c4 >> 2)) * 4) * 64 + (c4 & 3) * 16 + (r & 15);
+    const float as = FUSED ? __uint_as_float(row_top[r & 15]) / 127.0f : p.a_s[row];
+    uint32_t w[2];
+    float y[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) y[v] = (float)src[64 * v] * (as * p.b_s[col + v < p.N ? col + v : p.N - 1]);
+    w[0] = pack_bf16x2(y[0], y[1]);
+    w[1] = pack_bf16x2(y[2], y[3]);
+    uint16_t* dst = p.C + row * p.ldc + col;
+    if (vec && col + 4 <= p.N) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    } else {
+      for (int v = 0; v < 4 && col + v < p.N; ++v) dst[v] = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
+    }
+  }
+}
+
 // ---- any alignment ---------------------------------------------------------------------
 
 // 64x64 tiles, 4 waves of 32x32, any alignment: 16-byte chunks through
@@ -518,14 +734,57 @@ hipError_t launch_tiles(const GemmI8Args& a, hipStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// Operands for the direct-to-LDS loads, with a tile's rows within 31-bit offsets.
+bool dma_ok(const GemmI8Args& a) {
+  return a.K > 0 && a.K % 16 == 0 && aligned16(a.B, a.ldb) && a.ldb < (1 << 23) && aligned16(a.A, a.lda) &&
+         a.lda < (1 << 23);
+}
+
+template <class SRC_TAG, int FM, int FN, int D, bool HALF>
+hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, hipStream_t stream) {
+  constexpr bool FUSED = !std::is_void<SRC_TAG>::value;
+  using CF = SplitCfg<FM, FN, D, FUSED, HALF>;
+  auto kernel = gemm_i8_split_kernel<SRC_TAG, FM, FN, D, HALF>;
+  // rows of codes 16 bytes apart modulo the LDS's 128-byte bank row
+  const int code_ld = FUSED ? (int)((a.K + BK - 1) / BK * BK + 16) : 0;
+  const int64_t grid = (a.M + CF::TM - 1) / CF::TM * ((a.N + CF::TN - 1) / CF::TN);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * kSplitWaves), 0, stream, a, x, code_ld);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// The int8 linear layer in one launch: few rows, whose quantisation every
+// workgroup repeats.
+bool linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q) {
+  return g.M <= 16 && g.K >= 8 && g.K % 16 == 0 && aligned16(g.B, g.ldb) && g.ldb < (1 << 23) &&
+         g.M * g.K <= kFusedCodes && !q.f32;
+}
+
+hipError_t launch_linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q, hipStream_t stream) {
+  using Plain = std::integral_constant<Src, kBf16>;
+  using Gated = std::integral_constant<Src, kGated>;
+  const bool half = (g.N + 15) / 16 < device_cu_count();
+  if (q.u != nullptr)
+    return half ? launch_split<Gated, 1, 1, 4, true>(g, q, stream) : launch_split<Gated, 1, 1, 3, false>(g, q, stream);
+  return half ? launch_split<Plain, 1, 1, 4, true>(g, q, stream) : launch_split<Plain, 1, 1, 3, false>(g, q, stream);
+}
+
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
-  const bool span = a.lda < (1 << 23) && a.ldb < (1 << 23);  // a tile's rows within 31-bit offsets
-  if (a.K > 0 && a.K % 16 == 0 && aligned16(a.A, a.lda) && aligned16(a.B, a.ldb) && span) {
+  if (dma_ok(a)) {
     const int cus = device_cu_count();
+    const RowQuantArgs none{};
     if (tiles<I8Big>(a) >= cus) return launch_tiles<I8Big>(a, stream);
     if (tiles<I8Mid>(a) >= cus) return launch_tiles<I8Mid>(a, stream);
-    return launch_tiles<I8Small>(a, stream);
+    if (a.M <= 16)
+      return (a.N + 15) / 16 < cus ? launch_split<void, 1, 1, 4, true>(a, none, stream)
+                                   : launch_split<void, 1, 1, 2, false>(a, none, stream);
+    if (a.M <= 32) return launch_split<void, 2, 1, 2, false>(a, none, stream);
+    if (tiles<I8Small>(a) >= cus) return launch_tiles<I8Small>(a, stream);
+    return launch_split<void, 4, 2, 1, false>(a, none, stream);
   }
   const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
   hipLaunchKernelGGL(gemm_i8_any_kernel, grid, dim3(256), 0, stream, a);
