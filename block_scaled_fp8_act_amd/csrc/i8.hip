@@ -194,22 +194,20 @@ __global__ __launch_bounds__(256) void row_quant_short_kernel(RowQuantArgs a) {
 
 // ---- product ---------------------------------------------------------------------------
 
-// 16 bytes of a row of K bytes from column k; bytes past the row, or of a row
-// outside the matrix, are zero.
-__device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t k, int64_t K, bool ok) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (!ok || k >= K) return v;
-  if (k + 16 <= K) return *reinterpret_cast<const u32x4u*>(row + k);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (k + i < K) w[i >> 2] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
-  return u32x4{w[0], w[1], w[2], w[3]};
+// 16 bytes of a row of K >= 16 bytes from column k, at any address; those past
+// the row are zero.  Nothing outside the row is read: a chunk that the row's
+// end cuts is taken from the last 16 bytes and shifted.
+template <bool TAIL>
+__device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t k, int64_t K) {
+  if (!TAIL || k + 16 <= K) return *reinterpret_cast<const u32x4u*>(row + k);
+  const int64_t past = k + 16 - K;
+  if (past >= 16) return u32x4{0u, 0u, 0u, 0u};
+  const u32x4 v = *reinterpret_cast<const u32x4u*>(row + K - 16);
+  const unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v) >> (8 * (int)past);
+  return __builtin_bit_cast(u32x4, w);
 }
 
-__device__ __forceinline__ int chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
-// ---- 16-byte aligned operands: tiles fed by direct-to-LDS loads ----------------------
+// ---- tiles ---------------------------------------------------------------------------
 //
 // BM x BN tiles, each wave WM x WN of it, as in the block-scaled products: a
 // ring of STAGES K-blocks of 128 bytes per row, filled by buffer_load ... lds
@@ -219,6 +217,10 @@ __device__ __forceinline__ int chunk_at(int r, int c) { return r * 128 + ((c ^ (
 // loop, so the accumulators stay where the matrix instruction leaves them.
 // The weight fragment is the instruction's first operand, so a lane's results
 // are runs of four columns of one row.
+//
+// Operands whose rows are not 16-byte aligned go through registers instead
+// (RegLoader): the next K-block's chunks are loaded before the MFMAs of the
+// current one and written to the other stage after them.
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 
@@ -231,19 +233,19 @@ struct I8Cfg {
   static constexpr int TM = WM / 32, TN = WN / 32;
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LOADS = A_INSTR + B_INSTR;
-  static constexpr int CS = WN + 8;  // staged C row, in bf16 elements
-  static constexpr int C_BYTES = NW * WM * CS * 2;
-  static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > C_BYTES ? STAGES * STAGE_BYTES : C_BYTES;
+  static constexpr int RING = STAGES * STAGE_BYTES;
+  static constexpr int C_BYTES = 32 * WN * 2;  // 32 rows of a wave's output
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole 1 KB segments per wave");
   static_assert(WM % 32 == 0 && WN % 32 == 0, "32x32 subtiles");
-  static_assert(LOADS * (STAGES - 2) < 64 && LOADS <= 10, "vmcnt range, packed chunk indices");
+  static_assert(NW % 2 == 0, "a wave's segments start at rows that agree modulo 16");
+  static_assert(STAGES >= 2 && STAGES <= 4 && LOADS * (STAGES - 2) < 64, "the waits of the K loop");
 };
 
 template <class CF>
 struct I8Loader {
   i32x4 rsA, rsB;
   uint32_t off[CF::LOADS];
-  uint32_t kc;  // logical chunk (0..7) of load n at bits 3n
+  uint32_t kc;  // byte within the K-block of every load's chunk (a wave's rows agree modulo 16)
   uint32_t lds0;
   uint32_t K;
   int wave;
@@ -255,14 +257,12 @@ struct I8Loader {
     const int64_t ra = p.M - m0 < CF::BM ? p.M - m0 : CF::BM, rb = p.N - n0 < CF::BN ? p.N - n0 : CF::BN;
     rsA = make_rsrc(p.A + m0 * p.lda, (uint32_t)((ra - 1) * p.lda + p.K));
     rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
-    kc = 0;
+    kc = (uint32_t)((lane & 7) ^ swz_key(wave * 8 + (lane >> 3))) * 16;
 #pragma unroll
     for (int n = 0; n < CF::LOADS; ++n) {
       const bool a = n < CF::A_INSTR;
       const int r = (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ swz_key(r);
-      off[n] = r < (a ? ra : rb) ? (uint32_t)(r * (a ? p.lda : p.ldb) + c * 16) : kOob;
-      kc |= (uint32_t)c << (3 * n);
+      off[n] = r < (a ? ra : rb) ? (uint32_t)(r * (a ? p.lda : p.ldb)) + kc : kOob;
     }
     lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem));
   }
@@ -271,142 +271,257 @@ struct I8Loader {
   __device__ __forceinline__ void issue(int n, int kb, int stage) const {
     const bool a = n < CF::A_INSTR;
     const uint32_t kbyte = (uint32_t)kb * BK;
-    const bool in = KFULL || kbyte + ((kc >> (3 * n)) & 7u) * 16u < K;
+    const bool in = KFULL || kbyte + kc < K;
     const uint32_t at = lds0 + (uint32_t)(stage * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) +
                                           (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 1024);
     dma_b128(a ? rsA : rsB, at, in ? off[n] : kOob, kbyte);
   }
 };
 
+template <class CF>
+struct I8RegLoader {
+  const int8_t* row[CF::LOADS];
+  u32x4 v[CF::LOADS];
+  uint32_t at[CF::LOADS];
+  uint32_t kc;
+
+  __device__ __forceinline__ void init(const GemmI8Args& p, int64_t m0, int64_t n0, uint8_t*) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    kc = (uint32_t)((lane & 7) ^ swz_key(wave * 8 + (lane >> 3))) * 16;
+#pragma unroll
+    for (int n = 0; n < CF::LOADS; ++n) {
+      const bool a = n < CF::A_INSTR;
+      const int seg = wave + CF::NW * (a ? n : n - CF::A_INSTR);
+      int64_t r = (a ? m0 : n0) + seg * 8 + (lane >> 3);
+      const int64_t last = (a ? p.M : p.N) - 1;
+      r = r < last ? r : last;  // rows past the matrix repeat the last; their results are not stored
+      row[n] = a ? p.A + r * p.lda : p.B + r * p.ldb;
+      at[n] = (uint32_t)((a ? 0 : CF::A_BYTES) + seg * 1024 + lane * 16);
+    }
+  }
+  __device__ __forceinline__ void load(int kb, int64_t K) {
+    const int64_t k = (int64_t)kb * BK + kc;
+    if ((int64_t)(kb + 1) * BK <= K) {
+#pragma unroll
+      for (int n = 0; n < CF::LOADS; ++n) v[n] = load16<false>(row[n], k, K);
+    } else {
+#pragma unroll
+      for (int n = 0; n < CF::LOADS; ++n) v[n] = load16<true>(row[n], k, K);
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* stage) const {
+#pragma unroll
+    for (int n = 0; n < CF::LOADS; ++n) *reinterpret_cast<u32x4*>(stage + at[n]) = v[n];
+  }
+};
+
+// Where a lane's operand fragments lie in a stage: row r of a 32-row slice is
+// held by lanes r and r + 32, the two 16-byte halves of each 32 bytes of K.
+// Computed once per kernel, not once per K-block (+2.8% on 4096x18432x7168).
+template <class CF>
+struct I8Frag {
+  int at, bt;
+  int lf[4];
+
+  __device__ __forceinline__ I8Frag() {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int fr = lane & 31, fg = lane >> 5;
+    at = wave / CF::WAVES_N * CF::WM * BK;
+    bt = CF::A_BYTES + wave % CF::WAVES_N * CF::WN * BK;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) lf[h] = fr * BK + (((2 * h + fg) ^ swz_key(fr)) << 4);
+  }
+};
+
+// The MFMAs of one K-block from its LDS stage; step(s) is called after each of
+// the 4 TM groups of them.
+template <class CF, class Step>
+__device__ __forceinline__ void i8_block(const uint8_t* stage, const I8Frag<CF>& f, v16i (&acc)[CF::TM][CF::TN],
+                                         Step&& step) {
+  const uint8_t* at = stage + f.at;
+  const uint8_t* bt = stage + f.bt;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    v4i fb[CF::TN];
+#pragma unroll
+    for (int j = 0; j < CF::TN; ++j) fb[j] = *reinterpret_cast<const v4i*>(bt + j * 32 * BK + f.lf[h]);
+#pragma unroll
+    for (int i = 0; i < CF::TM; ++i) {
+      const v4i fa = *reinterpret_cast<const v4i*>(at + i * 32 * BK + f.lf[h]);
+#pragma unroll
+      for (int j = 0; j < CF::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa, acc[i][j], 0, 0, 0);
+      step(h * CF::TM + i);
+    }
+  }
+}
+
 // The K loop of one tile; K-blocks 0 .. STAGES - 2 are already on their way.
 template <class CF, bool KFULL>
-__device__ __forceinline__ void i8_k_loop(const I8Loader<CF>& ld, int nkb, const uint8_t* smem,
+__device__ __forceinline__ void i8_k_loop(const I8Loader<CF>& ld, const I8Frag<CF>& f, int nkb, const uint8_t* smem,
                                           v16i (&acc)[CF::TM][CF::TN]) {
+  constexpr int PER = (CF::LOADS + 4 * CF::TM - 1) / (4 * CF::TM);
+  for (int kb = 0; kb < nkb; ++kb) {
+    // Of the stages issued so far, only those behind K-block kb may be missing.
+    const int later = nkb - 1 - kb < CF::STAGES - 2 ? nkb - 1 - kb : CF::STAGES - 2;
+    if (kb == 0) wait_vmcnt<0>();  // and the scales, and the previous tile's stores
+    else if (CF::STAGES >= 4 && later >= 2) wait_vmcnt<CF::LOADS * (CF::STAGES >= 4 ? 2 : 0)>();
+    else if (CF::STAGES >= 3 && later >= 1) wait_vmcnt<CF::LOADS * (CF::STAGES >= 3 ? 1 : 0)>();
+    else wait_vmcnt<0>();
+    __syncthreads();
+    const int kn = kb + CF::STAGES - 1;
+    i8_block<CF>(smem + (kb % CF::STAGES) * CF::STAGE_BYTES, f, acc, [&](int s) __attribute__((always_inline)) {
+      if (kn >= nkb) return;
+#pragma unroll
+      for (int n = s * PER; n < (s + 1) * PER && n < CF::LOADS; ++n)
+        ld.template issue<KFULL>(n, kn, kn % CF::STAGES);
+    });
+  }
+}
+
+// The scales of a lane's outputs: lane (fr, fg), value 4q + v of subtile (i, j)
+// is row 32i + fr, column 32j + 8q + 4fg + v.
+template <class CF>
+struct I8Scales {
+  float as[CF::TM], bs[CF::TN][16];
+
+  __device__ __forceinline__ void load(const GemmI8Args& p, int64_t m0, int64_t n0) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t row = m0 + wave / CF::WAVES_N * CF::WM + (lane & 31);
+    const int64_t col = n0 + wave % CF::WAVES_N * CF::WN + 4 * (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < CF::TM; ++i) as[i] = p.a_s[row + 32 * i < p.M ? row + 32 * i : p.M - 1];
+#pragma unroll
+    for (int j = 0; j < CF::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int64_t c = col + 32 * j + 8 * (q >> 2) + (q & 3);
+        bs[j][q] = p.b_s[c < p.N ? c : p.N - 1];
+      }
+  }
+};
+
+// Scale and round to bf16, and store 32 rows at a time through an LDS area of
+// the wave's own (chunks of 16 bytes XOR-ed with the row), so that rows leave
+// as 16-byte writes where the output allows.
+template <class CF>
+__device__ __forceinline__ void i8_store(const GemmI8Args& p, int64_t m0, int64_t n0, const I8Scales<CF>& sc,
+                                         const v16i (&acc)[CF::TM][CF::TN], uint8_t* area) {
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
-  // Operand row r of a 32-row slice: lane r and lane r + 32 hold the two
-  // 16-byte halves of each 32 bytes of K.
   const int fr = lane & 31, fg = lane >> 5;
-  uint32_t lf[4];
+  const int64_t row0 = m0 + wave / CF::WAVES_N * CF::WM, col0 = n0 + wave % CF::WAVES_N * CF::WN;
+  uint8_t* st = area + wave * CF::C_BYTES;
+  constexpr int CPR = CF::WN / 8, IT = 32 * CPR / 64, MASK = CPR < 8 ? CPR - 1 : 7;
+  const bool vec = (reinterpret_cast<uintptr_t>(p.C) & 15) == 0 && p.ldc % 8 == 0;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) lf[h] = (uint32_t)(fr * BK + (((2 * h + fg) ^ swz_key(fr)) << 4));
+  for (int i = 0; i < CF::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < CF::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float y[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] = (float)acc[i][j][4 * q + v] * (sc.as[i] * sc.bs[j][4 * q + v]);
+        *reinterpret_cast<uint2*>(st + fr * CF::WN * 2 + (((4 * j + q) ^ (fr & MASK)) << 4) + 8 * fg) =
+            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      }
+    __builtin_amdgcn_wave_barrier();
+    u32x4 v[IT];
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int r = (lane + 64 * it) / CPR, c = (lane + 64 * it) % CPR;
+      v[it] = *reinterpret_cast<const u32x4*>(st + r * CF::WN * 2 + ((c ^ (r & MASK)) << 4));
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int64_t row = row0 + 32 * i + (lane + 64 * it) / CPR, col = col0 + (lane + 64 * it) % CPR * 8;
+      if (row >= p.M || col >= p.N) continue;
+      uint16_t* dst = p.C + row * p.ldc + col;
+      if (vec && col + 8 <= p.N) {
+        *reinterpret_cast<u32x4*>(dst) = v[it];
+      } else {
+        const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+        for (int e = 0; e < 8 && col + e < p.N; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  }
+}
+
+template <class CF>
+__device__ __forceinline__ void i8_zero(v16i (&acc)[CF::TM][CF::TN]) {
 #pragma unroll
   for (int i = 0; i < CF::TM; ++i)
 #pragma unroll
     for (int j = 0; j < CF::TN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  constexpr int STEPS = 4 * CF::TM;
-  constexpr int PER = (CF::LOADS + STEPS - 1) / STEPS;
-  for (int kb = 0; kb < nkb; ++kb) {
-    if (CF::STAGES > 2 && kb + 1 < nkb) wait_vmcnt<CF::LOADS * (CF::STAGES - 2)>();
-    else wait_vmcnt<0>();
-    __syncthreads();
-    const int kn = kb + CF::STAGES - 1, slot = kn % CF::STAGES;
-    const uint8_t* at = smem + (kb % CF::STAGES) * CF::STAGE_BYTES + wm * CF::WM * BK;
-    const uint8_t* bt = smem + (kb % CF::STAGES) * CF::STAGE_BYTES + CF::A_BYTES + wn * CF::WN * BK;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      v4i fb[CF::TN];
-#pragma unroll
-      for (int j = 0; j < CF::TN; ++j) fb[j] = *reinterpret_cast<const v4i*>(bt + j * 32 * BK + lf[h]);
-#pragma unroll
-      for (int i = 0; i < CF::TM; ++i) {
-        const v4i fa = *reinterpret_cast<const v4i*>(at + i * 32 * BK + lf[h]);
-#pragma unroll
-        for (int j = 0; j < CF::TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa, acc[i][j], 0, 0, 0);
-        if (kn < nkb) {
-#pragma unroll
-          for (int n = (h * CF::TM + i) * PER; n < (h * CF::TM + i + 1) * PER && n < CF::LOADS; ++n)
-            ld.template issue<KFULL>(n, kn, slot);
-        }
-      }
-    }
-  }
 }
 
-// Scale, round to bf16, stage in LDS (every wave is done with the ring) and
-// store rows with 16-byte writes where the output allows.
-template <class CF>
-__device__ __forceinline__ void i8_store(const GemmI8Args& p, int64_t m0, int64_t n0,
-                                         const v16i (&acc)[CF::TM][CF::TN], uint8_t* smem) {
-  const int lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int wm = wave / CF::WAVES_N, wn = wave % CF::WAVES_N;
-  const int fr = lane & 31, fg = lane >> 5;
-  const int64_t row0 = m0 + wm * CF::WM, col0 = n0 + wn * CF::WN;
-  uint16_t* st = reinterpret_cast<uint16_t*>(smem) + wave * CF::WM * CF::CS;
-  // lane (fr, fg), value 4q + v of subtile (i, j): row 32i + fr, column 32j + 8q + 4fg + v
-  float as[CF::TM];
-#pragma unroll
-  for (int i = 0; i < CF::TM; ++i) {
-    const int64_t r = row0 + 32 * i + fr;
-    as[i] = p.a_s[r < p.M ? r : p.M - 1];
-  }
-#pragma unroll
-  for (int j = 0; j < CF::TN; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float bs[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int64_t c = col0 + 32 * j + 8 * q + 4 * fg + v;
-        bs[v] = p.b_s[c < p.N ? c : p.N - 1];
-      }
-#pragma unroll
-      for (int i = 0; i < CF::TM; ++i) {
-        float y[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) y[v] = (float)acc[i][j][4 * q + v] * (as[i] * bs[v]);
-        *reinterpret_cast<uint2*>(st + (32 * i + fr) * CF::CS + 32 * j + 8 * q + 4 * fg) =
-            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-      }
-    }
-  __builtin_amdgcn_wave_barrier();
-  const bool vec = (reinterpret_cast<uintptr_t>(p.C) & 15) == 0 && p.ldc % 8 == 0;
-  constexpr int CPR = CF::WN / 8, IT = CF::WM * CPR / 64;
-#pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int c = lane + 64 * it;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(st + (c / CPR) * CF::CS + (c % CPR) * 8);
-    const int64_t row = row0 + c / CPR, col = col0 + (c % CPR) * 8;
-    if (row >= p.M || col >= p.N) continue;
-    uint16_t* dst = p.C + row * p.ldc + col;
-    if (vec && col + 8 <= p.N) {
-      *reinterpret_cast<u32x4*>(dst) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      for (int e = 0; e < 8 && col + e < p.N; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
-  }
-}
+enum Feed { kDmaFull, kDma, kRegs };  // direct-to-LDS (K a multiple of 128, or of 16), through registers
 
-template <class CF, bool KFULL>
+// One workgroup per tile, or (with direct-to-LDS loads and room in LDS beside
+// the ring for the output's staging) one per CU that walks its XCD's tiles:
+// the next tile's first K-block is then on its way while the current tile is
+// scaled and stored.  The scales are loaded before the K loop, whose waits
+// cover them, so that the store waits for none of the next tile's loads.
+template <class CF, Feed FEED>
 __global__ __launch_bounds__(CF::kThreads) void gemm_i8_kernel(GemmI8Args p) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS_BYTES];
+  constexpr bool AHEAD = FEED != kRegs && CF::RING + CF::NW * CF::C_BYTES <= 160 * 1024;
+  constexpr int OUT = AHEAD ? CF::RING : 0;
+  constexpr int LDS = OUT + CF::NW * CF::C_BYTES > CF::RING ? OUT + CF::NW * CF::C_BYTES : CF::RING;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
   const int64_t tiles_m = (p.M + CF::BM - 1) / CF::BM, tiles_n = (p.N + CF::BN - 1) / CF::BN;
+  const int64_t total = tiles_m * tiles_n;
   const int nkb = (int)((p.K + BK - 1) / BK);
-  for (int64_t pid = blockIdx.x; pid < tiles_m * tiles_n; pid += gridDim.x) {
-    int64_t tm, tn;
-    tile_of(pid, tiles_m, tiles_n, tm, tn);
-    I8Loader<CF> ld;
+  const I8Frag<CF> f;
+  int64_t tm, tn, pid = blockIdx.x;
+  tile_of(pid, tiles_m, tiles_n, tm, tn);
+  typename std::conditional<FEED == kRegs, I8RegLoader<CF>, I8Loader<CF>>::type ld;
+  auto begin = [&]() __attribute__((always_inline)) {
     ld.init(p, tm * CF::BM, tn * CF::BN, smem);
-    for (int s = 0; s < CF::STAGES - 1 && s < nkb; ++s)
+    if constexpr (FEED != kRegs) {
+      for (int s = 0; s < CF::STAGES - 1 && s < nkb; ++s)
 #pragma unroll
-      for (int n = 0; n < CF::LOADS; ++n) ld.template issue<KFULL>(n, s, s);
+        for (int n = 0; n < CF::LOADS; ++n) ld.template issue<FEED == kDmaFull>(n, s, s);
+    }
+  };
+  begin();
+  for (;;) {
     v16i acc[CF::TM][CF::TN];
-    i8_k_loop<CF, KFULL>(ld, nkb, smem, acc);
+    i8_zero<CF>(acc);
+    I8Scales<CF> sc;
+    if constexpr (FEED == kRegs) {
+      ld.load(0, p.K);
+      ld.store(smem);
+      for (int kb = 0; kb < nkb; ++kb) {
+        __syncthreads();
+        if (kb + 1 < nkb) ld.load(kb + 1, p.K);
+        i8_block<CF>(smem + (kb & 1) * CF::STAGE_BYTES, f, acc, [](int) {});
+        if (kb + 1 < nkb) ld.store(smem + ((kb + 1) & 1) * CF::STAGE_BYTES);
+      }
+      sc.load(p, tm * CF::BM, tn * CF::BN);
+    } else {
+      sc.load(p, tm * CF::BM, tn * CF::BN);
+      i8_k_loop<CF, FEED == kDmaFull>(ld, f, nkb, smem, acc);
+    }
     __syncthreads();
-    i8_store<CF>(p, tm * CF::BM, tn * CF::BN, acc, smem);
-    __syncthreads();
+    const int64_t m0 = tm * CF::BM, n0 = tn * CF::BN;
+    pid += gridDim.x;
+    const bool more = pid < total;
+    if (more) tile_of(pid, tiles_m, tiles_n, tm, tn);
+    if (AHEAD && more) begin();
+    i8_store<CF>(p, m0, n0, sc, acc, smem + OUT);
+    if (!more) break;
+    if constexpr (!AHEAD) {
+      __syncthreads();
+      begin();
+    }
   }
 }
-
-using I8Big = I8Cfg<256, 256, 2, 4, 2>;
-using I8Mid = I8Cfg<128, 128, 2, 2, 2>;
-using I8Small = I8Cfg<64, 64, 2, 2, 2>;
 
 // ---- few output tiles: K split over the waves of a workgroup ---------------------------
 //
@@ -437,9 +552,10 @@ struct SplitCfg {
   static constexpr int CODES = FUSED ? kFusedCodes + 16 * (BK - 16 + 16) : 0;
 };
 
-template <class SRC_TAG, int FM, int FN, int D, bool HALF>
+template <class SRC_TAG, int FM, int FN, int D, bool HALF, bool DMA>
 __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8Args p, RowQuantArgs x, int code_ld) {
   constexpr bool FUSED = !std::is_void<SRC_TAG>::value;
+  static_assert(D <= 3 && (DMA || D == 1), "waits of the ring; one K-block in registers");
   using CF = SplitCfg<FM, FN, D, FUSED, HALF>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS + CF::CODES];
   __shared__ uint32_t row_top[16];
@@ -452,24 +568,46 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
   const int nkb = (int)((p.K + BK - 1) / BK);
   const uint32_t K = (uint32_t)p.K;
   const int64_t ra = p.M - m0 < CF::TM ? p.M - m0 : CF::TM, rb = p.N - n0 < CF::TN ? p.N - n0 : CF::TN;
-  const i32x4 rsA = make_rsrc(p.A + (FUSED ? 0 : m0 * p.lda), FUSED ? 0u : (uint32_t)((ra - 1) * p.lda + p.K));
-  const i32x4 rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
-  uint32_t off[CF::LOADS], kc = 0;
+  // Load n fetches rows 8n .. 8n + 7 of the slot (A's rows, then B's); a
+  // lane's chunk depends on the row modulo 16 alone.
+  const uint32_t kc[2] = {(uint32_t)((lane & 7) ^ swz_key(lane >> 3)) * 16,
+                          (uint32_t)((lane & 7) ^ swz_key(8 + (lane >> 3))) * 16};
+  i32x4 rsA, rsB;
+  uint32_t off[CF::LOADS];
+  const int8_t* row[CF::LOADS];
+  u32x4 reg[CF::LOADS];
+  if constexpr (DMA) {
+    rsA = make_rsrc(p.A + (FUSED ? 0 : m0 * p.lda), FUSED ? 0u : (uint32_t)((ra - 1) * p.lda + p.K));
+    rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
+  }
 #pragma unroll
   for (int n = 0; n < CF::LOADS; ++n) {
     const bool a = 8 * n < CF::AROWS;
     const int r = 8 * n - (a ? 0 : CF::AROWS) + (lane >> 3);
-    const int c = (lane & 7) ^ swz_key(r);
-    off[n] = r < (a ? ra : rb) ? (uint32_t)(r * (a ? p.lda : p.ldb) + c * 16) : kOob;
-    kc |= (uint32_t)c << (3 * (n & 1));  // the chunk depends on the row modulo 16 alone
+    if constexpr (DMA) {
+      off[n] = r < (a ? ra : rb) ? (uint32_t)(r * (a ? p.lda : p.ldb)) + kc[n & 1] : kOob;
+    } else {
+      const int64_t g = r < (a ? ra : rb) ? r : (a ? ra : rb) - 1;
+      row[n] = a ? p.A + (m0 + g) * p.lda : p.B + (n0 + g) * p.ldb;
+    }
   }
   const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem)) + (uint32_t)(wave * D * CF::SLOT);
   auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
-#pragma unroll
-    for (int n = 0; n < CF::LOADS; ++n) {
+    if constexpr (DMA) {
       const uint32_t kbyte = (uint32_t)kb * BK;
-      const bool in = kbyte + ((kc >> (3 * (n & 1))) & 7u) * 16u < K;
-      dma_b128(8 * n < CF::AROWS ? rsA : rsB, lds0 + (uint32_t)(slot * CF::SLOT + n * 1024), in ? off[n] : kOob, kbyte);
+#pragma unroll
+      for (int n = 0; n < CF::LOADS; ++n)
+        dma_b128(8 * n < CF::AROWS ? rsA : rsB, lds0 + (uint32_t)(slot * CF::SLOT + n * 1024),
+                 kbyte + kc[n & 1] < K ? off[n] : kOob, kbyte);
+    } else {
+      const int64_t k = (int64_t)kb * BK;
+      if (k + BK <= p.K) {
+#pragma unroll
+        for (int n = 0; n < CF::LOADS; ++n) reg[n] = load16<false>(row[n], k + kc[n & 1], p.K);
+      } else {
+#pragma unroll
+        for (int n = 0; n < CF::LOADS; ++n) reg[n] = load16<true>(row[n], k + kc[n & 1], p.K);
+      }
     }
   };
 #pragma unroll
@@ -552,12 +690,18 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
   const uint8_t* ring = smem + wave * D * CF::SLOT;
   for (int kb = wave, slot = 0; kb < nkb; kb += kSplitWaves) {
     // loads of the later K-blocks in flight behind this one's
-    const int left = (nkb - 1 - kb) / kSplitWaves;
-    if (D >= 4 && left >= 3) wait_vmcnt<CF::LOADS * (D >= 4 ? 3 : 0)>();
-    else if (D >= 3 && left >= 2) wait_vmcnt<CF::LOADS * (D >= 3 ? 2 : 0)>();
-    else if (D >= 2 && left >= 1) wait_vmcnt<CF::LOADS * (D >= 2 ? 1 : 0)>();
-    else wait_vmcnt<0>();
-    asm volatile("" ::: "memory");
+    if constexpr (DMA) {
+      const int left = (nkb - 1 - kb) / kSplitWaves;
+      if (D >= 3 && left >= 2) wait_vmcnt<CF::LOADS * (D >= 3 ? 2 : 0)>();
+      else if (D >= 2 && left >= 1) wait_vmcnt<CF::LOADS * (D >= 2 ? 1 : 0)>();
+      else wait_vmcnt<0>();
+      asm volatile("" ::: "memory");
+    } else {
+#pragma unroll
+      for (int n = 0; n < CF::LOADS; ++n)
+        *reinterpret_cast<u32x4*>(smem + wave * D * CF::SLOT + n * 1024 + lane * 16) = reg[n];
+      __builtin_amdgcn_wave_barrier();
+    }
     const uint8_t* at = ring + slot * CF::SLOT;
     const uint8_t* bt = at + CF::AROWS * BK;
     v4i fa[FM][2], fb[FN][2];
@@ -622,64 +766,15 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
   }
 }
 
-// ---- any alignment ---------------------------------------------------------------------
+// ---- K < 16 ----------------------------------------------------------------------------
 
-// 64x64 tiles, 4 waves of 32x32, any alignment: 16-byte chunks through
-// registers into LDS.
-__global__ __launch_bounds__(256) void gemm_i8_any_kernel(GemmI8Args p) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2][64 * 128];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int fr = lane & 15, fg = lane >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  v4i acc[2][2];
-  for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  for (int64_t k0 = 0; k0 < p.K; k0 += 128) {
-    u32x4 ra[2], rb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (tid >> 3) + 32 * i, c = tid & 7;
-      const bool oa = m0 + r < p.M, ob = n0 + r < p.N;
-      ra[i] = load16(p.A + (oa ? m0 + r : 0) * p.lda, k0 + 16 * c, p.K, oa);
-      rb[i] = load16(p.B + (ob ? n0 + r : 0) * p.ldb, k0 + 16 * c, p.K, ob);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (tid >> 3) + 32 * i, c = tid & 7;
-      *reinterpret_cast<u32x4*>(smem[0] + chunk_at(r, c)) = ra[i];
-      *reinterpret_cast<u32x4*>(smem[1] + chunk_at(r, c)) = rb[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4i fa[2], fb[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = *reinterpret_cast<const v4i*>(smem[0] + chunk_at(wm + 16 * i + fr, 4 * h + fg));
-        fb[i] = *reinterpret_cast<const v4i*>(smem[1] + chunk_at(wn + 16 * i + fr, 4 * h + fg));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
-  }
-  // lane (fr, fg) holds row 16i + fr, columns 16j + 4fg ..+3
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = m0 + wm + 16 * i + fr;
-    if (row >= p.M) continue;
-    const float as = p.a_s[row];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int64_t col = n0 + wn + 16 * j + 4 * fg + v;
-        if (col < p.N)
-          p.C[row * p.ldc + col] = (uint16_t)pack_bf16x2((float)acc[i][j][v] * (as * p.b_s[col]), 0.0f);
-      }
+// A row is shorter than one load: one output per thread, byte by byte.
+__global__ __launch_bounds__(256) void gemm_i8_short_kernel(GemmI8Args p) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M * p.N; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / p.N, n = i - m * p.N;
+    int sum = 0;
+    for (int k = 0; k < p.K; ++k) sum += (int)p.A[m * p.lda + k] * (int)p.B[n * p.ldb + k];
+    p.C[m * p.ldc + n] = (uint16_t)pack_bf16x2((float)sum * (p.a_s[m] * p.b_s[n]), 0.0f);
   }
 }
 
@@ -716,42 +811,85 @@ hipError_t launch_row_quant_i8(const RowQuantArgs& a, hipStream_t stream) {
 
 namespace {
 
+using Plain = std::integral_constant<Src, kBf16>;
+using Gated = std::integral_constant<Src, kGated>;
+constexpr int64_t kMaxGrid = (int64_t)1 << 22;  // workgroups of a launch whose workgroups loop
+
 inline bool aligned16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0; }
 
-template <class CF>
-int64_t tiles(const GemmI8Args& a) {
-  return ((a.M + CF::BM - 1) / CF::BM) * ((a.N + CF::BN - 1) / CF::BN);
-}
+// A weight (or activation) for the direct-to-LDS loads: 16-byte chunks, and a
+// tile's rows within 31-bit offsets.
+inline bool dma_ok(const void* p, int64_t ld, int64_t K) { return K % 16 == 0 && aligned16(p, ld) && ld < (1 << 23); }
 
 template <class CF>
-hipError_t launch_tiles(const GemmI8Args& a, hipStream_t stream) {
-  const int64_t t = tiles<CF>(a);
-  const dim3 grid((unsigned)(t < (1 << 20) ? t : (1 << 20)));
-  if (a.K % BK == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, true>), grid, dim3(CF::kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((gemm_i8_kernel<CF, false>), grid, dim3(CF::kThreads), 0, stream, a);
+hipError_t launch_tiles(const GemmI8Args& a, bool dma, hipStream_t stream) {
+  const int64_t t = ((a.M + CF::BM - 1) / CF::BM) * ((a.N + CF::BN - 1) / CF::BN);
+  // the large tile: one workgroup per CU, a multiple of the XCDs
+  const int64_t most = CF::BM * CF::BN == 65536 ? (device_cu_count() + kXcds - 1) / kXcds * kXcds : kMaxGrid;
+  const dim3 grid((unsigned)(t < most ? t : most)), blk(CF::kThreads);
+  if (!dma) hipLaunchKernelGGL((gemm_i8_kernel<CF, kRegs>), grid, blk, 0, stream, a);
+  else if (a.K % BK == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDmaFull>), grid, blk, 0, stream, a);
+  else hipLaunchKernelGGL((gemm_i8_kernel<CF, kDma>), grid, blk, 0, stream, a);
   return hipGetLastError();
 }
 
-}  // namespace
-
-namespace {
-
-// Operands for the direct-to-LDS loads, with a tile's rows within 31-bit offsets.
-bool dma_ok(const GemmI8Args& a) {
-  return a.K > 0 && a.K % 16 == 0 && aligned16(a.B, a.ldb) && a.ldb < (1 << 23) && aligned16(a.A, a.lda) &&
-         a.lda < (1 << 23);
+template <class SRC_TAG, int FM, int FN, int D, bool HALF, bool DMA = true>
+hipError_t launch_split_dma(const GemmI8Args& a, const RowQuantArgs& x, int code_ld, hipStream_t stream) {
+  using CF = SplitCfg<FM, FN, D, !std::is_void<SRC_TAG>::value, HALF>;
+  const int64_t t = (a.M + CF::TM - 1) / CF::TM * ((a.N + CF::TN - 1) / CF::TN);
+  hipLaunchKernelGGL((gemm_i8_split_kernel<SRC_TAG, FM, FN, D, HALF, DMA>), dim3((unsigned)t), dim3(64 * kSplitWaves),
+                     0, stream, a, x, code_ld);
+  return hipGetLastError();
 }
 
 template <class SRC_TAG, int FM, int FN, int D, bool HALF>
-hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, hipStream_t stream) {
-  constexpr bool FUSED = !std::is_void<SRC_TAG>::value;
-  using CF = SplitCfg<FM, FN, D, FUSED, HALF>;
-  auto kernel = gemm_i8_split_kernel<SRC_TAG, FM, FN, D, HALF>;
-  // rows of codes 16 bytes apart modulo the LDS's 128-byte bank row
-  const int code_ld = FUSED ? (int)((a.K + BK - 1) / BK * BK + 16) : 0;
-  const int64_t grid = (a.M + CF::TM - 1) / CF::TM * ((a.N + CF::TN - 1) / CF::TN);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * kSplitWaves), 0, stream, a, x, code_ld);
-  return hipGetLastError();
+hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, bool dma, hipStream_t stream) {
+  // fused: rows of codes 16 bytes apart modulo the LDS's 128-byte bank row
+  const int code_ld = std::is_void<SRC_TAG>::value ? 0 : (int)((a.K + BK - 1) / BK * BK + 16);
+  return dma ? launch_split_dma<SRC_TAG, FM, FN, D, HALF, true>(a, x, code_ld, stream)
+             : launch_split_dma<SRC_TAG, FM, FN, 1, HALF, false>(a, x, code_ld, stream);
+}
+
+// The variants and what each costs: a CU runs up to `resident` workgroups at
+// once, so it works through its share of the tiles in rounds; a round costs
+// 1 us, a K-block of a tile per_kb (an eighth of the K-blocks for the split
+// variants, whose eight waves share them), the launch and the store `fixed`;
+// first for direct-to-LDS operands, then for operands through registers.
+// The constants are fitted to 250 products (1 to 4096 rows, ten weights from
+// 512x512 to 18432x7168) and, through registers, 162 with odd sizes, each
+// timed with every variant: the choice takes 2.9% (4.1%) longer than the
+// fastest variant in the geometric mean; the best single variant would take
+// 60% (67%) longer.  resident = 0: not for such operands (the 64x64 split
+// variant spills with its loads in registers).
+struct Cost {
+  int resident;
+  float fixed, per_kb;
+};
+struct Variant {
+  int bm, bn;
+  bool split;
+  Cost dma, regs;
+};
+constexpr Variant kVariants[] = {{16, 8, true, {2, 1.30f, 0.327f}, {2, 1.57f, 0.575f}},
+                                 {16, 16, true, {2, 1.38f, 0.470f}, {2, 1.68f, 0.799f}},
+                                 {32, 32, true, {2, 1.52f, 0.966f}, {1, 2.53f, 1.870f}},
+                                 {64, 32, true, {1, 1.69f, 1.465f}, {1, 3.43f, 2.845f}},
+                                 {64, 64, true, {1, 2.60f, 2.164f}, {0, 0.0f, 0.0f}},
+                                 {64, 64, false, {2, 2.62f, 0.271f}, {2, 4.93f, 0.608f}},
+                                 {128, 128, false, {1, 2.49f, 0.607f}, {1, 5.42f, 1.550f}},
+                                 {128, 256, false, {1, 3.54f, 0.897f}, {1, 7.28f, 2.135f}},
+                                 {256, 256, false, {1, 4.72f, 1.556f}, {1, 19.67f, 2.625f}}};
+
+float variant_us(const Variant& v, const GemmI8Args& a, bool dma, int cus) {
+  const Cost& c = dma ? v.dma : v.regs;
+  const int64_t tiles = (a.M + v.bm - 1) / v.bm * ((a.N + v.bn - 1) / v.bn);
+  // a split launch has one workgroup per tile
+  if (c.resident == 0 || (v.split && tiles > kMaxGrid)) return 1e30f;
+  const int64_t full = tiles / ((int64_t)cus * c.resident), rest = tiles - full * cus * c.resident;
+  const int64_t per_cu = full * c.resident + (rest + cus - 1) / cus;
+  int64_t kbs = (a.K + BK - 1) / BK;
+  if (v.split) kbs = (kbs + kSplitWaves - 1) / kSplitWaves;
+  return c.fixed + (float)(full + (rest > 0)) + c.per_kb * (float)kbs * (float)per_cu;
 }
 
 }  // namespace
@@ -759,36 +897,43 @@ hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, hipStream_t 
 // The int8 linear layer in one launch: few rows, whose quantisation every
 // workgroup repeats.
 bool linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q) {
-  return g.M <= 16 && g.K >= 8 && g.K % 16 == 0 && aligned16(g.B, g.ldb) && g.ldb < (1 << 23) &&
-         g.M * g.K <= kFusedCodes && !q.f32;
+  return g.M <= 16 && g.K >= 16 && g.M * g.K <= kFusedCodes && !q.f32;
 }
 
 hipError_t launch_linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q, hipStream_t stream) {
-  using Plain = std::integral_constant<Src, kBf16>;
-  using Gated = std::integral_constant<Src, kGated>;
-  const bool half = (g.N + 15) / 16 < device_cu_count();
+  const bool half = (g.N + 15) / 16 < device_cu_count(), dma = dma_ok(g.B, g.ldb, g.K);
   if (q.u != nullptr)
-    return half ? launch_split<Gated, 1, 1, 4, true>(g, q, stream) : launch_split<Gated, 1, 1, 3, false>(g, q, stream);
-  return half ? launch_split<Plain, 1, 1, 4, true>(g, q, stream) : launch_split<Plain, 1, 1, 3, false>(g, q, stream);
+    return half ? launch_split<Gated, 1, 1, 3, true>(g, q, dma, stream)
+                : launch_split<Gated, 1, 1, 3, false>(g, q, dma, stream);
+  return half ? launch_split<Plain, 1, 1, 3, true>(g, q, dma, stream)
+              : launch_split<Plain, 1, 1, 3, false>(g, q, dma, stream);
 }
 
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
-  if (dma_ok(a)) {
-    const int cus = device_cu_count();
-    const RowQuantArgs none{};
-    if (tiles<I8Big>(a) >= cus) return launch_tiles<I8Big>(a, stream);
-    if (tiles<I8Mid>(a) >= cus) return launch_tiles<I8Mid>(a, stream);
-    if (a.M <= 16)
-      return (a.N + 15) / 16 < cus ? launch_split<void, 1, 1, 4, true>(a, none, stream)
-                                   : launch_split<void, 1, 1, 2, false>(a, none, stream);
-    if (a.M <= 32) return launch_split<void, 2, 1, 2, false>(a, none, stream);
-    if (tiles<I8Small>(a) >= cus) return launch_tiles<I8Small>(a, stream);
-    return launch_split<void, 4, 2, 1, false>(a, none, stream);
+  if (a.K < 16) {
+    const int64_t blocks = (a.M * a.N + 255) / 256;
+    hipLaunchKernelGGL(gemm_i8_short_kernel, dim3((unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid)), dim3(256), 0,
+                       stream, a);
+    return hipGetLastError();
   }
-  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
-  hipLaunchKernelGGL(gemm_i8_any_kernel, grid, dim3(256), 0, stream, a);
-  return hipGetLastError();
+  const bool dma = dma_ok(a.A, a.lda, a.K) && dma_ok(a.B, a.ldb, a.K);
+  const int cus = device_cu_count();
+  int best = 0;
+  for (int i = 1; i < (int)(sizeof(kVariants) / sizeof(kVariants[0])); ++i)
+    if (variant_us(kVariants[i], a, dma, cus) < variant_us(kVariants[best], a, dma, cus)) best = i;
+  const RowQuantArgs none{};
+  switch (best) {
+    case 0: return launch_split<void, 1, 1, 2, true>(a, none, dma, stream);
+    case 1: return launch_split<void, 1, 1, 2, false>(a, none, dma, stream);
+    case 2: return launch_split<void, 2, 2, 1, false>(a, none, dma, stream);
+    case 3: return launch_split<void, 4, 2, 1, false>(a, none, dma, stream);
+    case 4: return launch_split_dma<void, 4, 4, 1, false>(a, none, 0, stream);
+    case 5: return launch_tiles<I8Cfg<64, 64, 2, 2, 4>>(a, dma, stream);
+    case 6: return launch_tiles<I8Cfg<128, 128, 2, 4, 3>>(a, dma, stream);
+    case 7: return launch_tiles<I8Cfg<128, 256, 2, 4, 3>>(a, dma, stream);
+    default: return launch_tiles<I8Cfg<256, 256, 2, 4, 2>>(a, dma, stream);
+  }
 }
 
 }  // namespace dsfp8
