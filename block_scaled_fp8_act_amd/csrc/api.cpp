@@ -658,7 +658,8 @@ dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx, const void* W13, int64_t 
                            int64_t k, int64_t E, int64_t D, int64_t F, void* out, int64_t ldo, void* workspace,
                            size_t workspace_bytes, hipStream_t stream) {
   static_assert(DSFP8_MOE_FEW_MAX_TOKENS == dsfp8::kMoeFewTokens, "header and library agree");
-  if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16 || E < 1 || E > kMaxExperts) return DSFP8_ERR_SHAPE;
+  if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16) return DSFP8_ERR_SHAPE;
+  if (E < 1 || E > dsfp8::kMaxRouteExperts) return DSFP8_ERR_SHAPE;
   if (!dim_ok(D) || !dim_ok(F) || !dim_ok(2 * F)) return DSFP8_ERR_SHAPE;
   if (weight_fmt != DSFP8_WEIGHT_E4M3 && weight_fmt != DSFP8_WEIGHT_I8) return DSFP8_ERR_DTYPE;
   const bool i8 = weight_fmt == DSFP8_WEIGHT_I8;

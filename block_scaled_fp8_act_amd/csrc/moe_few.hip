@@ -4,31 +4,40 @@
 //   h = SiLU(W1[e] x[t]) * (W3[e] x[t]),   out[t] = sum_j weights[t, j] W2[e] h.
 //
 // With a few tokens every expert that is hit has a few rows, so the layer is
-// bound by the bytes of the experts' weights, 3 D F each, read once.  The
-// products therefore run with the weights as the matrix instruction's first
-// operand, straight from memory to registers (no weight is used twice by a
-// workgroup, so LDS would only add a trip), converted to bf16, which holds
-// every e4m3 and int8 value exactly, and with up to 16 tokens as the columns
-// of its second operand.  Activations stay bf16; h is carried as the sum of two
-// bf16 values (16 significant bits), since the matrix cores are far from
-// busy and a second product per weight costs nothing that shows.
+// bound by the bytes of the hit experts' weights, 3 D F each, read once.  The
+// products run with the weights as the matrix instruction's first operand and
+// the tokens as the columns of its second: column c of column tile i is token
+// 16 i + c, zero where the token has not chosen the expert, and a tile without
+// any such token is skipped.  Weights are widened to bf16, which holds every
+// e4m3 and int8 value exactly; activations stay bf16, and h is carried as the
+// sum of two bf16 values (16 significant bits): the matrix cores have the time
+// for a second product per weight.
 //
-//   up    one workgroup per (leader pair, 32 columns of h).  The leader of an
-//         expert is its first (token, slot) pair; workgroups of other pairs
-//         end at once, so no list of experts has to be made first and no host
-//         synchronisation is needed.  The eight waves split D and join through
-//         LDS in a fixed order.
-//   down  one workgroup per 16 columns of the output; its waves take the
-//         (leader, piece of F) units in turn and add into an accumulator each,
-//         joined at the end in a fixed order.
+// Every wave streams its own share of the weights through an LDS slot of its
+// own: direct-to-LDS loads fetch whole 128-byte lines (8 rows each; loading
+// the operands straight into registers touches 16 lines for 64 bytes each),
+// the fragments of a step are read back, and the next step's loads are issued
+// before the step's products, so a slot is almost always on its way.  Weights
+// whose rows are not 16-byte aligned take the register loads instead.
 //
-// The second kernel reads from the workspace, for each leader pair, the number
-// of its tokens (0 for any other pair) and for each of them its row of h, the
-// token and the sum of the token's weights for the expert.
+//   up    tasks of (expert, 32 columns of h): 32 rows of w1 and of w3 over D.
+//         KS of a workgroup's eight waves share a task and join through LDS in
+//         a fixed order; KS is as large as it takes for the tasks to fill the
+//         machine.
+//   down  one workgroup per 16 RT columns of the output.  The steps (expert,
+//         128 elements of F) of all experts are dealt to the sixteen waves in
+//         equal consecutive ranges; a wave keeps its sums for all tokens in
+//         registers over its whole range, and the waves join once at the end
+//         in a fixed order, so no sum depends on timing.
+//
+// Which experts are hit is found by every workgroup for itself, from the
+// indices, with a table in LDS; so nothing has to be sorted first and the host
+// waits for nothing.
 #include <type_traits>
 
 #include "device.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace dsfp8 {
 namespace {
@@ -39,59 +48,81 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
-constexpr int kUpRows = 32;    // columns of h per workgroup (rows of w1, and as many of w3)
-constexpr int kDownRows = 16;  // output columns per workgroup
+constexpr int kUpWaves = 8, kDownWaves = 16;
+constexpr int kUpRows = 32;           // columns of h per task (rows of w1, and as many of w3)
+constexpr int kUpSlot = 2 * kUpRows * BK;
+constexpr int kMaxPairs = kMoeFewTokens * 16;
 
-struct TokenRef {
-  int32_t row_tok;  // row of h (the pair index) * 64 + token
-  float w;          // the token's weight for this expert
-};
+// Workspace: h as hi bf16 [T * k, Fp], then lo bf16 [T * k, Fp], by the first
+// pair of each (token, expert); Fp = F rounded up to 8.
+__host__ __device__ inline int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 
-// Workspace: counts int32 [P] (padded to 16 bytes), refs TokenRef [P, T],
-// h as hi bf16 [P, Fp] then lo bf16 [P, Fp], Fp = F rounded up to 128.
-struct Work {
-  int32_t* count;
-  TokenRef* ref;
-  uint16_t* hi;
-  uint16_t* lo;
-  int64_t Fp;
-};
-
-__host__ __device__ inline int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
-
-__host__ __device__ inline int64_t ref_offset(int64_t P) { return (P * 4 + 15) / 16 * 16; }
-__host__ __device__ inline int64_t h_offset(int64_t P, int64_t T) {
-  return ref_offset(P) + (P * T * (int64_t)sizeof(TokenRef) + 15) / 16 * 16;
+// The hit experts, in the order of their first (token, slot) pair.  Fills
+// idx[p] = expert of pair p (-1: none here) and list[i] = i-th hit expert; returns how
+// many there are.  table: E ints of scratch.
+template <int THREADS>
+__device__ __forceinline__ int hit_experts(const MoeFewArgs& a, int* table, int* idx, int* list, int* wave_n) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int P = a.T * a.k;
+  for (int e = threadIdx.x; e < a.E; e += THREADS) table[e] = P;
+  for (int p = threadIdx.x; p < P; p += THREADS) {
+    const int t = (int)((uint32_t)p / (uint32_t)a.k);
+    const int e = a.indices[(int64_t)t * a.ldi + (p - t * a.k)];
+    idx[p] = e >= 0 && e < a.E ? e : -1;
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += THREADS)
+    if (idx[p] >= 0) atomicMin(&table[idx[p]], p);
+  __syncthreads();
+  int total = 0;
+  for (int base = 0; base < P; base += THREADS) {
+    const int p = base + threadIdx.x;
+    const bool is = p < P && idx[p] >= 0 && table[idx[p]] == p;
+    const uint64_t m = __ballot(is);
+    if (lane == 0) wave_n[wave] = __popcll(m);
+    __syncthreads();
+    int at = total;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+      at += w < wave ? wave_n[w] : 0;
+      total += wave_n[w];
+    }
+    if (is) list[at + __popcll(m & ((1ull << lane) - 1))] = idx[p];
+    __syncthreads();
+  }
+  return total;
 }
 
-__device__ __forceinline__ Work work_of(const MoeFewArgs& a) {
-  const int64_t P = (int64_t)a.T * a.k;
-  uint8_t* b = static_cast<uint8_t*>(a.work);
-  Work w;
-  w.Fp = pad128(a.F);
-  w.count = reinterpret_cast<int32_t*>(b);
-  w.ref = reinterpret_cast<TokenRef*>(b + ref_offset(P));
-  w.hi = reinterpret_cast<uint16_t*>(b + h_offset(P, a.T));
-  w.lo = w.hi + P * w.Fp;
-  return w;
+// Lane t's view of an expert: the first of token t's slots that names it (-1:
+// none).
+__device__ __forceinline__ int slot_of(const MoeFewArgs& a, const int* idx, int e, int t) {
+  int first = -1;
+  if (t < a.T)
+    for (int j = a.k - 1; j >= 0; --j) first = idx[t * a.k + j] == e ? j : first;
+  return first;
 }
 
-// 16 bytes from element k (of SZ bytes) of a row of K elements; elements past
-// the row are zero.  TAIL = false promises that all of them lie in the row.
+// 16 bytes from element k (of SZ bytes) of a row of K elements, at any address;
+// elements past the row are zero and nothing outside the row is read.  TAIL =
+// false promises that all of them lie in the row; otherwise elements that the
+// row's end cuts are taken from its last 16 bytes and shifted (a row shorter
+// than that is read element by element).
 template <int SZ, bool TAIL>
 __device__ __forceinline__ u32x4 load16(const uint8_t* row, int64_t k, int64_t K) {
   constexpr int n = 16 / SZ;
   if (!TAIL || k + n <= K) return *reinterpret_cast<const u32x4u*>(row + k * SZ);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < n; ++i) {
-    if (k + i >= K) continue;
-    const uint32_t v = SZ == 1 ? (uint32_t)row[k + i] : (uint32_t) reinterpret_cast<const uint16_t*>(row)[k + i];
-    w[i * SZ / 4] |= v << (8 * (i * SZ % 4));
+  if (k >= K) return u32x4{0u, 0u, 0u, 0u};
+  unsigned __int128 w = 0;
+  if (K >= n) {
+    w = __builtin_bit_cast(unsigned __int128, *reinterpret_cast<const u32x4u*>(row + (K - n) * SZ));
+    w >>= 8 * SZ * (int)(k + n - K);
+  } else {
+#pragma unroll 1
+    for (int64_t i = K - 1; i >= k; --i)
+      w = w << (8 * SZ) |
+          (SZ == 1 ? (uint32_t)row[i] : (uint32_t) reinterpret_cast<const uint16_t*>(row)[i]);
   }
-  return u32x4{w[0], w[1], w[2], w[3]};
+  return __builtin_bit_cast(u32x4, w);
 }
 
 // Eight stored weights as bf16 (exact for both formats).
@@ -119,7 +150,7 @@ __device__ __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
 // both operands take the elements in the same order, so the order in which
 // the instruction consumes them does not matter.  Result: row 4g + v, column r.
 template <bool I8>
-__device__ __forceinline__ v4f block_product(const u32x4 (&w)[2], const u32x4 (&b)[4], v4f acc) {
+__device__ __forceinline__ v4f block_product(const u32x4 (&w)[2], const u32x4* b, v4f acc) {
 #pragma unroll
   for (int s = 0; s < 4; ++s)
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<I8>(w[s >> 1][2 * (s & 1)], w[s >> 1][2 * (s & 1) + 1]),
@@ -127,263 +158,420 @@ __device__ __forceinline__ v4f block_product(const u32x4 (&w)[2], const u32x4 (&
   return acc;
 }
 
-template <bool I8, int CT>
-__global__ __launch_bounds__(kThreads) void moe_few_up_kernel(MoeFewArgs a) {
-  __shared__ float red[kWaves][2 * kUpRows][17];
-  __shared__ int tok[kMoeFewTokens], pair[kMoeFewTokens];
-  const Work wk = work_of(a);
+// Up to 32 consecutive rows of a weight, for one task or expert.
+template <bool DMA>
+struct Panel {
+  const uint8_t* base;
+  i32x4 rs;
+  int rows;
+
+  __device__ __forceinline__ void set(const uint8_t* p, int64_t ld, int n, int64_t K) {
+    base = p;
+    rows = n;
+    if constexpr (DMA) rs = make_rsrc(p, (uint32_t)((n - 1) * ld + K));
+  }
+};
+
+// A wave's stream of weight blocks, NB blocks of 16 rows x 128 elements per
+// step, through its LDS slot or (weights that are not 16-byte aligned)
+// straight into the fragment registers.
+template <int NB, bool DMA>
+struct Stream {
+  u32x4 w[NB][2];  // the step's fragments: lane (r, g) elements 32g .. 32g+31 of row r
+  uint32_t lds;
+  const uint8_t* slot;
+  uint32_t voff[2], kc[2];
+
+  __device__ __forceinline__ void init(const uint8_t* s, int64_t ld) {
+    slot = s;
+    lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(s));
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = 8 * h + (lane >> 3);
+      kc[h] = 16 * (uint32_t)((lane & 7) ^ swz_key(r));
+      voff[h] = (uint32_t)(r * ld) + kc[h];
+    }
+  }
+
+  // Block b of the step: rows 16 i .. of the panel, elements k .. k + 127 of K.
+  __device__ __forceinline__ void issue(int b, const Panel<DMA>& p, int i, int64_t ld, uint32_t k, uint32_t K) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (DMA) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = 16 * i + 8 * h + (lane >> 3) < p.rows && k + kc[h] < K;
+        dma_b128(p.rs, lds + (uint32_t)(b * 2048 + h * 1024), in ? voff[h] : kOob, (uint32_t)(16 * i * ld) + k);
+      }
+    } else {
+      const int r = 16 * i + (lane & 15);
+      const uint8_t* row = p.base + (r < p.rows ? r : 0) * ld;
+      const int64_t kk = k + 32 * (lane >> 4);
+      if (k + BK <= K) {
+        w[b][0] = load16<1, false>(row, kk, K);
+        w[b][1] = load16<1, false>(row, kk + 16, K);
+      } else {
+        w[b][0] = load16<1, true>(row, kk, K);
+        w[b][1] = load16<1, true>(row, kk + 16, K);
+      }
+    }
+  }
+
+  // The step's loads have arrived; afterwards the slot is free.
+  __device__ __forceinline__ void take() {
+    if constexpr (DMA) {
+      const int lane = threadIdx.x & 63, fr = lane & 15, fg = lane >> 4;
+      wait_vmcnt<0>();
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[b][h] = *reinterpret_cast<const u32x4*>(slot + b * 2048 + swz(fr, 2 * fg + h));
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+};
+
+// SiLU(g) * u, split into the two bf16 values hi + lo.
+__device__ __forceinline__ void split_gate(float g, float u, uint16_t& hi, uint16_t& lo) {
+  const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+  const float top = bf16_lo(pack_bf16x2(h, 0.0f));
+  // an infinite or NaN h stays so in hi alone
+  hi = (uint16_t)pack_bf16x2(top, 0.0f);
+  lo = (uint16_t)pack_bf16x2(fabsf(top) < __builtin_inff() ? h - top : 0.0f, 0.0f);
+}
+
+template <bool I8, int CT, bool DMA>
+__global__ __launch_bounds__(64 * kUpWaves, CT == 1 && DMA ? 4 : 2) void moe_few_up_kernel(MoeFewArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kUpWaves * kUpSlot];
+  __shared__ int idx[kMaxPairs], list[kMaxPairs];
+  __shared__ int wave_n[kUpWaves];
+  static_assert(kMaxRouteExperts * 4 <= kUpWaves * kUpSlot, "the table of experts lies in the ring");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int p0 = blockIdx.y;
-  const int e = __builtin_amdgcn_readfirstlane(a.indices[(int64_t)(p0 / a.k) * a.ldi + p0 % a.k]);
-  // This expert's tokens: lane t looks through token t's slots.
-  int first = -1;
-  float wsum = 0.0f;
-  if (lane < a.T)
-    for (int j = 0; j < a.k; ++j)
-      if (a.indices[(int64_t)lane * a.ldi + j] == e) {
-        if (first < 0) first = j;
-        wsum += bf16_lo(a.weights[(int64_t)lane * a.ldwt + j]);
-      }
-  const uint64_t mask = __ballot(first >= 0);
-  const int lead = __builtin_ctzll(mask);
-  const bool mine = e >= 0 && e < a.E && lead * a.k + __shfl(first, lead) == p0;
-  const int n = mine ? __popcll(mask) : 0;
-  if (wave == 0) {
-    const int c = __popcll(mask & ((1ull << lane) - 1));
-    if (mine && first >= 0) {
-      tok[c] = lane;
-      pair[c] = lane * a.k + first;
-      if (blockIdx.x == 0) wk.ref[(int64_t)p0 * a.T + c] = TokenRef{pair[c] * 64 + lane, wsum};
-    }
-    if (blockIdx.x == 0 && lane == 0) wk.count[p0] = n;
-  }
-  if (n == 0) return;
-  __syncthreads();
-
   const int fr = lane & 15, fg = lane >> 4;
-  const int64_t f0 = (int64_t)blockIdx.x * kUpRows;
-  const int nct = (n + 15) >> 4;
-  const int nkb = (int)((a.D + 127) >> 7);
-  const uint8_t* we = a.w13 + (int64_t)e * 2 * a.F * a.ldw13;
-  // Row tile i (0, 1: w1; 2, 3: w3); rows past F read row 0 and are not stored.
-  const uint8_t* row[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t f = f0 + 16 * (i & 1) + fr;
-    row[i] = we + (f < a.F ? (i >> 1) * a.F + f : 0) * a.ldw13;
-  }
-  const uint8_t* xr[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c)
-    xr[c] = reinterpret_cast<const uint8_t*>(a.x + (int64_t)(16 * c + fr < n ? tok[16 * c + fr] : 0) * a.ldx);
-  v4f acc[4][CT];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t kbn = (2 * a.F + 127) >> 7;
-  const float* se = I8 ? nullptr : a.s13 + (int64_t)e * kbn * a.lds13;
+  const int hits = hit_experts<64 * kUpWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n);
+  const int nkb = (int)((a.D + BK - 1) / BK);
+  const uint32_t tiles = (uint32_t)((a.F + kUpRows - 1) / kUpRows);
+  const int64_t tasks = (int64_t)hits * tiles, Fp = pad8(a.F);
+  uint16_t* hi = static_cast<uint16_t*>(a.work);
+  uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
+  int ks = 1;
+  while (ks < kUpWaves && tasks * ks < (int64_t)gridDim.x * kUpWaves && 2 * ks <= nkb) ks *= 2;
+  const int sub = wave & (ks - 1), per = kUpWaves / ks;
+  Stream<4, DMA> st;
+  st.init(ring + wave * kUpSlot, a.ldw13);
+  float(*red)[17] = reinterpret_cast<float(*)[17]>(ring + wave * kUpSlot);
+  static_assert(2 * kUpRows * 17 * 4 <= kUpSlot, "a wave's sums fit its slot");
 
-  auto block = [&](int kb, auto tail) __attribute__((always_inline)) {
-    constexpr bool TAIL = decltype(tail)::value;
-    const int64_t k = (int64_t)kb * 128 + 32 * fg;
-    u32x4 w[4][2];
+  for (int64_t base = (int64_t)blockIdx.x * per; base < tasks; base += (int64_t)gridDim.x * per) {
+    __syncthreads();
+    const int64_t task = base + wave / ks;
+    const bool live = task < tasks;
+    const int e = __builtin_amdgcn_readfirstlane(list[live ? (uint32_t)task / tiles : 0]);
+    const int64_t f0 = live ? (int64_t)((uint32_t)task % tiles) * kUpRows : 0;
+    const int first = slot_of(a, idx, e, lane);
+    const uint64_t mask = live ? __ballot(first >= 0) : 0;
+    v4f acc[4][CT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) w[i][h] = load16<1, TAIL>(row[i], k + 16 * h, a.D);
-    // the scale of each of a lane's four result rows: a 128-row block may
-    // begin inside the w3 rows when F is no multiple of 128
-    v4f sc[4];
-    if constexpr (!I8) {
+      for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (live) {
+      const int rows = (int)(a.F - f0 < kUpRows ? a.F - f0 : kUpRows);
+      Panel<DMA> w1, w3;
+      const uint8_t* at1 = a.w13 + ((int64_t)e * 2 * a.F + f0) * a.ldw13;
+      w1.set(at1, a.ldw13, rows, a.D);
+      w3.set(at1 + a.F * a.ldw13, a.ldw13, rows, a.D);
+      auto issue = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.issue(i, i < 2 ? w1 : w3, i & 1, a.ldw13, (uint32_t)kb * BK, (uint32_t)a.D);
+      };
+      // x of column tile c, elements of K-block kb; zero for tokens that have not chosen e
+      auto columns = [&](int c, int kb, u32x4 (&b)[4]) __attribute__((always_inline)) {
+        const bool on = (mask >> (16 * c + fr)) & 1;
+        const uint8_t* row = reinterpret_cast<const uint8_t*>(a.x + (int64_t)(on ? 16 * c + fr : 0) * a.ldx);
+        const int64_t k = (int64_t)kb * BK + 32 * fg;
+        const bool full = (int64_t)(kb + 1) * BK <= a.D;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          b[s] = u32x4{0u, 0u, 0u, 0u};
+          if (!on) continue;
+          b[s] = full ? load16<2, false>(row, k + 8 * s, a.D) : load16<2, true>(row, k + 8 * s, a.D);
+        }
+      };
+      // Block scales: w1's 32 rows lie in one 128-row block; w3's may span two,
+      // when F is no multiple of 32.
+      const int64_t r3 = a.F + f0;
+      const float* se = a.s13 + (I8 ? 0 : (int64_t)e * ((2 * a.F + BK - 1) / BK) * a.lds13);
+      const float* s1p = se + (f0 >> 7) * a.lds13;
+      const float* s3p = se + (r3 >> 7) * a.lds13;
+      const float* s3q = se + ((r3 + rows - 1) >> 7) * a.lds13;
+      const int cut = (int)(BK - (r3 & (BK - 1)));  // first w3 row of the second block
+      u32x4 b[4];
+      int kb = sub;
+      if (kb < nkb) {
+        issue(kb);
+        if constexpr (CT == 1) columns(0, kb, b);
+      }
+      for (; kb < nkb; kb += ks) {
+        float s1 = 1.0f, s3a = 1.0f, s3b = 1.0f;
+        if constexpr (!I8) {
+          s1 = s1p[kb];
+          s3a = s3p[kb];
+          s3b = s3q[kb];
+        }
+        st.take();
+        const bool more = kb + ks < nkb;
+        if (DMA && CT == 1 && more) issue(kb + ks);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          if (CT > 1) {
+            if (((mask >> (16 * c)) & 0xffff) == 0) continue;
+            columns(c, kb, b);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (I8) {
+              acc[i][c] = block_product<I8>(st.w[i], b, acc[i][c]);
+            } else {
+              const v4f part = block_product<I8>(st.w[i], b, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const float s = i < 2 ? s1 : (16 * (i & 1) + 4 * fg + v < cut ? s3a : s3b);
+                acc[i][c][v] = __builtin_fmaf(part[v], s, acc[i][c][v]);
+              }
+            }
+          }
+        }
+        if (more) {
+          if (!DMA || CT > 1) issue(kb + ks);
+          if constexpr (CT == 1) columns(0, kb + ks, b);
+        }
+      }
+    }
+
+    // Join the waves' sums, gate, and write h: 32 x 16 values per task and column tile.
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      if (c > 0) __syncthreads();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
+        for (int v = 0; v < 4; ++v) red[16 * i + 4 * fg + v][fr] = acc[i][c][v];
+      __syncthreads();
+      const float* group = reinterpret_cast<const float*>(ring + (wave - sub) * kUpSlot);
+      for (int q = sub * 64 + lane; q < kUpRows * 16; q += ks * 64) {
+        const int r = q & (kUpRows - 1), t = 16 * c + (q >> 5);
+        const int slot = __shfl(first, t & 63);
+        const int64_t f = f0 + r;
+        if (!((mask >> t) & 1) || f >= Fp) continue;
+        uint16_t vh = 0, vl = 0;
+        if (f < a.F) {
+          float g = 0.0f, u = 0.0f;
+          for (int w = 0; w < ks; ++w) {
+            g += group[w * (kUpSlot / 4) + r * 17 + (q >> 5)];
+            u += group[w * (kUpSlot / 4) + (kUpRows + r) * 17 + (q >> 5)];
+          }
+          if constexpr (I8) {
+            g *= a.s13[(int64_t)e * a.lds13 + f];
+            u *= a.s13[(int64_t)e * a.lds13 + a.F + f];
+          }
+          split_gate(g, u, vh, vl);
+        }
+        const int64_t at = ((int64_t)t * a.k + slot) * Fp + f;
+        hi[at] = vh;
+        lo[at] = vl;
+      }
+    }
+  }
+}
+
+// RT row tiles of 16 output columns per workgroup.
+template <bool I8, int CT, int RT, bool DMA>
+__global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArgs a) {
+  constexpr int SLOT = RT * 16 * BK;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kDownWaves * SLOT];
+  __shared__ int idx[kMaxPairs], list[kMaxPairs];
+  __shared__ int wave_n[kDownWaves];
+  static_assert(kMaxRouteExperts * 4 <= kDownWaves * SLOT, "the table of experts lies in the ring");
+  constexpr int CJ = CT < 2 ? CT : 2;  // column tiles joined at a time
+  static_assert(16 * CJ * 16 * RT * 4 <= SLOT, "a wave's sums fit its slot");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int fr = lane & 15, fg = lane >> 4;
+  // F = 0: the up kernel did not run, and the output is zero
+  const int hits = a.F > 0 ? hit_experts<64 * kDownWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n) : 0;
+  const int64_t d0 = (int64_t)blockIdx.x * (16 * RT), Fp = pad8(a.F);
+  const int rows = (int)(a.D - d0 < 16 * RT ? a.D - d0 : 16 * RT);
+  const uint16_t* hi = static_cast<const uint16_t*>(a.work);
+  const uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
+  const int per = (int)((a.F + BK - 1) / BK);
+  const int64_t steps = (int64_t)hits * per;
+  const int64_t s0 = steps * wave / kDownWaves, s1 = steps * (wave + 1) / kDownWaves;
+  const int64_t kbd = (a.D + BK - 1) / BK;
+
+  Stream<RT, DMA> st;
+  st.init(ring + wave * SLOT, a.ldw2);
+  v4f acc[RT][CT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+  int at = (int)(s0 / per), kp = (int)(s0 - (int64_t)at * per);
+  auto expert = [&](int i) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(list[i]); };
+  Panel<DMA> w2;
+  auto issue = [&](int e, int p) __attribute__((always_inline)) {
+    w2.set(a.w2 + ((int64_t)e * a.D + d0) * a.ldw2, a.ldw2, rows, a.F);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) st.issue(i, w2, i, a.ldw2, (uint32_t)p * BK, (uint32_t)a.F);
+  };
+  // Per expert: lane t's first slot and weight, and the rows' scales (I8).
+  int first = -1;
+  float wsum = 0.0f;
+  uint64_t mask = 0;
+  float rs[RT][4];
+  auto enter = [&](int e) __attribute__((always_inline)) {
+    first = slot_of(a, idx, e, lane);
+    mask = __ballot(first >= 0);
+    wsum = 0.0f;
+    if (first >= 0)
+      for (int j = first; j < a.k; ++j)
+        if (idx[lane * a.k + j] == e) wsum += bf16_lo(a.weights[(int64_t)lane * a.ldwt + j]);
+    if constexpr (I8) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
         for (int v = 0; v < 4; ++v) {
-          int64_t r = f0 + 16 * (i & 1) + 4 * fg + v;
-          r = (i >> 1) * a.F + (r < a.F ? r : a.F - 1);
-          sc[i][v] = se[(r >> 7) * a.lds13 + kb];
+          const int r = 16 * i + 4 * fg + v;
+          rs[i][v] = a.s2[(int64_t)e * a.lds2 + d0 + (r < rows ? r : rows - 1)];
         }
     }
+  };
+  // h of column tile c, elements of step p.
+  auto columns = [&](int c, int p, u32x4 (&bh)[4], u32x4 (&bl)[4]) __attribute__((always_inline)) {
+    const int slot = __shfl(first, 16 * c + fr);
+    const bool on = (mask >> (16 * c + fr)) & 1;
+    const int64_t row = on ? ((int64_t)(16 * c + fr) * a.k + slot) * Fp : 0;
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (c >= nct) continue;
-      u32x4 b[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        b[s] = 16 * c + fr < n ? load16<2, TAIL>(xr[c], k + 8 * s, a.D) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (I8) {
-          acc[i][c] = block_product<I8>(w[i], b, acc[i][c]);
-        } else {
-          const v4f part = block_product<I8>(w[i], b, v4f{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][c][v] = __builtin_fmaf(part[v], sc[i][v], acc[i][c][v]);
-        }
+    for (int s = 0; s < 4; ++s) {
+      const int64_t k = (int64_t)p * BK + 32 * fg + 8 * s;
+      bh[s] = bl[s] = u32x4{0u, 0u, 0u, 0u};
+      if (on && k < a.F) {
+        bh[s] = *reinterpret_cast<const u32x4*>(hi + row + k);
+        bl[s] = *reinterpret_cast<const u32x4*>(lo + row + k);
       }
     }
   };
-  for (int kb = wave; kb < nkb; kb += kWaves) {
-    if ((int64_t)(kb + 1) * 128 <= a.D) block(kb, std::false_type{});
-    else block(kb, std::true_type{});
-  }
 
-  // Join the waves' sums, gate, and write h.
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    if (c >= nct) continue;
+  u32x4 bh[4], bl[4];
+  int e = 0;
+  if (s0 < s1) {
+    e = expert(at);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave][16 * i + 4 * fg + v][fr] = acc[i][c][v];
-    __syncthreads();
-    const int r = threadIdx.x & 31, col = threadIdx.x >> 5;
-    if (16 * c + col >= n) continue;
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      g += red[w][r][col];
-      u += red[w][kUpRows + r][col];
-    }
-    const int64_t f = f0 + r;
-    float h = 0.0f;
-    if (f < a.F) {
-      if constexpr (I8) {
-        const float* sr = a.s13 + (int64_t)e * a.lds13;
-        g *= sr[f];
-        u *= sr[a.F + f];
-      }
-      h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-    }
-    const float hi = bf16_lo(pack_bf16x2(h, 0.0f));
-    // an infinite or NaN h stays so in hi alone
-    const float lo = fabsf(hi) < __builtin_inff() ? h - hi : 0.0f;
-    const int64_t at = (int64_t)pair[16 * c + col] * wk.Fp + f;
-    wk.hi[at] = (uint16_t)pack_bf16x2(hi, 0.0f);
-    wk.lo[at] = (uint16_t)pack_bf16x2(lo, 0.0f);
-  }
-}
-
-template <bool I8, int CT>
-__global__ __launch_bounds__(kThreads) void moe_few_down_kernel(MoeFewArgs a) {
-  __shared__ float sum[kWaves][16 * CT][kDownRows + 4];
-  __shared__ int list[kMoeFewTokens * 16];
-  __shared__ int wave_n[kWaves];
-  const Work wk = work_of(a);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int P = a.F > 0 ? a.T * a.k : 0;  // F = 0: the up kernel did not run, the output is zero
-  for (int i = lane; i < 16 * CT * (kDownRows + 4); i += 64) (&sum[wave][0][0])[i] = 0.0f;
-  // The leaders, in pair order.
-  int total = 0;
-  for (int base = 0; base < P; base += kThreads) {
-    const int p = base + threadIdx.x;
-    const bool is = p < P && wk.count[p] > 0;
-    const uint64_t m = __ballot(is);
-    if (lane == 0) wave_n[wave] = __popcll(m);
-    __syncthreads();
-    int at = total;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) at += wave_n[w];
-      total += wave_n[w];
-    }
-    if (is) list[at + __popcll(m & ((1ull << lane) - 1))] = p;
+    enter(e);
+    issue(e, kp);
+    if constexpr (CT == 1) columns(0, kp, bh, bl);
+  } else {
     __syncthreads();
   }
-
-  const int fr = lane & 15, fg = lane >> 4;
-  const int64_t d0 = (int64_t)blockIdx.x * kDownRows;
-  const int nkb = (int)(wk.Fp >> 7);
-  const int64_t kbd = (a.D + 127) >> 7;
-  // With fewer leaders than waves an expert's F is cut into pieces.
-  const int pieces = total > 0 && total < kWaves ? (kWaves + total - 1) / total : 1;
-  for (int unit = wave; unit < total * pieces; unit += kWaves) {
-    const int p0 = __builtin_amdgcn_readfirstlane(list[unit / pieces]);
-    const int piece = unit % pieces;
-    const int e = __builtin_amdgcn_readfirstlane(a.indices[(int64_t)(p0 / a.k) * a.ldi + p0 % a.k]);
-    const int n = __builtin_amdgcn_readfirstlane(wk.count[p0]);
-    const int64_t d = d0 + fr;
-    const uint8_t* row = a.w2 + ((int64_t)e * a.D + (d < a.D ? d : 0)) * a.ldw2;
-    const float* se = I8 ? nullptr : a.s2 + ((int64_t)e * kbd + (d0 >> 7)) * a.lds2;
-    const int b0 = nkb * piece / pieces, b1 = nkb * (piece + 1) / pieces;
+  for (int64_t s = s0; s < s1; ++s) {
+    const float sc = I8 ? 1.0f : a.s2[((int64_t)e * kbd + (d0 >> 7)) * a.lds2 + kp];
+    const bool more = s + 1 < s1;
+    const bool turn = kp + 1 == per;
+    const int kn = turn ? 0 : kp + 1;
+    const int en = more && turn ? expert(at + 1) : e;
+    st.take();
+    if (DMA && CT == 1 && more) issue(en, kn);
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      if (16 * c >= n) continue;
-      const bool on = 16 * c + fr < n;
-      const TokenRef ref = on ? wk.ref[(int64_t)p0 * a.T + 16 * c + fr] : TokenRef{0, 0.0f};
-      const int64_t hrow = (int64_t)(ref.row_tok >> 6) * wk.Fp;
-      v4f acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int kb = b0; kb < b1; ++kb) {
-        const int64_t k = (int64_t)kb * 128 + 32 * fg;
-        u32x4 w[2], hh[4], hl[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w[h] = load16<1, true>(row, k + 16 * h, a.F);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          hh[s] = on ? *reinterpret_cast<const u32x4*>(wk.hi + hrow + k + 8 * s) : u32x4{0u, 0u, 0u, 0u};
-          hl[s] = on ? *reinterpret_cast<const u32x4*>(wk.lo + hrow + k + 8 * s) : u32x4{0u, 0u, 0u, 0u};
-        }
-        if constexpr (I8) {
-          acc = block_product<I8>(w, hl, block_product<I8>(w, hh, acc));
-        } else {
-          const v4f part = block_product<I8>(w, hl, block_product<I8>(w, hh, v4f{0.0f, 0.0f, 0.0f, 0.0f}));
-          const float s = se[kb];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(part[v], s, acc[v]);
-        }
+      if (CT > 1) {
+        if (((mask >> (16 * c)) & 0xffff) == 0) continue;
+        columns(c, kp, bh, bl);
       }
-      if (!on) continue;
-      // One lane of each row group per token: no two lanes share an address.
-      float* dst = &sum[wave][ref.row_tok & 63][4 * fg];
+      const float w = __shfl(wsum, 16 * c + fr);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float y = acc[v];
-        if constexpr (I8) {
-          const int64_t dv = d0 + 4 * fg + v;
-          y *= a.s2[(int64_t)e * a.lds2 + (dv < a.D ? dv : a.D - 1)];
-        }
-        dst[v] = __builtin_fmaf(y, ref.w, dst[v]);
+      for (int i = 0; i < RT; ++i) {
+        const v4f part = block_product<I8>(st.w[i], bl, block_product<I8>(st.w[i], bh, v4f{0.0f, 0.0f, 0.0f, 0.0f}));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][c][v] = __builtin_fmaf(part[v], I8 ? rs[i][v] * w : sc * w, acc[i][c][v]);
       }
     }
+    if (more) {
+      if (turn) {
+        ++at;
+        e = en;
+        enter(e);
+      }
+      kp = kn;
+      if (!DMA || CT > 1) issue(e, kp);
+      if constexpr (CT == 1) columns(0, kp, bh, bl);
+    }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * kDownRows; i += kThreads) {
-    const int t = i / kDownRows, r = i % kDownRows;
-    float y = 0.0f;
+
+  // sums[wave][token][row], in the waves' slots
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) y += sum[w][t][r];
-    if (d0 + r < a.D) a.out[(int64_t)t * a.ldo + d0 + r] = (uint16_t)pack_bf16x2(y, 0.0f);
+  for (int c0 = 0; c0 < CT; c0 += CJ) {
+    float* mine = reinterpret_cast<float*>(ring + wave * SLOT);
+    if (c0 > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int c = 0; c < CJ; ++c)
+        *reinterpret_cast<v4f*>(mine + (16 * c + fr) * (16 * RT) + 16 * i + 4 * fg) = acc[i][c0 + c];
+    __syncthreads();
+    for (int q = threadIdx.x; q < 16 * CJ * 16 * RT; q += 64 * kDownWaves) {
+      float y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kDownWaves; ++w) y += reinterpret_cast<const float*>(ring + w * SLOT)[q];
+      const int t = 16 * c0 + q / (16 * RT), r = q % (16 * RT);
+      if (t < a.T && r < rows) a.out[(int64_t)t * a.ldo + d0 + r] = (uint16_t)pack_bf16x2(y, 0.0f);
+    }
   }
 }
 
-template <bool I8, int CT>
+template <bool I8, int CT, bool DMA>
 hipError_t launch(const MoeFewArgs& a, hipStream_t stream) {
+  const int cus = device_cu_count();
   if (a.F > 0) {
-    const dim3 up((unsigned)(pad128(a.F) / kUpRows), (unsigned)(a.T * a.k));
-    hipLaunchKernelGGL((moe_few_up_kernel<I8, CT>), up, dim3(kThreads), 0, stream, a);
+    // at most two workgroups per CU, which is what fits
+    const int64_t tasks = (int64_t)a.T * a.k * ((a.F + kUpRows - 1) / kUpRows);
+    const int64_t grid = tasks < 2 * cus ? tasks : 2 * cus;
+    hipLaunchKernelGGL((moe_few_up_kernel<I8, CT, DMA>), dim3((unsigned)grid), dim3(64 * kUpWaves), 0, stream, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
-  const dim3 down((unsigned)((a.D + kDownRows - 1) / kDownRows));
-  hipLaunchKernelGGL((moe_few_down_kernel<I8, CT>), down, dim3(kThreads), 0, stream, a);
+  const dim3 blk(64 * kDownWaves);
+  if ((a.D + 31) / 32 >= cus / 2)
+    hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 2, DMA>), dim3((unsigned)((a.D + 31) / 32)), blk, 0, stream, a);
+  else
+    hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 1, DMA>), dim3((unsigned)((a.D + 15) / 16)), blk, 0, stream, a);
   return hipGetLastError();
+}
+
+// 16-byte aligned weight rows, 16 of them within 31-bit offsets.
+inline bool dma_ok(const void* p, int64_t ld, int64_t K) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0 && K % 16 == 0 && ld < ((int64_t)1 << 26);
+}
+
+template <bool I8, int CT>
+hipError_t launch_feed(const MoeFewArgs& a, hipStream_t stream) {
+  return dma_ok(a.w13, a.ldw13, a.D) && dma_ok(a.w2, a.ldw2, a.F) ? launch<I8, CT, true>(a, stream)
+                                                                  : launch<I8, CT, false>(a, stream);
 }
 
 template <bool I8>
 hipError_t launch_ct(const MoeFewArgs& a, hipStream_t stream) {
-  if (a.T <= 16) return launch<I8, 1>(a, stream);
-  if (a.T <= 32) return launch<I8, 2>(a, stream);
-  return launch<I8, 4>(a, stream);
+  if (a.T <= 16) return launch_feed<I8, 1>(a, stream);
+  if (a.T <= 32) return launch_feed<I8, 2>(a, stream);
+  return launch_feed<I8, 4>(a, stream);
 }
 
 }  // namespace
 
-size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) {
-  return (size_t)(h_offset(T * k, T) + T * k * pad128(F) * 4);
-}
+size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) { return (size_t)(T * k * pad8(F) * 4); }
 
 hipError_t launch_moe_few(const MoeFewArgs& a, hipStream_t stream) {
   return a.i8 ? launch_ct<true>(a, stream) : launch_ct<false>(a, stream);
