@@ -6,12 +6,12 @@
 // With a few tokens every expert that is hit has a few rows, so the layer is
 // bound by the bytes of the hit experts' weights, 3 D F each, read once.  The
 // products run with the weights as the matrix instruction's first operand and
-// the tokens as the columns of its second: column c of column tile i is token
-// 16 i + c, zero where the token has not chosen the expert, and a tile without
-// any such token is skipped.  Weights are widened to bf16, which holds every
-// e4m3 and int8 value exactly; activations stay bf16, and h is carried as the
-// sum of two bf16 values (16 significant bits): the matrix cores have the time
-// for a second product per weight.
+// up to 16 of the expert's tokens as the columns of its second (an expert with
+// more tokens makes several units of 16, whose weights come from the caches
+// after the first).  Weights are widened to bf16, which holds every e4m3 and
+// int8 value exactly; activations stay bf16, and h is carried as the sum of two
+// bf16 values (16 significant bits): the matrix cores have the time for a
+// second product per weight.
 //
 // Every wave streams its own share of the weights through an LDS slot of its
 // own: direct-to-LDS loads fetch whole 128-byte lines (8 rows each; loading
@@ -20,19 +20,17 @@
 // before the step's products, so a slot is almost always on its way.  Weights
 // whose rows are not 16-byte aligned take the register loads instead.
 //
-//   up    tasks of (expert, 32 columns of h): 32 rows of w1 and of w3 over D.
+//   up    tasks of (unit, 32 columns of h): 32 rows of w1 and of w3 over D.
 //         KS of a workgroup's eight waves share a task and join through LDS in
-//         a fixed order; KS is as large as it takes for the tasks to fill the
-//         machine.
-//   down  one workgroup per 16 RT columns of the output.  The steps (expert,
-//         128 elements of F) of all experts are dealt to the sixteen waves in
-//         equal consecutive ranges; a wave keeps its sums for all tokens in
+//         a fixed order.
+//   down  one workgroup per 16 RT columns of the output.  The steps (unit, 128
+//         elements of F) of all units are dealt to the sixteen waves in equal
+//         consecutive ranges; a wave keeps its sums for all tokens in
 //         registers over its whole range, and the waves join once at the end
 //         in a fixed order, so no sum depends on timing.
 //
-// Which experts are hit is found by every workgroup for itself, from the
-// indices, with a table in LDS; so nothing has to be sorted first and the host
-// waits for nothing.
+// Which experts are hit is found by every workgroup for itself from the
+// indices, so nothing has to be sorted first and the host waits for nothing.
 #include <type_traits>
 
 #include "device.h"
@@ -57,50 +55,121 @@ constexpr int kMaxPairs = kMoeFewTokens * 16;
 // pair of each (token, expert); Fp = F rounded up to 8.
 __host__ __device__ inline int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 
-// The hit experts, in the order of their first (token, slot) pair.  Fills
-// idx[p] = expert of pair p (-1: none here) and list[i] = i-th hit expert; returns how
-// many there are.  table: E ints of scratch.
+// The work units: a hit expert and up to 16 of its tokens (kColumns), experts
+// in the order of their first (token, slot) pair.  list[i] = expert | group <<
+// 16; an expert's g-th group holds its 16 g-th to 16 g + 15-th token.  idx[p] =
+// expert of pair p (-1: none here).
+constexpr int kColumns = 16;
+constexpr int kMaxUnits = kMaxPairs;  // at most one per pair
+
+// At most 64 pairs (and so at most 16 tokens per expert, as long as T <= 16):
+// every wave finds the units by itself, in registers, lane p holding pair p.
+// Lanes naming the same expert are found with ballots over the bits of the
+// expert; the lowest of them leads.
+__device__ __forceinline__ int find_units_wave(const MoeFewArgs& a, int* idx, int* list) {
+  const int lane = threadIdx.x & 63;
+  const int P = a.T * a.k;
+  int e = -1;
+  if (lane < P) {
+    const int t = (int)((uint32_t)lane / (uint32_t)a.k);
+    e = a.indices[(int64_t)t * a.ldi + (lane - t * a.k)];
+    if (e < 0 || e >= a.E) e = -1;
+  }
+  idx[lane] = e;
+  uint64_t same = ~0ull;
+#pragma unroll
+  for (int b = 0; b < 12; ++b) {
+    const uint64_t m = __ballot((e >> b) & 1);
+    same &= (e >> b) & 1 ? m : ~m;
+  }
+  const uint64_t valid = __ballot(e >= 0);
+  const bool lead = e >= 0 && __builtin_ctzll(same & valid) == lane;
+  const uint64_t leads = __ballot(lead);
+  if (lead) list[__popcll(leads & ((1ull << lane) - 1))] = e;
+  __builtin_amdgcn_wave_barrier();
+  return __popcll(leads);
+}
+
+// Any number of pairs, by the whole workgroup; table: 2 E ints of scratch.
 template <int THREADS>
-__device__ __forceinline__ int hit_experts(const MoeFewArgs& a, int* table, int* idx, int* list, int* wave_n) {
+__device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* idx, int* list, int (*wave_n)[4]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int P = a.T * a.k;
-  for (int e = threadIdx.x; e < a.E; e += THREADS) table[e] = P;
+  int* lead = table;             // [E]: first pair of each expert
+  int* count = table + a.E;      // [E]: tokens of each expert
+  for (int e = threadIdx.x; e < a.E; e += THREADS) {
+    lead[e] = P;
+    count[e] = 0;
+  }
   for (int p = threadIdx.x; p < P; p += THREADS) {
     const int t = (int)((uint32_t)p / (uint32_t)a.k);
     const int e = a.indices[(int64_t)t * a.ldi + (p - t * a.k)];
     idx[p] = e >= 0 && e < a.E ? e : -1;
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < P; p += THREADS)
-    if (idx[p] >= 0) atomicMin(&table[idx[p]], p);
+  for (int p = threadIdx.x; p < P; p += THREADS) {
+    const int e = idx[p];
+    if (e < 0) continue;
+    atomicMin(&lead[e], p);
+    // a token that names the expert twice counts once
+    bool again = false;
+    for (int q = p - (int)((uint32_t)p % (uint32_t)a.k); q < p; ++q) again |= idx[q] == e;
+    if (!again) atomicAdd(&count[e], 1);
+  }
   __syncthreads();
   int total = 0;
   for (int base = 0; base < P; base += THREADS) {
     const int p = base + threadIdx.x;
-    const bool is = p < P && idx[p] >= 0 && table[idx[p]] == p;
-    const uint64_t m = __ballot(is);
-    if (lane == 0) wave_n[wave] = __popcll(m);
-    __syncthreads();
-    int at = total;
+    const int e = p < P ? idx[p] : -1;
+    const int groups = e >= 0 && lead[e] == p ? (count[e] + kColumns - 1) / kColumns : 0;
+    int below = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-      at += w < wave ? wave_n[w] : 0;
-      total += wave_n[w];
+    for (int g = 0; g < 4; ++g) {
+      const uint64_t m = __ballot(groups > g);
+      below += __popcll(m & ((1ull << lane) - 1));
+      if (lane == 0) wave_n[wave][g] = __popcll(m);
     }
-    if (is) list[at + __popcll(m & ((1ull << lane) - 1))] = idx[p];
+    __syncthreads();
+    int at = total + below;
+    for (int w = 0; w < THREADS / 64; ++w) {
+      const int n = wave_n[w][0] + wave_n[w][1] + wave_n[w][2] + wave_n[w][3];
+      at += w < wave ? n : 0;
+      total += n;
+    }
+    for (int g = 0; g < groups; ++g) list[at + g] = e | g << 16;
     __syncthreads();
   }
   return total;
 }
 
-// Lane t's view of an expert: the first of token t's slots that names it (-1:
-// none).
-__device__ __forceinline__ int slot_of(const MoeFewArgs& a, const int* idx, int e, int t) {
-  int first = -1;
-  if (t < a.T)
-    for (int j = a.k - 1; j >= 0; --j) first = idx[t * a.k + j] == e ? j : first;
-  return first;
-}
+// A unit's columns.  Lane t: the first of token t's slots that names the expert
+// (first, -1: none or another group) and the token's column (rank); lane c
+// (modulo 16) holds column c's token and pair, cols says how many there are.
+struct Unit {
+  int e, first, rank, cols, tok, pair;
+
+  __device__ __forceinline__ void set(const MoeFewArgs& a, const int* idx, int entry, int* scratch) {
+    const int lane = threadIdx.x & 63;
+    e = __builtin_amdgcn_readfirstlane(entry & 0xffff);
+    const int g = __builtin_amdgcn_readfirstlane(entry >> 16);
+    first = -1;
+    if (lane < a.T)
+      for (int j = a.k - 1; j >= 0; --j) first = idx[lane * a.k + j] == e ? j : first;
+    const uint64_t all = __ballot(first >= 0);
+    rank = __popcll(all & ((1ull << lane) - 1)) - kColumns * g;
+    if (rank < 0 || rank >= kColumns) first = -1;
+    cols = __popcll(all) - kColumns * g;
+    cols = cols < kColumns ? cols : kColumns;
+    if (first >= 0) scratch[rank] = (lane * a.k + first) << 8 | lane;
+    __builtin_amdgcn_wave_barrier();
+    const int v = scratch[lane & 15];
+    const bool on = (lane & 15) < cols;
+    tok = on ? v & 255 : 0;
+    pair = on ? v >> 8 : 0;
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ bool on() const { return (int)(threadIdx.x & 15) < cols; }
+};
 
 // 16 bytes from element k (of SZ bytes) of a row of K elements, at any address;
 // elements past the row are zero and nothing outside the row is read.  TAIL =
@@ -242,23 +311,42 @@ __device__ __forceinline__ void split_gate(float g, float u, uint16_t& hi, uint1
   lo = (uint16_t)pack_bf16x2(fabsf(top) < __builtin_inff() ? h - top : 0.0f, 0.0f);
 }
 
-template <bool I8, int CT, bool DMA>
-__global__ __launch_bounds__(64 * kUpWaves, CT == 1 && DMA ? 4 : 2) void moe_few_up_kernel(MoeFewArgs a) {
+template <bool I8, bool DMA>
+__global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(MoeFewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kUpWaves * kUpSlot];
-  __shared__ int idx[kMaxPairs], list[kMaxPairs];
-  __shared__ int wave_n[kUpWaves];
-  static_assert(kMaxRouteExperts * 4 <= kUpWaves * kUpSlot, "the table of experts lies in the ring");
+  __shared__ int idx[kMaxPairs], list[kMaxUnits];
+  __shared__ int wave_n[kUpWaves][4], scratch[kUpWaves][kColumns];
+  static_assert(kMaxRouteExperts * 8 <= kUpWaves * kUpSlot, "the table of experts lies in the ring");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int fr = lane & 15, fg = lane >> 4;
-  const int hits = hit_experts<64 * kUpWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n);
+  int *my_idx = idx, *my_list = list;
+  int units;
+  if (a.T * a.k <= 64 && a.T <= kColumns) {
+    my_idx = idx + 64 * wave;
+    my_list = list + 64 * wave;
+    units = find_units_wave(a, my_idx, my_list);
+  } else {
+    units = find_units<64 * kUpWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n);
+  }
+  units = __builtin_amdgcn_readfirstlane(units);
   const int nkb = (int)((a.D + BK - 1) / BK);
   const uint32_t tiles = (uint32_t)((a.F + kUpRows - 1) / kUpRows);
-  const int64_t tasks = (int64_t)hits * tiles, Fp = pad8(a.F);
+  const int64_t tasks = (int64_t)units * tiles, Fp = pad8(a.F);
   uint16_t* hi = static_cast<uint16_t*>(a.work);
   uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
+  // KS waves per task: the fewest K-blocks per wave over all rounds, counting
+  // the start and the join of a task as two.
   int ks = 1;
-  while (ks < kUpWaves && tasks * ks < (int64_t)gridDim.x * kUpWaves && 2 * ks <= nkb) ks *= 2;
+  int64_t least = INT64_MAX;
+  for (int c = 1; c <= kUpWaves; c *= 2) {
+    const int64_t slots = (int64_t)gridDim.x * (kUpWaves / c);
+    const int64_t cost = (tasks + slots - 1) / slots * ((nkb + c - 1) / c + 2);
+    if (cost < least) {
+      least = cost;
+      ks = c;
+    }
+  }
   const int sub = wave & (ks - 1), per = kUpWaves / ks;
   Stream<4, DMA> st;
   st.init(ring + wave * kUpSlot, a.ldw13);
@@ -266,18 +354,16 @@ __global__ __launch_bounds__(64 * kUpWaves, CT == 1 && DMA ? 4 : 2) void moe_few
   static_assert(2 * kUpRows * 17 * 4 <= kUpSlot, "a wave's sums fit its slot");
 
   for (int64_t base = (int64_t)blockIdx.x * per; base < tasks; base += (int64_t)gridDim.x * per) {
-    __syncthreads();
     const int64_t task = base + wave / ks;
     const bool live = task < tasks;
-    const int e = __builtin_amdgcn_readfirstlane(list[live ? (uint32_t)task / tiles : 0]);
-    const int64_t f0 = live ? (int64_t)((uint32_t)task % tiles) * kUpRows : 0;
-    const int first = slot_of(a, idx, e, lane);
-    const uint64_t mask = live ? __ballot(first >= 0) : 0;
-    v4f acc[4][CT];
+    const uint32_t ui = live ? (uint32_t)task / tiles : 0;
+    const int64_t f0 = live ? (int64_t)((uint32_t)task - ui * tiles) * kUpRows : 0;
+    Unit u;
+    u.set(a, my_idx, my_list[ui], scratch[wave]);
+    const int e = u.e;
+    v4f acc[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     if (live) {
       const int rows = (int)(a.F - f0 < kUpRows ? a.F - f0 : kUpRows);
       Panel<DMA> w1, w3;
@@ -288,17 +374,21 @@ __global__ __launch_bounds__(64 * kUpWaves, CT == 1 && DMA ? 4 : 2) void moe_few
 #pragma unroll
         for (int i = 0; i < 4; ++i) st.issue(i, i < 2 ? w1 : w3, i & 1, a.ldw13, (uint32_t)kb * BK, (uint32_t)a.D);
       };
-      // x of column tile c, elements of K-block kb; zero for tokens that have not chosen e
-      auto columns = [&](int c, int kb, u32x4 (&b)[4]) __attribute__((always_inline)) {
-        const bool on = (mask >> (16 * c + fr)) & 1;
-        const uint8_t* row = reinterpret_cast<const uint8_t*>(a.x + (int64_t)(on ? 16 * c + fr : 0) * a.ldx);
-        const int64_t k = (int64_t)kb * BK + 32 * fg;
-        const bool full = (int64_t)(kb + 1) * BK <= a.D;
+      // x of the lane's column, elements of K-block kb
+      const bool on = u.on();
+      const uint8_t* xrow = reinterpret_cast<const uint8_t*>(a.x + (int64_t)u.tok * a.ldx);
+      u32x4 b[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          b[s] = u32x4{0u, 0u, 0u, 0u};
-          if (!on) continue;
-          b[s] = full ? load16<2, false>(row, k + 8 * s, a.D) : load16<2, true>(row, k + 8 * s, a.D);
+      for (int s = 0; s < 4; ++s) b[s] = u32x4{0u, 0u, 0u, 0u};
+      auto columns = [&](int kb) __attribute__((always_inline)) {
+        if (!on) return;
+        const int64_t k = (int64_t)kb * BK + 32 * fg;
+        if ((int64_t)(kb + 1) * BK <= a.D) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) b[s] = load16<2, false>(xrow, k + 8 * s, a.D);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) b[s] = load16<2, true>(xrow, k + 8 * s, a.D);
         }
       };
       // Block scales: w1's 32 rows lie in one 128-row block; w3's may span two,
@@ -309,13 +399,11 @@ __global__ __launch_bounds__(64 * kUpWaves, CT == 1 && DMA ? 4 : 2) void moe_few
       const float* s3p = se + (r3 >> 7) * a.lds13;
       const float* s3q = se + ((r3 + rows - 1) >> 7) * a.lds13;
       const int cut = (int)(BK - (r3 & (BK - 1)));  // first w3 row of the second block
-      u32x4 b[4];
-      int kb = sub;
-      if (kb < nkb) {
-        issue(kb);
-        if constexpr (CT == 1) columns(0, kb, b);
+      if (sub < nkb) {
+        issue(sub);
+        columns(sub);
       }
-      for (; kb < nkb; kb += ks) {
+      for (int kb = sub; kb < nkb; kb += ks) {
         float s1 = 1.0f, s3a = 1.0f, s3b = 1.0f;
         if constexpr (!I8) {
           s1 = s1p[kb];
@@ -324,192 +412,191 @@ __global__ __launch_bounds__(64 * kUpWaves, CT == 1 && DMA ? 4 : 2) void moe_few
         }
         st.take();
         const bool more = kb + ks < nkb;
-        if (DMA && CT == 1 && more) issue(kb + ks);
+        if (DMA && more) issue(kb + ks);
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          if (CT > 1) {
-            if (((mask >> (16 * c)) & 0xffff) == 0) continue;
-            columns(c, kb, b);
-          }
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (I8) {
+            acc[i] = block_product<I8>(st.w[i], b, acc[i]);
+          } else {
+            const v4f part = block_product<I8>(st.w[i], b, v4f{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (I8) {
-              acc[i][c] = block_product<I8>(st.w[i], b, acc[i][c]);
-            } else {
-              const v4f part = block_product<I8>(st.w[i], b, v4f{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                const float s = i < 2 ? s1 : (16 * (i & 1) + 4 * fg + v < cut ? s3a : s3b);
-                acc[i][c][v] = __builtin_fmaf(part[v], s, acc[i][c][v]);
-              }
+            for (int v = 0; v < 4; ++v) {
+              const float s = i < 2 ? s1 : (16 * (i & 1) + 4 * fg + v < cut ? s3a : s3b);
+              acc[i][v] = __builtin_fmaf(part[v], s, acc[i][v]);
             }
           }
         }
         if (more) {
-          if (!DMA || CT > 1) issue(kb + ks);
-          if constexpr (CT == 1) columns(0, kb + ks, b);
+          if (!DMA) issue(kb + ks);
+          columns(kb + ks);
         }
       }
     }
 
-    // Join the waves' sums, gate, and write h: 32 x 16 values per task and column tile.
+    // Join the waves' sums, gate, and write h: 32 x 16 values per task.
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (c > 0) __syncthreads();
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) red[16 * i + 4 * fg + v][fr] = acc[i][c][v];
-      __syncthreads();
-      const float* group = reinterpret_cast<const float*>(ring + (wave - sub) * kUpSlot);
-      for (int q = sub * 64 + lane; q < kUpRows * 16; q += ks * 64) {
-        const int r = q & (kUpRows - 1), t = 16 * c + (q >> 5);
-        const int slot = __shfl(first, t & 63);
-        const int64_t f = f0 + r;
-        if (!((mask >> t) & 1) || f >= Fp) continue;
-        uint16_t vh = 0, vl = 0;
-        if (f < a.F) {
-          float g = 0.0f, u = 0.0f;
-          for (int w = 0; w < ks; ++w) {
-            g += group[w * (kUpSlot / 4) + r * 17 + (q >> 5)];
-            u += group[w * (kUpSlot / 4) + (kUpRows + r) * 17 + (q >> 5)];
-          }
-          if constexpr (I8) {
-            g *= a.s13[(int64_t)e * a.lds13 + f];
-            u *= a.s13[(int64_t)e * a.lds13 + a.F + f];
-          }
-          split_gate(g, u, vh, vl);
+      for (int v = 0; v < 4; ++v) red[16 * i + 4 * fg + v][fr] = acc[i][v];
+    __syncthreads();
+    const float* group = reinterpret_cast<const float*>(ring + (wave - sub) * kUpSlot);
+    for (int q = sub * 64 + lane; q < kUpRows * kColumns; q += ks * 64) {
+      const int r = q & (kUpRows - 1), c = q >> 5;
+      const int pair = __shfl(u.pair, c);
+      const int64_t f = f0 + r;
+      if (!live || c >= u.cols || f >= Fp) continue;
+      uint16_t vh = 0, vl = 0;
+      if (f < a.F) {
+        float g = 0.0f, up = 0.0f;
+        for (int w = 0; w < ks; ++w) {
+          g += group[w * (kUpSlot / 4) + r * 17 + c];
+          up += group[w * (kUpSlot / 4) + (kUpRows + r) * 17 + c];
         }
-        const int64_t at = ((int64_t)t * a.k + slot) * Fp + f;
-        hi[at] = vh;
-        lo[at] = vl;
+        if constexpr (I8) {
+          g *= a.s13[(int64_t)e * a.lds13 + f];
+          up *= a.s13[(int64_t)e * a.lds13 + a.F + f];
+        }
+        split_gate(g, up, vh, vl);
       }
+      hi[(int64_t)pair * Fp + f] = vh;
+      lo[(int64_t)pair * Fp + f] = vl;
     }
+    __syncthreads();
   }
 }
 
-// RT row tiles of 16 output columns per workgroup.
+// RT row tiles of 16 output columns per workgroup; CT column tiles of 16 tokens.
 template <bool I8, int CT, int RT, bool DMA>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArgs a) {
   constexpr int SLOT = RT * 16 * BK;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kDownWaves * SLOT];
-  __shared__ int idx[kMaxPairs], list[kMaxPairs];
-  __shared__ int wave_n[kDownWaves];
-  static_assert(kMaxRouteExperts * 4 <= kDownWaves * SLOT, "the table of experts lies in the ring");
+  __shared__ int idx[kMaxPairs], list[kMaxUnits];
+  __shared__ int wave_n[kDownWaves][4], scratch[kDownWaves][kColumns];
+  static_assert(kMaxRouteExperts * 8 <= kDownWaves * SLOT, "the table of experts lies in the ring");
+  static_assert(64 * kDownWaves <= kMaxPairs, "a list of 64 per wave");
   constexpr int CJ = CT < 2 ? CT : 2;  // column tiles joined at a time
   static_assert(16 * CJ * 16 * RT * 4 <= SLOT, "a wave's sums fit its slot");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int fr = lane & 15, fg = lane >> 4;
-  // F = 0: the up kernel did not run, and the output is zero
-  const int hits = a.F > 0 ? hit_experts<64 * kDownWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n) : 0;
+  int *my_idx = idx, *my_list = list;
+  int units = 0;  // F = 0: the up kernel did not run, and the output is zero
+  if (a.F > 0) {
+    if (a.T * a.k <= 64 && a.T <= kColumns) {
+      my_idx = idx + 64 * wave;
+      my_list = list + 64 * wave;
+      units = find_units_wave(a, my_idx, my_list);
+    } else {
+      units = find_units<64 * kDownWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n);
+    }
+  }
+  units = __builtin_amdgcn_readfirstlane(units);
   const int64_t d0 = (int64_t)blockIdx.x * (16 * RT), Fp = pad8(a.F);
   const int rows = (int)(a.D - d0 < 16 * RT ? a.D - d0 : 16 * RT);
   const uint16_t* hi = static_cast<const uint16_t*>(a.work);
   const uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
   const int per = (int)((a.F + BK - 1) / BK);
-  const int64_t steps = (int64_t)hits * per;
+  const int64_t steps = (int64_t)units * per;
   const int64_t s0 = steps * wave / kDownWaves, s1 = steps * (wave + 1) / kDownWaves;
   const int64_t kbd = (a.D + BK - 1) / BK;
 
   Stream<RT, DMA> st;
   st.init(ring + wave * SLOT, a.ldw2);
-  v4f acc[RT][CT];
+  v4f acc[RT], sum[RT][CT];  // the current unit's columns; every token's
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int i = 0; i < RT; ++i) {
+    acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-  int at = (int)(s0 / per), kp = (int)(s0 - (int64_t)at * per);
-  auto expert = [&](int i) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(list[i]); };
+    for (int c = 0; c < CT; ++c) sum[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   Panel<DMA> w2;
   auto issue = [&](int e, int p) __attribute__((always_inline)) {
     w2.set(a.w2 + ((int64_t)e * a.D + d0) * a.ldw2, a.ldw2, rows, a.F);
 #pragma unroll
     for (int i = 0; i < RT; ++i) st.issue(i, w2, i, a.ldw2, (uint32_t)p * BK, (uint32_t)a.F);
   };
-  // Per expert: lane t's first slot and weight, and the rows' scales (I8).
-  int first = -1;
-  float wsum = 0.0f;
-  uint64_t mask = 0;
-  float rs[RT][4];
-  auto enter = [&](int e) __attribute__((always_inline)) {
-    first = slot_of(a, idx, e, lane);
-    mask = __ballot(first >= 0);
-    wsum = 0.0f;
-    if (first >= 0)
-      for (int j = first; j < a.k; ++j)
-        if (idx[lane * a.k + j] == e) wsum += bf16_lo(a.weights[(int64_t)lane * a.ldwt + j]);
+  u32x4 bh[4], bl[4];
+  Unit u;
+  auto columns = [&](int p) __attribute__((always_inline)) {
+    const int64_t row = (int64_t)u.pair * Fp;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int64_t k = (int64_t)p * BK + 32 * fg + 8 * s;
+      bh[s] = bl[s] = u32x4{0u, 0u, 0u, 0u};
+      if (u.on() && k < a.F) {
+        bh[s] = *reinterpret_cast<const u32x4*>(hi + row + k);
+        bl[s] = *reinterpret_cast<const u32x4*>(lo + row + k);
+      }
+    }
+  };
+  // Add a finished unit's columns to their tokens, times the tokens' weights.
+  auto leave = [&]() __attribute__((always_inline)) {
+    float w = 0.0f;
+    if (u.first >= 0)
+      for (int j = u.first; j < a.k; ++j)
+        if (my_idx[lane * a.k + j] == u.e) w += bf16_lo(a.weights[(int64_t)lane * a.ldwt + j]);
     if constexpr (I8) {
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int r = 16 * i + 4 * fg + v;
-          rs[i][v] = a.s2[(int64_t)e * a.lds2 + d0 + (r < rows ? r : rows - 1)];
+          acc[i][v] *= a.s2[(int64_t)u.e * a.lds2 + d0 + (r < rows ? r : rows - 1)];
         }
     }
-  };
-  // h of column tile c, elements of step p.
-  auto columns = [&](int c, int p, u32x4 (&bh)[4], u32x4 (&bl)[4]) __attribute__((always_inline)) {
-    const int slot = __shfl(first, 16 * c + fr);
-    const bool on = (mask >> (16 * c + fr)) & 1;
-    const int64_t row = on ? ((int64_t)(16 * c + fr) * a.k + slot) * Fp : 0;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int64_t k = (int64_t)p * BK + 32 * fg + 8 * s;
-      bh[s] = bl[s] = u32x4{0u, 0u, 0u, 0u};
-      if (on && k < a.F) {
-        bh[s] = *reinterpret_cast<const u32x4*>(hi + row + k);
-        bl[s] = *reinterpret_cast<const u32x4*>(lo + row + k);
-      }
-    }
-  };
-
-  u32x4 bh[4], bl[4];
-  int e = 0;
-  if (s0 < s1) {
-    e = expert(at);
-    __syncthreads();
-    enter(e);
-    issue(e, kp);
-    if constexpr (CT == 1) columns(0, kp, bh, bl);
-  } else {
-    __syncthreads();
-  }
-  for (int64_t s = s0; s < s1; ++s) {
-    const float sc = I8 ? 1.0f : a.s2[((int64_t)e * kbd + (d0 >> 7)) * a.lds2 + kp];
-    const bool more = s + 1 < s1;
-    const bool turn = kp + 1 == per;
-    const int kn = turn ? 0 : kp + 1;
-    const int en = more && turn ? expert(at + 1) : e;
-    st.take();
-    if (DMA && CT == 1 && more) issue(en, kn);
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      if (CT > 1) {
-        if (((mask >> (16 * c)) & 0xffff) == 0) continue;
-        columns(c, kp, bh, bl);
-      }
-      const float w = __shfl(wsum, 16 * c + fr);
+      const int has = __shfl(u.first, 16 * c + fr), col = __shfl(u.rank, 16 * c + fr);
+      const float wc = __shfl(w, 16 * c + fr);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const v4f part = block_product<I8>(st.w[i], bl, block_product<I8>(st.w[i], bh, v4f{0.0f, 0.0f, 0.0f, 0.0f}));
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][c][v] = __builtin_fmaf(part[v], I8 ? rs[i][v] * w : sc * w, acc[i][c][v]);
-      }
+        for (int v = 0; v < 4; ++v) {
+          const float y = __shfl(acc[i][v], (lane & 48) | (col & 15));
+          if (has >= 0) sum[i][c][v] = __builtin_fmaf(y, wc, sum[i][c][v]);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+
+  int at = per > 0 ? (int)(s0 / per) : 0, kp = (int)(s0 - (int64_t)at * per);
+  __syncthreads();  // the table of experts gives way to the ring
+  if (s0 < s1) {
+    const int entry = my_list[at];
+    issue(__builtin_amdgcn_readfirstlane(entry & 0xffff), kp);
+    u.set(a, my_idx, entry, scratch[wave]);
+    columns(kp);
+  }
+  for (int64_t s = s0; s < s1; ++s) {
+    const float sc = I8 ? 1.0f : a.s2[((int64_t)u.e * kbd + (d0 >> 7)) * a.lds2 + kp];
+    const bool more = s + 1 < s1, turn = kp + 1 == per;
+    const int kn = turn ? 0 : kp + 1;
+    int entry = 0, en = u.e;
+    if (more && turn) {
+      entry = my_list[at + 1];
+      en = __builtin_amdgcn_readfirstlane(entry & 0xffff);
+    }
+    st.take();
+    if (DMA && more) issue(en, kn);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const v4f part = block_product<I8>(st.w[i], bl, block_product<I8>(st.w[i], bh, v4f{0.0f, 0.0f, 0.0f, 0.0f}));
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][v] = I8 ? acc[i][v] + part[v] : __builtin_fmaf(part[v], sc, acc[i][v]);
+    }
+    if (turn || !more) leave();
     if (more) {
+      if (!DMA) issue(en, kn);
       if (turn) {
         ++at;
-        e = en;
-        enter(e);
+        u.set(a, my_idx, entry, scratch[wave]);
       }
       kp = kn;
-      if (!DMA || CT > 1) issue(e, kp);
-      if constexpr (CT == 1) columns(0, kp, bh, bl);
+      columns(kp);
     }
   }
+  __syncthreads();
 
   // sums[wave][token][row], in the waves' slots
 #pragma unroll
@@ -520,7 +607,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int c = 0; c < CJ; ++c)
-        *reinterpret_cast<v4f*>(mine + (16 * c + fr) * (16 * RT) + 16 * i + 4 * fg) = acc[i][c0 + c];
+        *reinterpret_cast<v4f*>(mine + (16 * c + fr) * (16 * RT) + 16 * i + 4 * fg) = sum[i][c0 + c];
     __syncthreads();
     for (int q = threadIdx.x; q < 16 * CJ * 16 * RT; q += 64 * kDownWaves) {
       float y = 0.0f;
@@ -539,7 +626,7 @@ hipError_t launch(const MoeFewArgs& a, hipStream_t stream) {
     // at most two workgroups per CU, which is what fits
     const int64_t tasks = (int64_t)a.T * a.k * ((a.F + kUpRows - 1) / kUpRows);
     const int64_t grid = tasks < 2 * cus ? tasks : 2 * cus;
-    hipLaunchKernelGGL((moe_few_up_kernel<I8, CT, DMA>), dim3((unsigned)grid), dim3(64 * kUpWaves), 0, stream, a);
+    hipLaunchKernelGGL((moe_few_up_kernel<I8, DMA>), dim3((unsigned)grid), dim3(64 * kUpWaves), 0, stream, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -564,9 +651,7 @@ hipError_t launch_feed(const MoeFewArgs& a, hipStream_t stream) {
 
 template <bool I8>
 hipError_t launch_ct(const MoeFewArgs& a, hipStream_t stream) {
-  if (a.T <= 16) return launch_feed<I8, 1>(a, stream);
-  if (a.T <= 32) return launch_feed<I8, 2>(a, stream);
-  return launch_feed<I8, 4>(a, stream);
+  return a.T <= 16 ? launch_feed<I8, 1>(a, stream) : launch_feed<I8, 4>(a, stream);
 }
 
 }  // namespace
