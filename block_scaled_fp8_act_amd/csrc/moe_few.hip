@@ -57,9 +57,10 @@ __host__ __device__ inline int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 
 // The work units: a hit expert and up to 16 of its tokens (kColumns), experts
 // in the order of their first (token, slot) pair.  list[i] = expert | group <<
-// 16; an expert's g-th group holds its 16 g-th to 16 g + 15-th token.  idx[p] =
-// expert of pair p (-1: none here).
+// 16 | kAgain if the expert has several; its g-th group holds its 16 g-th to
+// 16 g + 15-th token.  idx[p] = expert of pair p (-1: none here).
 constexpr int kColumns = 16;
+constexpr int kAgain = 1 << 24;
 constexpr int kMaxUnits = kMaxPairs;  // at most one per pair
 
 // At most 64 pairs (and so at most 16 tokens per expert, as long as T <= 16):
@@ -136,7 +137,7 @@ __device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* 
       at += w < wave ? n : 0;
       total += n;
     }
-    for (int g = 0; g < groups; ++g) list[at + g] = e | g << 16;
+    for (int g = 0; g < groups; ++g) list[at + g] = e | g << 16 | (groups > 1 ? kAgain : 0);
     __syncthreads();
   }
   return total;
@@ -151,7 +152,7 @@ struct Unit {
   __device__ __forceinline__ void set(const MoeFewArgs& a, const int* idx, int entry, int* scratch) {
     const int lane = threadIdx.x & 63;
     e = __builtin_amdgcn_readfirstlane(entry & 0xffff);
-    const int g = __builtin_amdgcn_readfirstlane(entry >> 16);
+    const int g = __builtin_amdgcn_readfirstlane((entry >> 16) & 15);
     first = -1;
     if (lane < a.T)
       for (int j = a.k - 1; j >= 0; --j) first = idx[lane * a.k + j] == e ? j : first;
@@ -233,10 +234,14 @@ struct Panel {
   const uint8_t* base;
   i32x4 rs;
   int rows;
+  bool whole;  // no row past the matrix
+  bool once;   // no other unit reads it
 
-  __device__ __forceinline__ void set(const uint8_t* p, int64_t ld, int n, int64_t K) {
+  __device__ __forceinline__ void set(const uint8_t* p, int64_t ld, int n, int full, int64_t K, int entry) {
     base = p;
     rows = n;
+    whole = n == full;
+    once = !(entry & kAgain);
     if constexpr (DMA) rs = make_rsrc(p, (uint32_t)((n - 1) * ld + K));
   }
 };
@@ -267,10 +272,17 @@ struct Stream {
   __device__ __forceinline__ void issue(int b, const Panel<DMA>& p, int i, int64_t ld, uint32_t k, uint32_t K) {
     const int lane = threadIdx.x & 63;
     if constexpr (DMA) {
+      const bool edge = !p.whole || k + BK > K;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool in = 16 * i + 8 * h + (lane >> 3) < p.rows && k + kc[h] < K;
-        dma_b128(p.rs, lds + (uint32_t)(b * 2048 + h * 1024), in ? voff[h] : kOob, (uint32_t)(16 * i * ld) + k);
+        uint32_t v = voff[h];
+        if (edge) v = 16 * i + 8 * h + (lane >> 3) < p.rows && k + kc[h] < K ? v : kOob;
+        const uint32_t to = lds + (uint32_t)(b * 2048 + h * 1024), from = (uint32_t)(16 * i * ld) + k;
+        // nontemporal where nothing is read again: one token 78.1 -> 72.3 us,
+        // 16 tokens 521.7 -> 485.1; with it also for experts of several
+        // units, 64 tokens over 8 experts took 84.3 against 69.8 us
+        if (p.once) dma_b128_nt(p.rs, to, v, from);
+        else dma_b128(p.rs, to, v, from);
       }
     } else {
       const int r = 16 * i + (lane & 15);
@@ -335,18 +347,11 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
   const int64_t tasks = (int64_t)units * tiles, Fp = pad8(a.F);
   uint16_t* hi = static_cast<uint16_t*>(a.work);
   uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
-  // KS waves per task: the fewest K-blocks per wave over all rounds, counting
-  // the start and the join of a task as two.
+  // KS waves per task, up to all of them: the more share a task, the longer the
+  // run of each weight row that is read at one time (16 tokens: 462 us with
+  // eight waves per task, 485 with the one to eight that would balance best).
   int ks = 1;
-  int64_t least = INT64_MAX;
-  for (int c = 1; c <= kUpWaves; c *= 2) {
-    const int64_t slots = (int64_t)gridDim.x * (kUpWaves / c);
-    const int64_t cost = (tasks + slots - 1) / slots * ((nkb + c - 1) / c + 2);
-    if (cost < least) {
-      least = cost;
-      ks = c;
-    }
-  }
+  while (ks < kUpWaves && 2 * ks <= nkb) ks *= 2;
   const int sub = wave & (ks - 1), per = kUpWaves / ks;
   Stream<4, DMA> st;
   st.init(ring + wave * kUpSlot, a.ldw13);
@@ -358,8 +363,9 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
     const bool live = task < tasks;
     const uint32_t ui = live ? (uint32_t)task / tiles : 0;
     const int64_t f0 = live ? (int64_t)((uint32_t)task - ui * tiles) * kUpRows : 0;
+    const int entry = __builtin_amdgcn_readfirstlane(my_list[ui]);
     Unit u;
-    u.set(a, my_idx, my_list[ui], scratch[wave]);
+    u.set(a, my_idx, entry, scratch[wave]);
     const int e = u.e;
     v4f acc[4];
 #pragma unroll
@@ -368,8 +374,8 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
       const int rows = (int)(a.F - f0 < kUpRows ? a.F - f0 : kUpRows);
       Panel<DMA> w1, w3;
       const uint8_t* at1 = a.w13 + ((int64_t)e * 2 * a.F + f0) * a.ldw13;
-      w1.set(at1, a.ldw13, rows, a.D);
-      w3.set(at1 + a.F * a.ldw13, a.ldw13, rows, a.D);
+      w1.set(at1, a.ldw13, rows, kUpRows, a.D, entry);
+      w3.set(at1 + a.F * a.ldw13, a.ldw13, rows, kUpRows, a.D, entry);
       auto issue = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) st.issue(i, i < 2 ? w1 : w3, i & 1, a.ldw13, (uint32_t)kb * BK, (uint32_t)a.D);
@@ -494,7 +500,6 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
   const int64_t d0 = (int64_t)blockIdx.x * (16 * RT), Fp = pad8(a.F);
   const int rows = (int)(a.D - d0 < 16 * RT ? a.D - d0 : 16 * RT);
   const uint16_t* hi = static_cast<const uint16_t*>(a.work);
-  const uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
   const int per = (int)((a.F + BK - 1) / BK);
   const int64_t steps = (int64_t)units * per;
   const int64_t s0 = steps * wave / kDownWaves, s1 = steps * (wave + 1) / kDownWaves;
@@ -510,22 +515,34 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     for (int c = 0; c < CT; ++c) sum[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
   Panel<DMA> w2;
-  auto issue = [&](int e, int p) __attribute__((always_inline)) {
-    w2.set(a.w2 + ((int64_t)e * a.D + d0) * a.ldw2, a.ldw2, rows, a.F);
+  auto panel = [&](int entry) __attribute__((always_inline)) {
+    w2.set(a.w2 + ((int64_t)(entry & 0xffff) * a.D + d0) * a.ldw2, a.ldw2, rows, 16 * RT, a.F, entry);
+  };
+  auto issue = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) st.issue(i, w2, i, a.ldw2, (uint32_t)p * BK, (uint32_t)a.F);
   };
   u32x4 bh[4], bl[4];
   Unit u;
+  const int64_t to_lo = (int64_t)a.T * a.k * Fp;
   auto columns = [&](int p) __attribute__((always_inline)) {
-    const int64_t row = (int64_t)u.pair * Fp;
+    const uint16_t* h = hi + (int64_t)u.pair * Fp + p * BK + 32 * fg;
+    const int left = (int)(a.F - (int64_t)p * BK) - 32 * fg;  // of the row, from this lane's elements
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int64_t k = (int64_t)p * BK + 32 * fg + 8 * s;
-      bh[s] = bl[s] = u32x4{0u, 0u, 0u, 0u};
-      if (u.on() && k < a.F) {
-        bh[s] = *reinterpret_cast<const u32x4*>(hi + row + k);
-        bl[s] = *reinterpret_cast<const u32x4*>(lo + row + k);
+    for (int s = 0; s < 4; ++s) bh[s] = bl[s] = u32x4{0u, 0u, 0u, 0u};
+    if (!u.on()) return;
+    if ((int64_t)(p + 1) * BK <= a.F) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        bh[s] = *reinterpret_cast<const u32x4*>(h + 8 * s);
+        bl[s] = *reinterpret_cast<const u32x4*>(h + to_lo + 8 * s);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (8 * s >= left) continue;
+        bh[s] = *reinterpret_cast<const u32x4*>(h + 8 * s);
+        bl[s] = *reinterpret_cast<const u32x4*>(h + to_lo + 8 * s);
       }
     }
   };
@@ -563,8 +580,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
   int at = per > 0 ? (int)(s0 / per) : 0, kp = (int)(s0 - (int64_t)at * per);
   __syncthreads();  // the table of experts gives way to the ring
   if (s0 < s1) {
-    const int entry = my_list[at];
-    issue(__builtin_amdgcn_readfirstlane(entry & 0xffff), kp);
+    const int entry = __builtin_amdgcn_readfirstlane(my_list[at]);
+    panel(entry);
+    issue(kp);
     u.set(a, my_idx, entry, scratch[wave]);
     columns(kp);
   }
@@ -572,13 +590,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     const float sc = I8 ? 1.0f : a.s2[((int64_t)u.e * kbd + (d0 >> 7)) * a.lds2 + kp];
     const bool more = s + 1 < s1, turn = kp + 1 == per;
     const int kn = turn ? 0 : kp + 1;
-    int entry = 0, en = u.e;
+    int entry = 0;
     if (more && turn) {
-      entry = my_list[at + 1];
-      en = __builtin_amdgcn_readfirstlane(entry & 0xffff);
+      entry = __builtin_amdgcn_readfirstlane(my_list[at + 1]);
+      panel(entry);
     }
     st.take();
-    if (DMA && more) issue(en, kn);
+    if (DMA && more) issue(kn);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const v4f part = block_product<I8>(st.w[i], bl, block_product<I8>(st.w[i], bh, v4f{0.0f, 0.0f, 0.0f, 0.0f}));
@@ -587,7 +605,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     }
     if (turn || !more) leave();
     if (more) {
-      if (!DMA) issue(en, kn);
+      if (!DMA) issue(kn);
       if (turn) {
         ++at;
         u.set(a, my_idx, entry, scratch[wave]);
@@ -631,7 +649,10 @@ hipError_t launch(const MoeFewArgs& a, hipStream_t stream) {
     if (err != hipSuccess) return err;
   }
   const dim3 blk(64 * kDownWaves);
-  if ((a.D + 31) / 32 >= cus / 2)
+  // 32 output columns per workgroup read h half as often as 16 (7168 columns:
+  // 73 against 84 us for one token), if that leaves enough workgroups (4096
+  // columns: 128 of them take 78 us, 256 with 16 columns 70)
+  if ((a.D + 31) / 32 * 4 >= 3 * cus)
     hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 2, DMA>), dim3((unsigned)((a.D + 31) / 32)), blk, 0, stream, a);
   else
     hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 1, DMA>), dim3((unsigned)((a.D + 15) / 16)), blk, 0, stream, a);
