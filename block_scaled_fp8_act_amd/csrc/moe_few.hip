@@ -67,14 +67,15 @@ constexpr int kMaxUnits = kMaxPairs;  // at most one per pair
 // every wave finds the units by itself, in registers, lane p holding pair p.
 // Lanes naming the same expert are found with ballots over the bits of the
 // expert; the lowest of them leads.
-__device__ __forceinline__ int find_units_wave(const MoeFewArgs& a, int* idx, int* list) {
+__device__ __forceinline__ int find_units_wave(const MoeFewArgs& a, int* idx, int* list, float* wt) {
   const int lane = threadIdx.x & 63;
   const int P = a.T * a.k;
   int e = -1;
   if (lane < P) {
-    const int t = (int)((uint32_t)lane / (uint32_t)a.k);
-    e = a.indices[(int64_t)t * a.ldi + (lane - t * a.k)];
+    const int t = (int)((uint32_t)lane / (uint32_t)a.k), j = lane - t * a.k;
+    e = a.indices[(int64_t)t * a.ldi + j];
     if (e < 0 || e >= a.E) e = -1;
+    if (wt != nullptr) wt[lane] = bf16_lo(a.weights[(int64_t)t * a.ldwt + j]);
   }
   idx[lane] = e;
   uint64_t same = ~0ull;
@@ -93,7 +94,8 @@ __device__ __forceinline__ int find_units_wave(const MoeFewArgs& a, int* idx, in
 
 // Any number of pairs, by the whole workgroup; table: 2 E ints of scratch.
 template <int THREADS>
-__device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* idx, int* list, int (*wave_n)[4]) {
+__device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* idx, int* list, float* wt,
+                                          int (*wave_n)[4]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int P = a.T * a.k;
   int* lead = table;             // [E]: first pair of each expert
@@ -103,9 +105,10 @@ __device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* 
     count[e] = 0;
   }
   for (int p = threadIdx.x; p < P; p += THREADS) {
-    const int t = (int)((uint32_t)p / (uint32_t)a.k);
-    const int e = a.indices[(int64_t)t * a.ldi + (p - t * a.k)];
+    const int t = (int)((uint32_t)p / (uint32_t)a.k), j = p - t * a.k;
+    const int e = a.indices[(int64_t)t * a.ldi + j];
     idx[p] = e >= 0 && e < a.E ? e : -1;
+    if (wt != nullptr) wt[p] = bf16_lo(a.weights[(int64_t)t * a.ldwt + j]);
   }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += THREADS) {
@@ -337,9 +340,9 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
   if (a.T * a.k <= 64 && a.T <= kColumns) {
     my_idx = idx + 64 * wave;
     my_list = list + 64 * wave;
-    units = find_units_wave(a, my_idx, my_list);
+    units = find_units_wave(a, my_idx, my_list, nullptr);
   } else {
-    units = find_units<64 * kUpWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n);
+    units = find_units<64 * kUpWaves>(a, reinterpret_cast<int*>(ring), idx, list, nullptr, wave_n);
   }
   units = __builtin_amdgcn_readfirstlane(units);
   const int nkb = (int)((a.D + BK - 1) / BK);
@@ -477,6 +480,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
   constexpr int SLOT = RT * 16 * BK;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kDownWaves * SLOT];
   __shared__ int idx[kMaxPairs], list[kMaxUnits];
+  __shared__ float wt[kMaxPairs];
   __shared__ int wave_n[kDownWaves][4], scratch[kDownWaves][kColumns];
   static_assert(kMaxRouteExperts * 8 <= kDownWaves * SLOT, "the table of experts lies in the ring");
   static_assert(64 * kDownWaves <= kMaxPairs, "a list of 64 per wave");
@@ -486,14 +490,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int fr = lane & 15, fg = lane >> 4;
   int *my_idx = idx, *my_list = list;
+  float* my_wt = wt;
   int units = 0;  // F = 0: the up kernel did not run, and the output is zero
   if (a.F > 0) {
     if (a.T * a.k <= 64 && a.T <= kColumns) {
       my_idx = idx + 64 * wave;
       my_list = list + 64 * wave;
-      units = find_units_wave(a, my_idx, my_list);
+      my_wt = wt + 64 * wave;
+      units = find_units_wave(a, my_idx, my_list, my_wt);
     } else {
-      units = find_units<64 * kDownWaves>(a, reinterpret_cast<int*>(ring), idx, list, wave_n);
+      units = find_units<64 * kDownWaves>(a, reinterpret_cast<int*>(ring), idx, list, wt, wave_n);
     }
   }
   units = __builtin_amdgcn_readfirstlane(units);
@@ -551,7 +557,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     float w = 0.0f;
     if (u.first >= 0)
       for (int j = u.first; j < a.k; ++j)
-        if (my_idx[lane * a.k + j] == u.e) w += bf16_lo(a.weights[(int64_t)lane * a.ldwt + j]);
+        if (my_idx[lane * a.k + j] == u.e) w += my_wt[lane * a.k + j];
     if constexpr (I8) {
 #pragma unroll
       for (int i = 0; i < RT; ++i)
