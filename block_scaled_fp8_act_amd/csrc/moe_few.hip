@@ -6,12 +6,11 @@
 // With a few tokens every expert that is hit has a few rows, so the layer is
 // bound by the bytes of the hit experts' weights, 3 D F each, read once.  The
 // products run with the weights as the matrix instruction's first operand and
-// up to 16 of the expert's tokens as the columns of its second (an expert with
-// more tokens makes several units of 16, whose weights come from the caches
-// after the first).  Weights are widened to bf16, which holds every e4m3 and
-// int8 value exactly; activations stay bf16, and h is carried as the sum of two
-// bf16 values (16 significant bits): the matrix cores have the time for a
-// second product per weight.
+// some of the expert's tokens as the columns of its second (an expert with more
+// tokens makes several units, whose weights come from the caches after the
+// first).  Weights are widened to bf16, which holds every e4m3 and int8 value
+// exactly; activations stay bf16, and h is carried as the sum of two bf16
+// values (16 significant bits), which take two columns of the second product.
 //
 // Every wave streams its own share of the weights through an LDS slot of its
 // own: direct-to-LDS loads fetch whole 128-byte lines (8 rows each; loading
@@ -52,19 +51,20 @@ constexpr int kUpSlot = 2 * kUpRows * BK;
 constexpr int kMaxPairs = kMoeFewTokens * 16;
 
 // Workspace: h as hi bf16 [T * k, Fp], then lo bf16 [T * k, Fp], by the first
-// pair of each (token, expert); Fp = F rounded up to 8.
-__host__ __device__ inline int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
+// pair of each (token, expert); Fp = F rounded up to 128, zeros past F.
+__host__ __device__ inline int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
 
-// The work units: a hit expert and up to 16 of its tokens (kColumns), experts
-// in the order of their first (token, slot) pair.  list[i] = expert | group <<
-// 16 | kAgain if the expert has several; its g-th group holds its 16 g-th to
-// 16 g + 15-th token.  idx[p] = expert of pair p (-1: none here).
-constexpr int kColumns = 16;
+// The work units: a hit expert and up to COLS of its tokens, experts in the
+// order of their first (token, slot) pair.  list[i] = expert | group << 16 |
+// kAgain if the expert has several; its g-th group holds its COLS g-th to COLS
+// g + COLS - 1-th token.  idx[p] = expert of pair p (-1: none here); wt[p], if
+// asked for, its weight.
+constexpr int kUpCols = 16, kDownCols = 8;
 constexpr int kAgain = 1 << 24;
 constexpr int kMaxUnits = kMaxPairs;  // at most one per pair
 
-// At most 64 pairs (and so at most 16 tokens per expert, as long as T <= 16):
-// every wave finds the units by itself, in registers, lane p holding pair p.
+// At most 64 pairs of at most COLS tokens (so every expert is one unit): every
+// wave finds the units by itself, in registers, lane p holding pair p.
 // Lanes naming the same expert are found with ballots over the bits of the
 // expert; the lowest of them leads.
 __device__ __forceinline__ int find_units_wave(const MoeFewArgs& a, int* idx, int* list, float* wt) {
@@ -93,9 +93,9 @@ __device__ __forceinline__ int find_units_wave(const MoeFewArgs& a, int* idx, in
 }
 
 // Any number of pairs, by the whole workgroup; table: 2 E ints of scratch.
-template <int THREADS>
+template <int THREADS, int COLS>
 __device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* idx, int* list, float* wt,
-                                          int (*wave_n)[4]) {
+                                          int* wave_n) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int P = a.T * a.k;
   int* lead = table;             // [E]: first pair of each expert
@@ -125,18 +125,19 @@ __device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* 
   for (int base = 0; base < P; base += THREADS) {
     const int p = base + threadIdx.x;
     const int e = p < P ? idx[p] : -1;
-    const int groups = e >= 0 && lead[e] == p ? (count[e] + kColumns - 1) / kColumns : 0;
-    int below = 0;
+    const int groups = e >= 0 && lead[e] == p ? (count[e] + COLS - 1) / COLS : 0;
+    int below = 0, sum = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kMoeFewTokens / COLS; ++g) {
       const uint64_t m = __ballot(groups > g);
       below += __popcll(m & ((1ull << lane) - 1));
-      if (lane == 0) wave_n[wave][g] = __popcll(m);
+      sum += __popcll(m);
     }
+    if (lane == 0) wave_n[wave] = sum;
     __syncthreads();
     int at = total + below;
     for (int w = 0; w < THREADS / 64; ++w) {
-      const int n = wave_n[w][0] + wave_n[w][1] + wave_n[w][2] + wave_n[w][3];
+      const int n = wave_n[w];
       at += w < wave ? n : 0;
       total += n;
     }
@@ -148,10 +149,11 @@ __device__ __forceinline__ int find_units(const MoeFewArgs& a, int* table, int* 
 
 // A unit's columns.  Lane t: the first of token t's slots that names the expert
 // (first, -1: none or another group) and the token's column (rank); lane c
-// (modulo 16) holds column c's token and pair, cols says how many there are.
+// (modulo COLS) holds column c's token and pair, cols says how many there are.
 struct Unit {
   int e, first, rank, cols, tok, pair;
 
+  template <int COLS>
   __device__ __forceinline__ void set(const MoeFewArgs& a, const int* idx, int entry, int* scratch) {
     const int lane = threadIdx.x & 63;
     e = __builtin_amdgcn_readfirstlane(entry & 0xffff);
@@ -160,19 +162,18 @@ struct Unit {
     if (lane < a.T)
       for (int j = a.k - 1; j >= 0; --j) first = idx[lane * a.k + j] == e ? j : first;
     const uint64_t all = __ballot(first >= 0);
-    rank = __popcll(all & ((1ull << lane) - 1)) - kColumns * g;
-    if (rank < 0 || rank >= kColumns) first = -1;
-    cols = __popcll(all) - kColumns * g;
-    cols = cols < kColumns ? cols : kColumns;
+    rank = __popcll(all & ((1ull << lane) - 1)) - COLS * g;
+    if (rank < 0 || rank >= COLS) first = -1;
+    cols = __popcll(all) - COLS * g;
+    cols = cols < COLS ? cols : COLS;
     if (first >= 0) scratch[rank] = (lane * a.k + first) << 8 | lane;
     __builtin_amdgcn_wave_barrier();
-    const int v = scratch[lane & 15];
-    const bool on = (lane & 15) < cols;
+    const int v = scratch[lane & (COLS - 1)];
+    const bool on = (lane & (COLS - 1)) < cols;
     tok = on ? v & 255 : 0;
     pair = on ? v >> 8 : 0;
     __builtin_amdgcn_wave_barrier();
   }
-  __device__ __forceinline__ bool on() const { return (int)(threadIdx.x & 15) < cols; }
 };
 
 // 16 bytes from element k (of SZ bytes) of a row of K elements, at any address;
@@ -330,24 +331,24 @@ template <bool I8, bool DMA>
 __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(MoeFewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kUpWaves * kUpSlot];
   __shared__ int idx[kMaxPairs], list[kMaxUnits];
-  __shared__ int wave_n[kUpWaves][4], scratch[kUpWaves][kColumns];
+  __shared__ int wave_n[kUpWaves], scratch[kUpWaves][kUpCols];
   static_assert(kMaxRouteExperts * 8 <= kUpWaves * kUpSlot, "the table of experts lies in the ring");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int fr = lane & 15, fg = lane >> 4;
   int *my_idx = idx, *my_list = list;
   int units;
-  if (a.T * a.k <= 64 && a.T <= kColumns) {
+  if (a.T * a.k <= 64 && a.T <= kUpCols) {
     my_idx = idx + 64 * wave;
     my_list = list + 64 * wave;
     units = find_units_wave(a, my_idx, my_list, nullptr);
   } else {
-    units = find_units<64 * kUpWaves>(a, reinterpret_cast<int*>(ring), idx, list, nullptr, wave_n);
+    units = find_units<64 * kUpWaves, kUpCols>(a, reinterpret_cast<int*>(ring), idx, list, nullptr, wave_n);
   }
   units = __builtin_amdgcn_readfirstlane(units);
   const int nkb = (int)((a.D + BK - 1) / BK);
   const uint32_t tiles = (uint32_t)((a.F + kUpRows - 1) / kUpRows);
-  const int64_t tasks = (int64_t)units * tiles, Fp = pad8(a.F);
+  const int64_t tasks = (int64_t)units * tiles, Fp = pad128(a.F);
   uint16_t* hi = static_cast<uint16_t*>(a.work);
   uint16_t* lo = hi + (int64_t)a.T * a.k * Fp;
   // KS waves per task, up to all of them: the more share a task, the longer the
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
     const int64_t f0 = live ? (int64_t)((uint32_t)task - ui * tiles) * kUpRows : 0;
     const int entry = __builtin_amdgcn_readfirstlane(my_list[ui]);
     Unit u;
-    u.set(a, my_idx, entry, scratch[wave]);
+    u.set<kUpCols>(a, my_idx, entry, scratch[wave]);
     const int e = u.e;
     v4f acc[4];
 #pragma unroll
@@ -383,14 +384,11 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) st.issue(i, i < 2 ? w1 : w3, i & 1, a.ldw13, (uint32_t)kb * BK, (uint32_t)a.D);
       };
-      // x of the lane's column, elements of K-block kb
-      const bool on = u.on();
+      // x of the lane's column, elements of K-block kb (a lane past the unit's
+      // columns reads token 0, and its column is never used)
       const uint8_t* xrow = reinterpret_cast<const uint8_t*>(a.x + (int64_t)u.tok * a.ldx);
       u32x4 b[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) b[s] = u32x4{0u, 0u, 0u, 0u};
       auto columns = [&](int kb) __attribute__((always_inline)) {
-        if (!on) return;
         const int64_t k = (int64_t)kb * BK + 32 * fg;
         if ((int64_t)(kb + 1) * BK <= a.D) {
 #pragma unroll
@@ -449,7 +447,7 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
       for (int v = 0; v < 4; ++v) red[16 * i + 4 * fg + v][fr] = acc[i][v];
     __syncthreads();
     const float* group = reinterpret_cast<const float*>(ring + (wave - sub) * kUpSlot);
-    for (int q = sub * 64 + lane; q < kUpRows * kColumns; q += ks * 64) {
+    for (int q = sub * 64 + lane; q < kUpRows * kUpCols; q += ks * 64) {
       const int r = q & (kUpRows - 1), c = q >> 5;
       const int pair = __shfl(u.pair, c);
       const int64_t f = f0 + r;
@@ -470,18 +468,29 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
       hi[(int64_t)pair * Fp + f] = vh;
       lo[(int64_t)pair * Fp + f] = vl;
     }
+    // the last task of a unit clears its rows from there to Fp
+    const int rest = live && f0 + kUpRows >= a.F ? (int)(Fp - f0) - kUpRows : 0;
+    for (int q = sub * 64 + lane; q < rest * kUpCols; q += ks * 64) {
+      const int c = q & (kUpCols - 1);
+      const int pair = scratch[wave][c] >> 8;
+      if (c >= u.cols) continue;
+      const int64_t at = (int64_t)pair * Fp + f0 + kUpRows + (q >> 4);
+      hi[at] = 0;
+      lo[at] = 0;
+    }
     __syncthreads();
   }
 }
 
-// RT row tiles of 16 output columns per workgroup; CT column tiles of 16 tokens.
+// `rows` output columns per workgroup in RT row tiles of 16 (rows a multiple of
+// 4); CT column tiles of 16 tokens.
 template <bool I8, int CT, int RT, bool DMA>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArgs a) {
+__global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArgs a, int wg_rows) {
   constexpr int SLOT = RT * 16 * BK;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kDownWaves * SLOT];
   __shared__ int idx[kMaxPairs], list[kMaxUnits];
   __shared__ float wt[kMaxPairs];
-  __shared__ int wave_n[kDownWaves][4], scratch[kDownWaves][kColumns];
+  __shared__ int wave_n[kDownWaves], scratch[kDownWaves][kDownCols];
   static_assert(kMaxRouteExperts * 8 <= kDownWaves * SLOT, "the table of experts lies in the ring");
   static_assert(64 * kDownWaves <= kMaxPairs, "a list of 64 per wave");
   constexpr int CJ = CT < 2 ? CT : 2;  // column tiles joined at a time
@@ -493,23 +502,23 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
   float* my_wt = wt;
   int units = 0;  // F = 0: the up kernel did not run, and the output is zero
   if (a.F > 0) {
-    if (a.T * a.k <= 64 && a.T <= kColumns) {
+    if (a.T * a.k <= 64 && a.T <= kDownCols) {
       my_idx = idx + 64 * wave;
       my_list = list + 64 * wave;
       my_wt = wt + 64 * wave;
       units = find_units_wave(a, my_idx, my_list, my_wt);
     } else {
-      units = find_units<64 * kDownWaves>(a, reinterpret_cast<int*>(ring), idx, list, wt, wave_n);
+      units = find_units<64 * kDownWaves, kDownCols>(a, reinterpret_cast<int*>(ring), idx, list, wt, wave_n);
     }
   }
   units = __builtin_amdgcn_readfirstlane(units);
-  const int64_t d0 = (int64_t)blockIdx.x * (16 * RT), Fp = pad8(a.F);
-  const int rows = (int)(a.D - d0 < 16 * RT ? a.D - d0 : 16 * RT);
+  const int64_t d0 = (int64_t)blockIdx.x * wg_rows, Fp = pad128(a.F);
+  const int rows = (int)(a.D - d0 < wg_rows ? a.D - d0 : wg_rows);
   const uint16_t* hi = static_cast<const uint16_t*>(a.work);
   const int per = (int)((a.F + BK - 1) / BK);
-  const int64_t steps = (int64_t)units * per;
-  const int64_t s0 = steps * wave / kDownWaves, s1 = steps * (wave + 1) / kDownWaves;
-  const int64_t kbd = (a.D + BK - 1) / BK;
+  const int64_t steps = (int64_t)units * per, s0 = steps * wave / kDownWaves;
+  const int n = (int)(steps * (wave + 1) / kDownWaves - s0);  // this wave's steps
+  int at = n > 0 ? (int)(s0 / per) : 0, kp = (int)(s0 - (int64_t)at * per);
 
   Stream<RT, DMA> st;
   st.init(ring + wave * SLOT, a.ldw2);
@@ -524,32 +533,37 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
   auto panel = [&](int entry) __attribute__((always_inline)) {
     w2.set(a.w2 + ((int64_t)(entry & 0xffff) * a.D + d0) * a.ldw2, a.ldw2, rows, 16 * RT, a.F, entry);
   };
-  auto issue = [&](int p) __attribute__((always_inline)) {
+  auto issue = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) st.issue(i, w2, i, a.ldw2, (uint32_t)p * BK, (uint32_t)a.F);
+    for (int i = 0; i < RT; ++i) st.issue(i, w2, i, a.ldw2, (uint32_t)k * BK, (uint32_t)a.F);
   };
-  u32x4 bh[4], bl[4];
+  // Columns 0 .. 7 hold the high parts of the unit's rows of h, columns 8 .. 15
+  // the low parts, so one product serves both (with a product each, of 16
+  // columns, the matrix and vector instructions held the stream up: 16 tokens
+  // 208 us against 180).  A lane past the unit's columns reads some row of h;
+  // what its column makes of it is never used.
+  u32x4 b[4];
+  float sca = 1.0f, scb = 1.0f;  // the step's block scales, of this block of rows and the next
+  const int64_t kbd = (a.D + BK - 1) / BK;
+  const int cut = (int)(BK - (d0 & (BK - 1)));  // first row of the next block
   Unit u;
-  const int64_t to_lo = (int64_t)a.T * a.k * Fp;
-  auto columns = [&](int p) __attribute__((always_inline)) {
-    const uint16_t* h = hi + (int64_t)u.pair * Fp + p * BK + 32 * fg;
-    const int left = (int)(a.F - (int64_t)p * BK) - 32 * fg;  // of the row, from this lane's elements
+  const uint16_t* hp = nullptr;
+  const float *spa = nullptr, *spb = nullptr;
+  auto enter = [&](int entry, int k) __attribute__((always_inline)) {
+    u.template set<kDownCols>(a, my_idx, entry, scratch[wave]);
+    hp = hi + (fr < kDownCols ? 0 : (int64_t)a.T * a.k * Fp) + (int64_t)u.pair * Fp + (int64_t)k * BK + 32 * fg;
+    if constexpr (!I8) {
+      spa = a.s2 + ((int64_t)u.e * kbd + (d0 >> 7)) * a.lds2 + k;
+      spb = a.s2 + ((int64_t)u.e * kbd + ((d0 + rows - 1) >> 7)) * a.lds2 + k;
+    }
+  };
+  auto columns = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) bh[s] = bl[s] = u32x4{0u, 0u, 0u, 0u};
-    if (!u.on()) return;
-    if ((int64_t)(p + 1) * BK <= a.F) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        bh[s] = *reinterpret_cast<const u32x4*>(h + 8 * s);
-        bl[s] = *reinterpret_cast<const u32x4*>(h + to_lo + 8 * s);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (8 * s >= left) continue;
-        bh[s] = *reinterpret_cast<const u32x4*>(h + 8 * s);
-        bl[s] = *reinterpret_cast<const u32x4*>(h + to_lo + 8 * s);
-      }
+    for (int s = 0; s < 4; ++s) b[s] = *reinterpret_cast<const u32x4*>(hp + 8 * s);
+    hp += BK;
+    if constexpr (!I8) {
+      sca = *spa++;
+      scb = *spb++;
     }
   };
   // Add a finished unit's columns to their tokens, times the tokens' weights.
@@ -571,11 +585,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     for (int c = 0; c < CT; ++c) {
       const int has = __shfl(u.first, 16 * c + fr), col = __shfl(u.rank, 16 * c + fr);
       const float wc = __shfl(w, 16 * c + fr);
+      const int from = (lane & 48) | (col & (kDownCols - 1));
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float y = __shfl(acc[i][v], (lane & 48) | (col & 15));
+          const float y = __shfl(acc[i][v], from) + __shfl(acc[i][v], from + kDownCols);
           if (has >= 0) sum[i][c][v] = __builtin_fmaf(y, wc, sum[i][c][v]);
         }
     }
@@ -583,41 +598,39 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(MoeFewArg
     for (int i = 0; i < RT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   };
 
-  int at = per > 0 ? (int)(s0 / per) : 0, kp = (int)(s0 - (int64_t)at * per);
   __syncthreads();  // the table of experts gives way to the ring
-  if (s0 < s1) {
+  if (n > 0) {
     const int entry = __builtin_amdgcn_readfirstlane(my_list[at]);
     panel(entry);
     issue(kp);
-    u.set(a, my_idx, entry, scratch[wave]);
-    columns(kp);
+    enter(entry, kp);
+    columns();
   }
-  for (int64_t s = s0; s < s1; ++s) {
-    const float sc = I8 ? 1.0f : a.s2[((int64_t)u.e * kbd + (d0 >> 7)) * a.lds2 + kp];
-    const bool more = s + 1 < s1, turn = kp + 1 == per;
-    const int kn = turn ? 0 : kp + 1;
+  for (int s = 0; s < n; ++s) {
+    const bool more = s + 1 < n, turn = ++kp == per;
     int entry = 0;
-    if (more && turn) {
-      entry = __builtin_amdgcn_readfirstlane(my_list[at + 1]);
-      panel(entry);
+    if (turn) {
+      kp = 0;
+      ++at;
+      if (more) {
+        entry = __builtin_amdgcn_readfirstlane(my_list[at]);
+        panel(entry);
+      }
     }
     st.take();
-    if (DMA && more) issue(kn);
+    if (DMA && more) issue(kp);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const v4f part = block_product<I8>(st.w[i], bl, block_product<I8>(st.w[i], bh, v4f{0.0f, 0.0f, 0.0f, 0.0f}));
+      const v4f part = block_product<I8>(st.w[i], b, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+      const float sc = 16 * i + 4 * fg < cut ? sca : scb;
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[i][v] = I8 ? acc[i][v] + part[v] : __builtin_fmaf(part[v], sc, acc[i][v]);
     }
     if (turn || !more) leave();
     if (more) {
-      if (!DMA) issue(kn);
-      if (turn) {
-        ++at;
-        u.set(a, my_idx, entry, scratch[wave]);
-      }
-      kp = kn;
-      columns(kp);
+      if (!DMA) issue(kp);
+      if (turn) enter(entry, 0);
+      columns();
     }
   }
   __syncthreads();
@@ -654,14 +667,13 @@ hipError_t launch(const MoeFewArgs& a, hipStream_t stream) {
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
-  const dim3 blk(64 * kDownWaves);
-  // 32 output columns per workgroup read h half as often as 16 (7168 columns:
-  // 73 against 84 us for one token), if that leaves enough workgroups (4096
-  // columns: 128 of them take 78 us, 256 with 16 columns 70)
-  if ((a.D + 31) / 32 * 4 >= 3 * cus)
-    hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 2, DMA>), dim3((unsigned)((a.D + 31) / 32)), blk, 0, stream, a);
-  else
-    hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 1, DMA>), dim3((unsigned)((a.D + 15) / 16)), blk, 0, stream, a);
+  // As many output columns per workgroup as spread them over all CUs, up to 32
+  // (7168 columns: 256 workgroups of 28 rather than 224 of 32).
+  const int64_t want = ((a.D + cus - 1) / cus + 3) / 4 * 4;
+  const int rows = (int)(want < 32 ? want : 32);
+  const dim3 grid((unsigned)((a.D + rows - 1) / rows)), blk(64 * kDownWaves);
+  if (rows > 16) hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 2, DMA>), grid, blk, 0, stream, a, rows);
+  else hipLaunchKernelGGL((moe_few_down_kernel<I8, CT, 1, DMA>), grid, blk, 0, stream, a, rows);
   return hipGetLastError();
 }
 
@@ -683,7 +695,7 @@ hipError_t launch_ct(const MoeFewArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) { return (size_t)(T * k * pad8(F) * 4); }
+size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) { return (size_t)(T * k * pad128(F) * 4); }
 
 hipError_t launch_moe_few(const MoeFewArgs& a, hipStream_t stream) {
   return a.i8 ? launch_ct<true>(a, stream) : launch_ct<false>(a, stream);
