@@ -406,44 +406,52 @@ def moe_combine(yr, indices, weights, token_rows, out=None):
 # ---- int8 linear layer -----------------------------------------------------------------
 
 
-class _on:
-    """Make a tensor's device current for a launch (a no-op when it already is)."""
-
-    def __init__(self, t):
-        self.dev = t.device.index
-        self.prev = None
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.dev:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+def _is_mat(t, dtype, dim=2):
+    """What `_mat` asks for, as one expression for calls whose cost counts."""
+    return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == dim
+            and (t.stride(dim - 1) == 1 or t.numel() == 0))
 
 
-def _same_device(t, **others):
+def _need(t, name, dtype, dim=2):
+    if not _is_mat(t, dtype, dim):
+        _mat(t, name, (dtype,), dim)
+
+
+def _same_device(dev, **others):
     for name, o in others.items():
-        if o.device != t.device:
-            raise Dsfp8Error(f"{name} must be on {t.device}, got {o.device}")
+        if o.get_device() != dev:
+            raise Dsfp8Error(f"{name} must be on device {dev}, got {o.device}")
 
 
 def _vec_f32(t, n, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (n,):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or t.shape != (n,):
         raise Dsfp8Error(f"{name} must be a float32 CUDA tensor of shape ({n},)")
     if n > 1 and t.stride(0) != 1:
         raise Dsfp8Error(f"{name} needs stride 1")
-    return t
 
 
 def _workspace(ws, need, t):
+    """The address and size of the caller's workspace, or of a new one."""
     if ws is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=t.device)
-    if not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != t.device:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=t.device)
+        return ws, ws.data_ptr(), need
+    if not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != t.get_device():
         raise Dsfp8Error(f"workspace must be a contiguous uint8 tensor on {t.device}")
-    return ws
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _launch(name, fn, dev, *args):
+    """Call an entry point on the device's current stream, with that device current."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        _check(name, st)
 
 
 def row_quant_i8(x, out=None):
@@ -457,71 +465,68 @@ def row_quant_i8(x, out=None):
     yo, so = out if out is not None else (None, None)
     y = _out(yo, (M, K), torch.int8, x.device, "y")
     s = _out(so, (M,), torch.float32, x.device, "s")
-    with _on(x):
-        st = _lib.load().dsfp8_row_quant_i8(x.data_ptr(), 0 if x.dtype == torch.float32 else 1, M, K, _ld(x),
-                                            y.data_ptr(), _ld(y), s.data_ptr(), _stream(x))
-    _check("row_quant_i8", st)
+    _launch("row_quant_i8", _lib.load().dsfp8_row_quant_i8, x.get_device(), x.data_ptr(),
+            0 if x.dtype == torch.float32 else 1, M, K, _ld(x), y.data_ptr(), _ld(y), s.data_ptr())
     return y, s
+
+
+def _gate_pair(g, u):
+    _need(g, "g", torch.bfloat16)
+    _need(u, "u", torch.bfloat16)
+    if g.shape != u.shape:
+        raise Dsfp8Error(f"g and u must have the same shape, got {tuple(g.shape)} and {tuple(u.shape)}")
+    _same_device(g.get_device(), u=u)
 
 
 def silu_mul_row_quant_i8(g, u, out=None):
     """``row_quant_i8(SiLU(g) * u)`` in one pass over bf16 ``g`` and ``u`` (the gate
     is evaluated in fp32 and not rounded before the quantisation)."""
-    _mat(g, "g", (torch.bfloat16,))
-    _mat(u, "u", (torch.bfloat16,))
-    if g.shape != u.shape:
-        raise Dsfp8Error(f"g and u must have the same shape, got {tuple(g.shape)} and {tuple(u.shape)}")
-    _same_device(g, u=u)
+    _gate_pair(g, u)
     M, I = g.shape
     yo, so = out if out is not None else (None, None)
     y = _out(yo, (M, I), torch.int8, g.device, "y")
     s = _out(so, (M,), torch.float32, g.device, "s")
-    with _on(g):
-        st = _lib.load().dsfp8_silu_mul_row_quant_i8(g.data_ptr(), _ld(g), u.data_ptr(), _ld(u), M, I, y.data_ptr(),
-                                                     _ld(y), s.data_ptr(), _stream(g))
-    _check("silu_mul_row_quant_i8", st)
+    _launch("silu_mul_row_quant_i8", _lib.load().dsfp8_silu_mul_row_quant_i8, g.get_device(), g.data_ptr(), _ld(g),
+            u.data_ptr(), _ld(u), M, I, y.data_ptr(), _ld(y), s.data_ptr())
     return y, s
 
 
 def gemm_i8(a, a_s, b, b_s, out=None):
     """bf16 ``C [M, N] = (A W^T) * a_s[:, None] * b_s`` of int8 ``A [M, K]`` and
     ``W [N, K]``, summed exactly; ``a_s [M]`` and ``b_s [N]`` are float32."""
-    _mat(a, "a", (torch.int8,))
-    _mat(b, "b", (torch.int8,))
+    _need(a, "a", torch.int8)
+    _need(b, "b", torch.int8)
     M, K = a.shape
     N, K2 = b.shape
     if K2 != K:
         raise Dsfp8Error(f"a and b disagree on K: {K} vs {K2}")
     _vec_f32(a_s, M, "a_s")
     _vec_f32(b_s, N, "b_s")
-    _same_device(a, a_s=a_s, b=b, b_s=b_s)
+    dev = a.get_device()
+    _same_device(dev, a_s=a_s, b=b, b_s=b_s)
     c = _out(out, (M, N), torch.bfloat16, a.device, "out")
-    with _on(a):
-        st = _lib.load().dsfp8_gemm_i8(a.data_ptr(), _ld(a), a_s.data_ptr(), b.data_ptr(), _ld(b), b_s.data_ptr(),
-                                       c.data_ptr(), _ld(c), M, N, K, _stream(a))
-    _check("gemm_i8", st)
+    _launch("gemm_i8", _lib.load().dsfp8_gemm_i8, dev, a.data_ptr(), _ld(a), a_s.data_ptr(), b.data_ptr(), _ld(b),
+            b_s.data_ptr(), c.data_ptr(), _ld(c), M, N, K)
     return c
 
 
 def _linear_i8(name, x, u, w, w_s, out, workspace):
-    _mat(w, "w", (torch.int8,))
+    _need(w, "w", torch.int8)
     M, K = x.shape
     N, K2 = w.shape
     if K2 != K:
         raise Dsfp8Error(f"the input and w disagree on K: {K} vs {K2}")
     _vec_f32(w_s, N, "w_s")
-    _same_device(x, w=w, w_s=w_s)
+    dev = x.get_device()
+    _same_device(dev, w=w, w_s=w_s)
     lib = _lib.load()
-    c = _out(out, (M, N), torch.bfloat16, x.device, "out")
-    ws = _workspace(workspace, lib.dsfp8_linear_i8_workspace_bytes(M, K), x)
-    tail = (w.data_ptr(), _ld(w), w_s.data_ptr(), c.data_ptr(), _ld(c), M, N, K, ws.data_ptr(), ws.numel(),
-            _stream(x))
-    with _on(x):
-        if u is None:
-            st = lib.dsfp8_linear_i8(x.data_ptr(), _ld(x), *tail)
-        else:
-            st = lib.dsfp8_silu_mul_linear_i8(x.data_ptr(), _ld(x), u.data_ptr(), _ld(u), *tail)
-    _check(name, st)
+    c = x.new_empty((M, N)) if out is None else _out(out, (M, N), torch.bfloat16, x.device, "out")
+    ws, wp, wn = _workspace(workspace, lib.dsfp8_linear_i8_workspace_bytes(M, N, K, 0 if u is None else 1), x)
+    tail = (w.data_ptr(), _ld(w), w_s.data_ptr(), c.data_ptr(), _ld(c), M, N, K, wp, wn)
+    if u is None:
+        _launch(name, lib.dsfp8_linear_i8, dev, x.data_ptr(), _ld(x), *tail)
+    else:
+        _launch(name, lib.dsfp8_silu_mul_linear_i8, dev, x.data_ptr(), _ld(x), u.data_ptr(), _ld(u), *tail)
     return c
 
 
@@ -529,18 +534,14 @@ def linear_i8(x, w, w_s, out=None, workspace=None):
     """bf16 ``[M, N]``: ``gemm_i8(*row_quant_i8(x), w, w_s)`` in one call, for bf16
     ``x [M, K]`` and an int8 weight ``w [N, K]`` with a float32 scale per output
     channel, ``w_s [N]`` (as ``row_quant_i8`` of the real weight gives them)."""
-    _mat(x, "x", (torch.bfloat16,))
+    _need(x, "x", torch.bfloat16)
     return _linear_i8("linear_i8", x, None, w, w_s, out, workspace)
 
 
 def silu_mul_linear_i8(g, u, w, w_s, out=None, workspace=None):
     """The gated form of :func:`linear_i8`, the down-projection of a feed-forward
     layer: ``gemm_i8(*silu_mul_row_quant_i8(g, u), w, w_s)`` in one call."""
-    _mat(g, "g", (torch.bfloat16,))
-    _mat(u, "u", (torch.bfloat16,))
-    if g.shape != u.shape:
-        raise Dsfp8Error(f"g and u must have the same shape, got {tuple(g.shape)} and {tuple(u.shape)}")
-    _same_device(g, u=u)
+    _gate_pair(g, u)
     return _linear_i8("silu_mul_linear_i8", g, u, w, w_s, out, workspace)
 
 
@@ -560,39 +561,44 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     [E, ceil(2F/128), ceil(D/128)]`` and ``w2_s [E, ceil(D/128), ceil(F/128)]``, or
     int8 with channel scales ``w13_s [E, 2F]`` and ``w2_s [E, D]``; ``indices``
     int32 and ``weights`` bf16 ``[T, k]``.  Activations are not quantised."""
-    _mat(x, "x", (torch.bfloat16,))
-    w13, w2 = _bytes(w13), _bytes(w2)
-    _mat(w13, "w13", (torch.uint8, torch.int8), dim=3)
-    _mat(w2, "w2", (w13.dtype,), dim=3)
-    indices = _int32_mat(indices, "indices")
-    _mat(weights, "weights", (torch.bfloat16,))
+    _need(x, "x", torch.bfloat16)
+    _mat(w13, "w13", (torch.uint8, torch.int8, torch.float8_e4m3fn), dim=3)
     i8 = w13.dtype == torch.int8
+    if not i8:
+        w13, w2 = _bytes(w13), _bytes(w2)
+    _need(w2, "w2", w13.dtype, 3)
+    if not _is_mat(indices, torch.int32):
+        _int32_mat(indices, "indices")
+    _need(weights, "weights", torch.bfloat16)
     T, D = x.shape
     E, F2, D2 = w13.shape
     F = F2 // 2
-    if D2 != D or F2 % 2 or tuple(w2.shape) != (E, D, F):
+    if D2 != D or F2 % 2 or w2.shape != (E, D, F):
         raise Dsfp8Error(f"w13 must be [E, 2F, {D}] and w2 [E, {D}, F], got {tuple(w13.shape)} and {tuple(w2.shape)}")
     k = indices.shape[1]
-    if indices.shape[0] != T or tuple(weights.shape) != (T, k):
+    if indices.shape[0] != T or weights.shape != (T, k):
         raise Dsfp8Error(f"indices and weights must be [{T}, k]")
-    _mat(w13_s, "w13_s", (torch.float32,), dim=2 if i8 else 3)
-    _mat(w2_s, "w2_s", (torch.float32,), dim=2 if i8 else 3)
+    _need(w13_s, "w13_s", torch.float32, 2 if i8 else 3)
+    _need(w2_s, "w2_s", torch.float32, 2 if i8 else 3)
     want13 = (E, F2) if i8 else (E, kblocks(F2), kblocks(D))
     want2 = (E, D) if i8 else (E, kblocks(D), kblocks(F))
-    if tuple(w13_s.shape) != want13 or tuple(w2_s.shape) != want2:
+    if w13_s.shape != want13 or w2_s.shape != want2:
         raise Dsfp8Error(f"scales must be w13_s {want13} and w2_s {want2}, got {tuple(w13_s.shape)} and "
                          f"{tuple(w2_s.shape)}")
-    for name, t in (("w13", w13), ("w2", w2)) + (() if i8 else (("w13_s", w13_s), ("w2_s", w2_s))):
-        if t.numel() > 0 and E > 1 and t.stride(0) != t.shape[1] * t.stride(1):
-            raise Dsfp8Error(f"{name}: experts must follow each other row by row")
-    _same_device(x, w13=w13, w13_s=w13_s, w2=w2, w2_s=w2_s, indices=indices, weights=weights)
+    if E > 1:
+        for name, t in (("w13", w13), ("w2", w2)) if i8 else (("w13", w13), ("w2", w2), ("w13_s", w13_s),
+                                                              ("w2_s", w2_s)):
+            st = t.stride()
+            if st[0] != t.shape[1] * st[1] and t.numel() > 0:
+                raise Dsfp8Error(f"{name}: experts must follow each other row by row")
+    dev = x.get_device()
+    if not (w13.get_device() == w2.get_device() == w13_s.get_device() == w2_s.get_device() == indices.get_device()
+            == weights.get_device() == dev):
+        _same_device(dev, w13=w13, w13_s=w13_s, w2=w2, w2_s=w2_s, indices=indices, weights=weights)
     lib = _lib.load()
-    out = _out(out, (T, D), torch.bfloat16, x.device, "out")
-    ws = _workspace(workspace, lib.dsfp8_moe_few_workspace_bytes(T, k, F), x)
-    with _on(x):
-        st = lib.dsfp8_moe_few(
-            x.data_ptr(), _ld(x), w13.data_ptr(), _ld(w13), w13_s.data_ptr(), _ld(w13_s), w2.data_ptr(), _ld(w2),
-            w2_s.data_ptr(), _ld(w2_s), 1 if i8 else 0, indices.data_ptr(), _ld(indices), weights.data_ptr(),
-            _ld(weights), T, k, E, D, F, out.data_ptr(), _ld(out), ws.data_ptr(), ws.numel(), _stream(x))
-    _check("moe_few", st)
+    out = x.new_empty((T, D)) if out is None else _out(out, (T, D), torch.bfloat16, x.device, "out")
+    ws, wp, wn = _workspace(workspace, lib.dsfp8_moe_few_workspace_bytes(T, k, F), x)
+    _launch("moe_few", lib.dsfp8_moe_few, dev, x.data_ptr(), _ld(x), w13.data_ptr(), _ld(w13), w13_s.data_ptr(),
+            _ld(w13_s), w2.data_ptr(), _ld(w2), w2_s.data_ptr(), _ld(w2_s), 1 if i8 else 0, indices.data_ptr(),
+            _ld(indices), weights.data_ptr(), _ld(weights), T, k, E, D, F, out.data_ptr(), _ld(out), wp, wn)
     return out

@@ -583,18 +583,23 @@ dsfp8_status linear_i8(const void* x, int64_t ldx, const void* u, int64_t ldu, c
   if (!dim_ok(M) || !dim_ok(N) || K < 0 || K > kMaxI8K) return DSFP8_ERR_SHAPE;
   DSFP8_TRY(check_mat(x, M, K, ldx, 2));
   if (u != nullptr) DSFP8_TRY(check_mat(u, M, K, ldu, 2));
-  if (workspace_bytes < dsfp8_linear_i8_workspace_bytes(M, K)) return DSFP8_ERR_WORKSPACE;
-  if (workspace == nullptr && M > 0) return DSFP8_ERR_NULL;
+  const size_t need = dsfp8_linear_i8_workspace_bytes(M, N, K, u != nullptr);
+  if (workspace_bytes < need) return DSFP8_ERR_WORKSPACE;
+  if (workspace == nullptr && need > 0) return DSFP8_ERR_NULL;
   if (!al(workspace, 16)) return DSFP8_ERR_ALIGN;
+  const bool fused = dsfp8::linear_i8_fused(M, N, K, u != nullptr);
   const int64_t ldy = pad16(K);
   int8_t* y = static_cast<int8_t*>(workspace);
-  float* s = reinterpret_cast<float*>(y + M * ldy);
+  float* s = reinterpret_cast<float*>(y + (fused ? 0 : M * ldy));
   dsfp8::GemmI8Args g;
-  DSFP8_TRY(gemm_i8_args(y, ldy, s, B, ldb, b_s, C, ldc, M, N, K, g));
+  DSFP8_TRY(gemm_i8_args(y, ldy, s, B, ldb, b_s, C, ldc, fused ? 0 : M, N, K, g));
+  DSFP8_TRY(check_mat(C, M, N, ldc, 2));
+  g.M = M;
   dsfp8::RowQuantArgs q;
-  DSFP8_TRY(row_quant_args(x, false, ldx, u, ldu, M, K, y, ldy, s, q));
+  DSFP8_TRY(row_quant_args(x, false, ldx, u, ldu, fused ? 0 : M, K, y, ldy, s, q));
+  q.M = M;
   if (M == 0 || N == 0) return DSFP8_OK;
-  if (dsfp8::linear_i8_fused(g, q)) return launched(dsfp8::launch_linear_i8_fused(g, q, stream));
+  if (fused) return launched(dsfp8::launch_linear_i8_fused(g, q, stream));
   const dsfp8_status st = launched(dsfp8::launch_row_quant_i8(q, stream));
   return st == DSFP8_OK ? launched(dsfp8::launch_gemm_i8(g, stream)) : st;
 }
@@ -627,8 +632,9 @@ dsfp8_status dsfp8_gemm_i8(const void* A, int64_t lda, const float* a_s, const v
   return launched(dsfp8::launch_gemm_i8(a, stream));
 }
 
-size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t K) {
-  if (!dim_ok(M) || K < 0 || K > kMaxI8K) return 0;
+size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated) {
+  if (!dim_ok(M) || !dim_ok(N) || K < 0 || K > kMaxI8K) return 0;
+  if (dsfp8::linear_i8_fused(M, N, K, gated != 0)) return 0;
   return (size_t)(M * pad16(K) + 4 * M);
 }
 
@@ -672,7 +678,7 @@ dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx, const void* W13, int64_t 
   DSFP8_TRY(check_mat(weights, T, k, ldwt, 2));
   DSFP8_TRY(check_mat(out, T, D, ldo, 2));
   if (workspace_bytes < dsfp8_moe_few_workspace_bytes(T, k, F)) return DSFP8_ERR_WORKSPACE;
-  if (workspace == nullptr && T > 0) return DSFP8_ERR_NULL;
+  if (workspace == nullptr && dsfp8_moe_few_workspace_bytes(T, k, F) > 0) return DSFP8_ERR_NULL;
   if (!al(workspace, 16)) return DSFP8_ERR_ALIGN;
   if (T == 0 || D == 0) return DSFP8_OK;
   dsfp8::MoeFewArgs a{};

@@ -175,9 +175,9 @@ struct MoeFewArgs {
 
 hipError_t launch_row_quant_i8(const RowQuantArgs& a, hipStream_t stream);
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream);
-// Quantisation and product in one launch, where linear_i8_fused says so (the
-// product's A and a_s are then not used).
-bool linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q);
+// Quantisation and product in one launch, where linear_i8_fused says so; the
+// product's A and a_s and the quantiser's y and s are then not used.
+bool linear_i8_fused(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q, hipStream_t stream);
 hipError_t launch_moe_few(const MoeFewArgs& a, hipStream_t stream);
 size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F);

@@ -498,9 +498,11 @@ dsfp8_status dsfp8_gemm_i8(const void* A, int64_t lda, const float* a_s, const v
  *
  *   x (g, u)  bf16 [M, K], row stride ldx (ldg, ldu)    (device, read)
  *   B, b_s, C  as for dsfp8_gemm_i8
- *   workspace  at least dsfp8_linear_i8_workspace_bytes(M, K) bytes, 16-byte
+ *   workspace  at least dsfp8_linear_i8_workspace_bytes bytes, 16-byte
  *            aligned (scratch: the codes and scales of x; needs no
- *            initialisation)                            (device, scratch)
+ *            initialisation); 0 bytes, and NULL, for few rows, whose
+ *            quantisation is part of the product's launch
+ *                                                       (device, scratch)
  * Errors: NULL, SHAPE, LD, ALIGN, WORKSPACE, LAUNCH.
  */
 dsfp8_status dsfp8_linear_i8(const void* x, int64_t ldx, const void* B, int64_t ldb, const float* b_s,
@@ -512,7 +514,8 @@ dsfp8_status dsfp8_silu_mul_linear_i8(const void* g, int64_t ldg, const void* u,
                                       void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
                                       void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t K);
+/* gated: nonzero for dsfp8_silu_mul_linear_i8. */
+size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated);
 
 /*
  * A whole routed-expert layer for a few tokens ([AG] 6.4 / 8.4 with the

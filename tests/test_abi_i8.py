@@ -64,16 +64,20 @@ def test_gemm(lib):
 
 
 def test_linear(lib):
-    need = lib.dsfp8_linear_i8_workspace_bytes(4, 50)
-    assert need == 4 * 64 + 16
-    assert lib.dsfp8_linear_i8_workspace_bytes(-1, 50) == 0
-    assert lib.dsfp8_linear_i8_workspace_bytes(4, 131072) == 0
+    bytes_ = lib.dsfp8_linear_i8_workspace_bytes        # M, N, K, gated
+    need = bytes_(40, 8, 50, 0)
+    assert need == 40 * 64 + 160
+    assert bytes_(-1, 8, 50, 0) == 0 and bytes_(4, -8, 50, 0) == 0 and bytes_(4, 8, 131072, 0) == 0
+    assert bytes_(4, 8, 50, 0) == 0 and bytes_(4, 8, 50, 1) == 0    # one launch: no scratch
+    assert bytes_(16, 8, 1040, 0) == 16 * 1044
+    assert bytes_(4, 8, 8, 0) == 4 * 16 + 16
     f = lib.dsfp8_linear_i8         # x, ldx, B, ldb, b_s, C, ldc, M, N, K, ws, wsb, stream
-    ok = [P, 50, P, 50, P, P, 8, 4, 8, 50, P, need, None]
+    ok = [P, 50, P, 50, P, P, 8, 40, 8, 50, P, need, None]
 
-    def with_(i, v):
+    def with_(i, v, *more):
         a = list(ok)
-        a[i] = v
+        for j, w in ((i, v),) + more:
+            a[j] = w
         return f(*a)
 
     assert with_(0, None) == NULL and with_(2, None) == NULL and with_(4, None) == NULL and with_(5, None) == NULL
@@ -81,11 +85,15 @@ def test_linear(lib):
     assert with_(0, P + 1) == ALIGN and with_(4, P + 2) == ALIGN and with_(5, P + 1) == ALIGN
     assert with_(1, 49) == LD and with_(3, 49) == LD and with_(6, 7) == LD
     assert with_(7, -1) == SHAPE and with_(8, -1) == SHAPE and with_(9, 131072) == SHAPE
+    # few rows: no workspace, the other arguments as ever
+    few = ((7, 4), (10, None), (11, 0))
+    assert with_(0, None, *few) == NULL and with_(2, None, *few) == NULL and with_(5, None, *few) == NULL
+    assert with_(1, 49, *few) == LD and with_(6, 7, *few) == LD and with_(5, P + 1, *few) == ALIGN
     assert f(None, 50, P, 50, P, None, 8, 0, 8, 50, None, 0, None) == OK
     g = lib.dsfp8_silu_mul_linear_i8    # g, ldg, u, ldu, B, ldb, b_s, C, ldc, M, N, K, ws, wsb, stream
-    assert g(P, 50, None, 50, P, 50, P, P, 8, 4, 8, 50, P, need, None) == NULL
-    assert g(P, 50, P, 49, P, 50, P, P, 8, 4, 8, 50, P, need, None) == LD
-    assert g(P, 50, P + 1, 50, P, 50, P, P, 8, 4, 8, 50, P, need, None) == ALIGN
+    assert g(P, 50, None, 50, P, 50, P, P, 8, 40, 8, 50, P, need, None) == NULL
+    assert g(P, 50, P, 49, P, 50, P, P, 8, 40, 8, 50, P, need, None) == LD
+    assert g(P, 50, P + 1, 50, P, 50, P, P, 8, 40, 8, 50, P, need, None) == ALIGN
 
 
 def test_moe_few(lib):

@@ -254,7 +254,7 @@ def test_refusals():
     with pytest.raises(ds.Dsfp8Error):
         ds.linear_i8(x[:, :31], w, s)
     with pytest.raises(ds.Dsfp8Error):
-        ds.linear_i8(x, w, s, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        ds.linear_i8(x.repeat(10, 1), w, s, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ds.Dsfp8Error):
         ds.linear_i8(x.t().contiguous().t(), w, s)
     with pytest.raises(ds.Dsfp8Error):
