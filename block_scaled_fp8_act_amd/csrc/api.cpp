@@ -27,6 +27,7 @@ int device_cu_count() {
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // rows, columns and K below 2^31
+constexpr int64_t kMoeFewMaxDim = (int64_t)1 << 26;  // grids and task numbers of its kernels within 32 bits
 constexpr int64_t kMaxExperts = 65536;
 
 inline int64_t nblk(int64_t n) { return (n + DSFP8_BLOCK - 1) / DSFP8_BLOCK; }
@@ -654,7 +655,7 @@ dsfp8_status dsfp8_silu_mul_linear_i8(const void* g, int64_t ldg, const void* u,
 // ---- routed experts for a few tokens ----------------------------------------------------
 
 size_t dsfp8_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) {
-  if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16 || !dim_ok(F)) return 0;
+  if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16 || F < 0 || F > kMoeFewMaxDim) return 0;
   return dsfp8::moe_few_workspace_bytes(T, k, F);
 }
 
@@ -666,7 +667,7 @@ dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx, const void* W13, int64_t 
   static_assert(DSFP8_MOE_FEW_MAX_TOKENS == dsfp8::kMoeFewTokens, "header and library agree");
   if (T < 0 || T > DSFP8_MOE_FEW_MAX_TOKENS || k < 1 || k > 16) return DSFP8_ERR_SHAPE;
   if (E < 1 || E > dsfp8::kMaxRouteExperts) return DSFP8_ERR_SHAPE;
-  if (!dim_ok(D) || !dim_ok(F) || !dim_ok(2 * F)) return DSFP8_ERR_SHAPE;
+  if (D < 0 || F < 0 || D > kMoeFewMaxDim || F > kMoeFewMaxDim) return DSFP8_ERR_SHAPE;
   if (weight_fmt != DSFP8_WEIGHT_E4M3 && weight_fmt != DSFP8_WEIGHT_I8) return DSFP8_ERR_DTYPE;
   const bool i8 = weight_fmt == DSFP8_WEIGHT_I8;
   DSFP8_TRY(check_mat(x, T, D, ldx, 2));

@@ -549,7 +549,7 @@ struct SplitCfg {
   static constexpr int RING = kSplitWaves * D * SLOT;
   static constexpr int SUM = TM * 16 * FN * 4;
   static constexpr int LDS = RING > SUM ? RING : SUM;
-  static constexpr int CODES = FUSED ? kFusedCodes + 16 * (BK - 16 + 16) : 0;
+  static constexpr int CODES = FUSED ? kFusedCodes + 16 * (BK - 1 + 16) : 0;  // rows padded to whole K-blocks, and 16 bytes
 };
 
 template <class SRC_TAG, int FM, int FN, int D, bool HALF, bool DMA>
@@ -902,7 +902,7 @@ float variant_us(const Variant& v, const GemmI8Args& a, bool dma, int cus) {
 // 4x7168x2048 8.0 against 8.7, but 8x7168x2048 9.4 against 8.8 and 2x18432x7168
 // 30.8 against 29.4).
 bool linear_i8_fused(int64_t M, int64_t N, int64_t K, bool gated) {
-  if (M < 1 || M > 16 || K < 16 || M * K > kFusedCodes) return false;
+  if (M < 1 || M > 16 || K < 16 || M * K > kFusedCodes) return false;  // what the kernel has room for
   const int64_t rounds = ((N + 15) / 16 + 255) / 256;
   return M * K * (gated ? 2 : 1) * (rounds < 1 ? 1 : rounds) <= 16384;
 }

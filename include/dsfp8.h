@@ -548,7 +548,8 @@ size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gate
  *   workspace  at least dsfp8_moe_few_workspace_bytes(T, k, F) bytes, 16-byte
  *            aligned; needs no initialisation               (device, scratch)
  * Limits: T <= DSFP8_MOE_FEW_MAX_TOKENS (more tokens: dsfp8_moe_route and the
- * grouped products), 1 <= k <= 16, 1 <= E <= 4096.  F = 0 writes zeros.
+ * grouped products), 1 <= k <= 16, 1 <= E <= 4096, D and F <= 2^26.  F = 0
+ * writes zeros.
  * Errors: DTYPE (unknown weight_fmt), NULL, SHAPE, LD, ALIGN, WORKSPACE, LAUNCH.
  */
 #define DSFP8_MOE_FEW_MAX_TOKENS 64

@@ -116,6 +116,8 @@ def test_moe_few(lib):
     assert with_((16, 0)) == SHAPE and with_((16, 17)) == SHAPE
     assert with_((17, 0)) == SHAPE and with_((17, 4097)) == SHAPE
     assert with_((18, -1)) == SHAPE and with_((19, 1 << 30)) == SHAPE
+    assert with_((18, (1 << 26) + 1)) == SHAPE and with_((19, (1 << 26) + 1)) == SHAPE
+    assert lib.dsfp8_moe_few_workspace_bytes(T, k, (1 << 26) + 1) == 0
     for i in (0, 2, 4, 6, 8, 11, 13, 20, 22):
         assert with_((i, None)) == NULL, i
     for i in (1, 3, 5, 7, 9, 12, 14, 21):
