@@ -218,8 +218,10 @@ __device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t k, int64_t K)
 // The weight fragment is the instruction's first operand, so a lane's results
 // are runs of four columns of one row.
 //
-// Operands whose rows are not 16-byte aligned go through registers instead
-// (RegLoader): the next K-block's chunks are loaded before the MFMAs of the
+// Operands whose rows are aligned to 4 bytes alone take the same path in loads
+// of 4 bytes (through registers instead, 333x2500x1000 took 11.0 us against 7.7,
+// and 4096x7168x2052 179 against 90).  All others go through registers
+// (I8RegLoader): the next K-block's chunks are loaded before the MFMAs of the
 // current one and written to the other stage after them.
 
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -243,6 +245,7 @@ struct I8Cfg {
 
 template <class CF>
 struct I8Loader {
+  static constexpr int LOADS = CF::LOADS;
   i32x4 rsA, rsB;
   uint32_t off[CF::LOADS];
   uint32_t kc;  // byte within the K-block of every load's chunk (a wave's rows agree modulo 16)
@@ -278,8 +281,50 @@ struct I8Loader {
   }
 };
 
+// The same with four bytes per lane, for rows that are only 4-byte aligned (K a
+// multiple of 4): a load fetches two rows.  A row past the matrix lies past the
+// descriptor's end by itself.
+template <class CF>
+struct I8Loader4 {
+  static constexpr int A_INSTR = 4 * CF::A_INSTR, LOADS = 4 * CF::LOADS;
+  static_assert(LOADS * (CF::STAGES - 2) < 64, "the waits of the K loop");
+  i32x4 rsA, rsB;
+  uint32_t offA, offB, stepA, stepB;  // of the wave's first row, and from load to load
+  uint32_t kc;
+  uint32_t lds0;
+  uint32_t K;
+
+  __device__ __forceinline__ void init(const GemmI8Args& p, int64_t m0, int64_t n0, uint8_t* smem) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    K = (uint32_t)p.K;
+    const int64_t ra = p.M - m0 < CF::BM ? p.M - m0 : CF::BM, rb = p.N - n0 < CF::BN ? p.N - n0 : CF::BN;
+    rsA = make_rsrc(p.A + m0 * p.lda, (uint32_t)((ra - 1) * p.lda + p.K));
+    rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
+    const int r = 2 * wave + (lane >> 5);
+    kc = (uint32_t)(((lane & 31) >> 2) ^ swz_key(r)) * 16 + 4 * (lane & 3);
+    offA = (uint32_t)(r * p.lda);
+    offB = (uint32_t)(r * p.ldb);
+    stepA = (uint32_t)(2 * CF::NW * p.lda);
+    stepB = (uint32_t)(2 * CF::NW * p.ldb);
+    lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem)) + (uint32_t)wave * 256;
+  }
+
+  template <bool>
+  __device__ __forceinline__ void issue(int n, int kb, int stage) const {
+    static_assert(CF::NW == 4 || CF::NW == 8, "a load's rows and the next's differ by 8 or 16");
+    const bool a = n < A_INSTR;
+    const int i = a ? n : n - A_INSTR;
+    const uint32_t kbyte = (uint32_t)kb * BK, k = kc ^ (CF::NW == 4 ? 16u * (i & 1) : 0u);
+    const uint32_t off = a ? offA + (uint32_t)i * stepA : offB + (uint32_t)i * stepB;
+    const uint32_t at = lds0 + (uint32_t)(stage * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) + i * CF::NW * 256);
+    dma_b32(a ? rsA : rsB, at, kbyte + k < K ? off + k : kOob, kbyte);
+  }
+};
+
 template <class CF>
 struct I8RegLoader {
+  static constexpr int LOADS = CF::LOADS;
   const int8_t* row[CF::LOADS];
   u32x4 v[CF::LOADS];
   uint32_t at[CF::LOADS];
@@ -358,23 +403,23 @@ __device__ __forceinline__ void i8_block(const uint8_t* stage, const I8Frag<CF>&
 }
 
 // The K loop of one tile; K-blocks 0 .. STAGES - 2 are already on their way.
-template <class CF, bool KFULL>
-__device__ __forceinline__ void i8_k_loop(const I8Loader<CF>& ld, const I8Frag<CF>& f, int nkb, const uint8_t* smem,
+template <class CF, bool KFULL, class LD>
+__device__ __forceinline__ void i8_k_loop(const LD& ld, const I8Frag<CF>& f, int nkb, const uint8_t* smem,
                                           v16i (&acc)[CF::TM][CF::TN]) {
-  constexpr int PER = (CF::LOADS + 4 * CF::TM - 1) / (4 * CF::TM);
+  constexpr int PER = (LD::LOADS + 4 * CF::TM - 1) / (4 * CF::TM);
   for (int kb = 0; kb < nkb; ++kb) {
     // Of the stages issued so far, only those behind K-block kb may be missing.
     const int later = nkb - 1 - kb < CF::STAGES - 2 ? nkb - 1 - kb : CF::STAGES - 2;
     if (kb == 0) wait_vmcnt<0>();  // and the scales, and the previous tile's stores
-    else if (CF::STAGES >= 4 && later >= 2) wait_vmcnt<CF::LOADS * (CF::STAGES >= 4 ? 2 : 0)>();
-    else if (CF::STAGES >= 3 && later >= 1) wait_vmcnt<CF::LOADS * (CF::STAGES >= 3 ? 1 : 0)>();
+    else if (CF::STAGES >= 4 && later >= 2) wait_vmcnt<LD::LOADS * (CF::STAGES >= 4 ? 2 : 0)>();
+    else if (CF::STAGES >= 3 && later >= 1) wait_vmcnt<LD::LOADS * (CF::STAGES >= 3 ? 1 : 0)>();
     else wait_vmcnt<0>();
     __syncthreads();
     const int kn = kb + CF::STAGES - 1;
     i8_block<CF>(smem + (kb % CF::STAGES) * CF::STAGE_BYTES, f, acc, [&](int s) __attribute__((always_inline)) {
       if (kn >= nkb) return;
 #pragma unroll
-      for (int n = s * PER; n < (s + 1) * PER && n < CF::LOADS; ++n)
+      for (int n = s * PER; n < (s + 1) * PER && n < LD::LOADS; ++n)
         ld.template issue<KFULL>(n, kn, kn % CF::STAGES);
     });
   }
@@ -461,7 +506,8 @@ __device__ __forceinline__ void i8_zero(v16i (&acc)[CF::TM][CF::TN]) {
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 }
 
-enum Feed { kDmaFull, kDma, kRegs };  // direct-to-LDS (K a multiple of 128, or of 16), through registers
+// direct-to-LDS (K a multiple of 128, of 16; of 4, in loads of 4 bytes), through registers
+enum Feed { kDmaFull, kDma, kDma4, kRegs };
 
 // One workgroup per tile, or (with direct-to-LDS loads and room in LDS beside
 // the ring for the output's staging) one per CU that walks its XCD's tiles:
@@ -480,13 +526,14 @@ __global__ __launch_bounds__(CF::kThreads) void gemm_i8_kernel(GemmI8Args p) {
   const I8Frag<CF> f;
   int64_t tm, tn, pid = blockIdx.x;
   tile_of(pid, tiles_m, tiles_n, tm, tn);
-  typename std::conditional<FEED == kRegs, I8RegLoader<CF>, I8Loader<CF>>::type ld;
+  typename std::conditional<FEED == kRegs, I8RegLoader<CF>,
+                            typename std::conditional<FEED == kDma4, I8Loader4<CF>, I8Loader<CF>>::type>::type ld;
   auto begin = [&]() __attribute__((always_inline)) {
     ld.init(p, tm * CF::BM, tn * CF::BN, smem);
     if constexpr (FEED != kRegs) {
       for (int s = 0; s < CF::STAGES - 1 && s < nkb; ++s)
 #pragma unroll
-        for (int n = 0; n < CF::LOADS; ++n) ld.template issue<FEED == kDmaFull>(n, s, s);
+        for (int n = 0; n < decltype(ld)::LOADS; ++n) ld.template issue<FEED == kDmaFull>(n, s, s);
     }
   };
   begin();
@@ -545,18 +592,20 @@ struct SplitCfg {
   static constexpr int TM = 16 * FM, TN = HALF ? 8 : 16 * FN;
   static constexpr int AROWS = FUSED ? 0 : TM;
   static constexpr int SLOT = (AROWS + TN) * BK;
-  static constexpr int LOADS = SLOT / 1024;  // 8 rows per load
   static constexpr int RING = kSplitWaves * D * SLOT;
   static constexpr int SUM = TM * 16 * FN * 4;
   static constexpr int LDS = RING > SUM ? RING : SUM;
   static constexpr int CODES = FUSED ? kFusedCodes + 16 * (BK - 1 + 16) : 0;  // rows padded to whole K-blocks, and 16 bytes
 };
 
-template <class SRC_TAG, int FM, int FN, int D, bool HALF, bool DMA>
+template <class SRC_TAG, int FM, int FN, int D, bool HALF, int W>
 __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8Args p, RowQuantArgs x, int code_ld) {
   constexpr bool FUSED = !std::is_void<SRC_TAG>::value;
+  constexpr bool DMA = W > 0;
   static_assert(D <= 3 && (DMA || D == 1), "waits of the ring; one K-block in registers");
   using CF = SplitCfg<FM, FN, D, FUSED, HALF>;
+  constexpr int BYTES = W == 4 ? 256 : 1024, LOADS = CF::SLOT / BYTES;  // of a load: 8 rows, or 2
+  static_assert(LOADS * (D - 1) < 64, "waits of the ring");
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS + CF::CODES];
   __shared__ uint32_t row_top[16];
   const int lane = threadIdx.x & 63;
@@ -568,20 +617,22 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
   const int nkb = (int)((p.K + BK - 1) / BK);
   const uint32_t K = (uint32_t)p.K;
   const int64_t ra = p.M - m0 < CF::TM ? p.M - m0 : CF::TM, rb = p.N - n0 < CF::TN ? p.N - n0 : CF::TN;
-  // Load n fetches rows 8n .. 8n + 7 of the slot (A's rows, then B's); a
-  // lane's chunk depends on the row modulo 16 alone.
+  // Load n fetches rows 8n .. 8n + 7 of the slot (A's rows, then B's; W = 4:
+  // rows 2n, 2n + 1); a lane's chunk depends on the row modulo 16 alone.
   const uint32_t kc[2] = {(uint32_t)((lane & 7) ^ swz_key(lane >> 3)) * 16,
                           (uint32_t)((lane & 7) ^ swz_key(8 + (lane >> 3))) * 16};
   i32x4 rsA, rsB;
-  uint32_t off[CF::LOADS];
-  const int8_t* row[CF::LOADS];
-  u32x4 reg[CF::LOADS];
+  uint32_t off[W == 16 ? LOADS : 1];
+  const int8_t* row[DMA ? 1 : LOADS];
+  u32x4 reg[DMA ? 1 : LOADS];
   if constexpr (DMA) {
     rsA = make_rsrc(p.A + (FUSED ? 0 : m0 * p.lda), FUSED ? 0u : (uint32_t)((ra - 1) * p.lda + p.K));
     rsB = make_rsrc(p.B + n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb + p.K));
   }
+  const uint32_t k4 = (uint32_t)(((lane & 31) >> 2) ^ (lane >> 5)) * 16 + 4 * (lane & 3);
+  const uint32_t off4[2] = {(uint32_t)((lane >> 5) * p.lda), (uint32_t)((lane >> 5) * p.ldb)};
 #pragma unroll
-  for (int n = 0; n < CF::LOADS; ++n) {
+  for (int n = 0; n < LOADS && W != 4; ++n) {
     const bool a = 8 * n < CF::AROWS;
     const int r = 8 * n - (a ? 0 : CF::AROWS) + (lane >> 3);
     if constexpr (DMA) {
@@ -593,20 +644,29 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
   }
   const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem)) + (uint32_t)(wave * D * CF::SLOT);
   auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
-    if constexpr (DMA) {
+    if constexpr (W == 4) {
       const uint32_t kbyte = (uint32_t)kb * BK;
 #pragma unroll
-      for (int n = 0; n < CF::LOADS; ++n)
+      for (int n = 0; n < LOADS; ++n) {
+        const bool a = 2 * n < CF::AROWS;
+        const int r = 2 * n - (a ? 0 : CF::AROWS);  // even; the key of r + 1 is that of r, its lowest bit flipped
+        const uint32_t k = k4 ^ (uint32_t)(16 * swz_key(r)), o = off4[a ? 0 : 1] + (uint32_t)(r * (a ? p.lda : p.ldb)) + k;
+        dma_b32(a ? rsA : rsB, lds0 + (uint32_t)(slot * CF::SLOT + n * 256), kbyte + k < K ? o : kOob, kbyte);
+      }
+    } else if constexpr (DMA) {
+      const uint32_t kbyte = (uint32_t)kb * BK;
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n)
         dma_b128(8 * n < CF::AROWS ? rsA : rsB, lds0 + (uint32_t)(slot * CF::SLOT + n * 1024),
                  kbyte + kc[n & 1] < K ? off[n] : kOob, kbyte);
     } else {
       const int64_t k = (int64_t)kb * BK;
       if (k + BK <= p.K) {
 #pragma unroll
-        for (int n = 0; n < CF::LOADS; ++n) reg[n] = load16<false>(row[n], k + kc[n & 1], p.K);
+        for (int n = 0; n < LOADS; ++n) reg[n] = load16<false>(row[n], k + kc[n & 1], p.K);
       } else {
 #pragma unroll
-        for (int n = 0; n < CF::LOADS; ++n) reg[n] = load16<true>(row[n], k + kc[n & 1], p.K);
+        for (int n = 0; n < LOADS; ++n) reg[n] = load16<true>(row[n], k + kc[n & 1], p.K);
       }
     }
   };
@@ -692,13 +752,13 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
     // loads of the later K-blocks in flight behind this one's
     if constexpr (DMA) {
       const int left = (nkb - 1 - kb) / kSplitWaves;
-      if (D >= 3 && left >= 2) wait_vmcnt<CF::LOADS * (D >= 3 ? 2 : 0)>();
-      else if (D >= 2 && left >= 1) wait_vmcnt<CF::LOADS * (D >= 2 ? 1 : 0)>();
+      if (D >= 3 && left >= 2) wait_vmcnt<LOADS * (D >= 3 ? 2 : 0)>();
+      else if (D >= 2 && left >= 1) wait_vmcnt<LOADS * (D >= 2 ? 1 : 0)>();
       else wait_vmcnt<0>();
       asm volatile("" ::: "memory");
     } else {
 #pragma unroll
-      for (int n = 0; n < CF::LOADS; ++n)
+      for (int n = 0; n < LOADS; ++n)
         *reinterpret_cast<u32x4*>(smem + wave * D * CF::SLOT + n * 1024 + lane * 16) = reg[n];
       __builtin_amdgcn_wave_barrier();
     }
@@ -821,46 +881,59 @@ inline bool aligned16(const void* p, int64_t ld) { return (reinterpret_cast<uint
 // tile's rows within 31-bit offsets.
 inline bool dma_ok(const void* p, int64_t ld, int64_t K) { return K % 16 == 0 && aligned16(p, ld) && ld < (1 << 23); }
 
+// For the same loads of 4 bytes.
+inline bool dma4_ok(const void* p, int64_t ld, int64_t K) {
+  return K % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 3) == 0 && ld % 4 == 0 && ld < (1 << 23);
+}
+
+// Bytes per lane of the operands' direct-to-LDS loads; 0: through registers.
+inline int feed_bytes(const GemmI8Args& a, bool with_a) {
+  if ((!with_a || dma_ok(a.A, a.lda, a.K)) && dma_ok(a.B, a.ldb, a.K)) return 16;
+  return (!with_a || dma4_ok(a.A, a.lda, a.K)) && dma4_ok(a.B, a.ldb, a.K) ? 4 : 0;
+}
+
 template <class CF>
-hipError_t launch_tiles(const GemmI8Args& a, bool dma, hipStream_t stream) {
+hipError_t launch_tiles(const GemmI8Args& a, int w, hipStream_t stream) {
   const int64_t t = ((a.M + CF::BM - 1) / CF::BM) * ((a.N + CF::BN - 1) / CF::BN);
   // the large tile: one workgroup per CU, a multiple of the XCDs
   const int64_t most = CF::BM * CF::BN == 65536 ? (device_cu_count() + kXcds - 1) / kXcds * kXcds : kMaxGrid;
   const dim3 grid((unsigned)(t < most ? t : most)), blk(CF::kThreads);
-  if (!dma) hipLaunchKernelGGL((gemm_i8_kernel<CF, kRegs>), grid, blk, 0, stream, a);
+  if (w == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kRegs>), grid, blk, 0, stream, a);
+  else if (w == 4) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDma4>), grid, blk, 0, stream, a);
   else if (a.K % BK == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDmaFull>), grid, blk, 0, stream, a);
   else hipLaunchKernelGGL((gemm_i8_kernel<CF, kDma>), grid, blk, 0, stream, a);
   return hipGetLastError();
 }
 
-template <class SRC_TAG, int FM, int FN, int D, bool HALF, bool DMA = true>
+template <class SRC_TAG, int FM, int FN, int D, bool HALF, int W = 16>
 hipError_t launch_split_dma(const GemmI8Args& a, const RowQuantArgs& x, int code_ld, hipStream_t stream) {
   using CF = SplitCfg<FM, FN, D, !std::is_void<SRC_TAG>::value, HALF>;
   const int64_t t = (a.M + CF::TM - 1) / CF::TM * ((a.N + CF::TN - 1) / CF::TN);
-  hipLaunchKernelGGL((gemm_i8_split_kernel<SRC_TAG, FM, FN, D, HALF, DMA>), dim3((unsigned)t), dim3(64 * kSplitWaves),
+  hipLaunchKernelGGL((gemm_i8_split_kernel<SRC_TAG, FM, FN, D, HALF, W>), dim3((unsigned)t), dim3(64 * kSplitWaves),
                      0, stream, a, x, code_ld);
   return hipGetLastError();
 }
 
 template <class SRC_TAG, int FM, int FN, int D, bool HALF>
-hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, bool dma, hipStream_t stream) {
+hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, int w, hipStream_t stream) {
   // fused: rows of codes 16 bytes apart modulo the LDS's 128-byte bank row
   const int code_ld = std::is_void<SRC_TAG>::value ? 0 : (int)((a.K + BK - 1) / BK * BK + 16);
-  return dma ? launch_split_dma<SRC_TAG, FM, FN, D, HALF, true>(a, x, code_ld, stream)
-             : launch_split_dma<SRC_TAG, FM, FN, 1, HALF, false>(a, x, code_ld, stream);
+  if (w == 16) return launch_split_dma<SRC_TAG, FM, FN, D, HALF, 16>(a, x, code_ld, stream);
+  if (w == 4) return launch_split_dma<SRC_TAG, FM, FN, D, HALF, 4>(a, x, code_ld, stream);
+  return launch_split_dma<SRC_TAG, FM, FN, 1, HALF, 0>(a, x, code_ld, stream);
 }
 
 // The variants and what each costs: a CU runs up to `resident` workgroups at
 // once, so it works through its share of the tiles in rounds; a round costs
 // 1 us, a K-block of a tile per_kb (an eighth of the K-blocks for the split
 // variants, whose eight waves share them), the launch and the store `fixed`;
-// first for direct-to-LDS operands, then for operands through registers.
-// The constants are fitted to 250 products (1 to 4096 rows, ten weights from
-// 512x512 to 18432x7168) and, through registers, 162 with odd sizes, each
-// timed with every variant: the choice takes 2.9% (4.1%) longer than the
-// fastest variant in the geometric mean; the best single variant would take
-// 60% (67%) longer.  resident = 0: not for such operands (the 64x64 split
-// variant spills with its loads in registers).
+// for direct-to-LDS operands in loads of 16 and of 4 bytes, and for operands
+// through registers.  The constants are fitted to 250 products (1 to 4096 rows,
+// ten weights from 512x512 to 18432x7168), 118 with rows aligned to 4 bytes
+// alone and 162 with odd sizes, each timed with every variant: the choice takes
+// 2.9% (1.1%, 4.1%) longer than the fastest variant in the geometric mean; the
+// best single variant would take 60% (-, 67%) longer.  resident = 0: not for
+// such operands (the 64x64 split variant spills with its loads in registers).
 struct Cost {
   int resident;
   float fixed, per_kb;
@@ -868,20 +941,20 @@ struct Cost {
 struct Variant {
   int bm, bn;
   bool split;
-  Cost dma, regs;
+  Cost dma, dma4, regs;
 };
-constexpr Variant kVariants[] = {{16, 8, true, {2, 1.30f, 0.327f}, {2, 1.57f, 0.575f}},
-                                 {16, 16, true, {2, 1.38f, 0.470f}, {2, 1.68f, 0.799f}},
-                                 {32, 32, true, {2, 1.52f, 0.966f}, {1, 2.53f, 1.870f}},
-                                 {64, 32, true, {1, 1.69f, 1.465f}, {1, 3.43f, 2.845f}},
-                                 {64, 64, true, {1, 2.60f, 2.164f}, {0, 0.0f, 0.0f}},
-                                 {64, 64, false, {2, 2.62f, 0.271f}, {2, 4.93f, 0.608f}},
-                                 {128, 128, false, {1, 2.49f, 0.607f}, {1, 5.42f, 1.550f}},
-                                 {128, 256, false, {1, 3.54f, 0.897f}, {1, 7.28f, 2.135f}},
-                                 {256, 256, false, {1, 4.72f, 1.556f}, {1, 19.67f, 2.625f}}};
+constexpr Variant kVariants[] = {{16, 8, true, {2, 1.30f, 0.327f}, {2, 1.99f, 0.280f}, {2, 1.57f, 0.575f}},
+                                 {16, 16, true, {2, 1.38f, 0.470f}, {2, 1.80f, 0.433f}, {2, 1.68f, 0.799f}},
+                                 {32, 32, true, {2, 1.52f, 0.966f}, {2, 2.19f, 0.761f}, {1, 2.53f, 1.870f}},
+                                 {64, 32, true, {1, 1.69f, 1.465f}, {1, 2.14f, 1.658f}, {1, 3.43f, 2.845f}},
+                                 {64, 64, true, {1, 2.60f, 2.164f}, {1, 3.35f, 2.380f}, {0, 0.0f, 0.0f}},
+                                 {64, 64, false, {2, 2.62f, 0.271f}, {2, 3.31f, 0.435f}, {2, 4.93f, 0.608f}},
+                                 {128, 128, false, {1, 2.49f, 0.607f}, {1, 3.14f, 0.953f}, {1, 5.42f, 1.550f}},
+                                 {128, 256, false, {1, 3.54f, 0.897f}, {1, 4.54f, 1.432f}, {1, 7.28f, 2.135f}},
+                                 {256, 256, false, {1, 4.72f, 1.556f}, {1, 6.71f, 2.282f}, {1, 19.67f, 2.625f}}};
 
-float variant_us(const Variant& v, const GemmI8Args& a, bool dma, int cus) {
-  const Cost& c = dma ? v.dma : v.regs;
+float variant_us(const Variant& v, const GemmI8Args& a, int w, int cus) {
+  const Cost& c = w == 16 ? v.dma : w == 4 ? v.dma4 : v.regs;
   const int64_t tiles = (a.M + v.bm - 1) / v.bm * ((a.N + v.bn - 1) / v.bn);
   // a split launch has one workgroup per tile
   if (c.resident == 0 || (v.split && tiles > kMaxGrid)) return 1e30f;
@@ -908,12 +981,13 @@ bool linear_i8_fused(int64_t M, int64_t N, int64_t K, bool gated) {
 }
 
 hipError_t launch_linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q, hipStream_t stream) {
-  const bool half = (g.N + 15) / 16 < device_cu_count(), dma = dma_ok(g.B, g.ldb, g.K);
+  const bool half = (g.N + 15) / 16 < device_cu_count();
+  const int w = feed_bytes(g, false);
   if (q.u != nullptr)
-    return half ? launch_split<Gated, 1, 1, 3, true>(g, q, dma, stream)
-                : launch_split<Gated, 1, 1, 3, false>(g, q, dma, stream);
-  return half ? launch_split<Plain, 1, 1, 3, true>(g, q, dma, stream)
-              : launch_split<Plain, 1, 1, 3, false>(g, q, dma, stream);
+    return half ? launch_split<Gated, 1, 1, 3, true>(g, q, w, stream)
+                : launch_split<Gated, 1, 1, 3, false>(g, q, w, stream);
+  return half ? launch_split<Plain, 1, 1, 3, true>(g, q, w, stream)
+              : launch_split<Plain, 1, 1, 3, false>(g, q, w, stream);
 }
 
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
@@ -924,22 +998,24 @@ hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
                        stream, a);
     return hipGetLastError();
   }
-  const bool dma = dma_ok(a.A, a.lda, a.K) && dma_ok(a.B, a.ldb, a.K);
+  const int w = feed_bytes(a, true);
   const int cus = device_cu_count();
   int best = 0;
   for (int i = 1; i < (int)(sizeof(kVariants) / sizeof(kVariants[0])); ++i)
-    if (variant_us(kVariants[i], a, dma, cus) < variant_us(kVariants[best], a, dma, cus)) best = i;
+    if (variant_us(kVariants[i], a, w, cus) < variant_us(kVariants[best], a, w, cus)) best = i;
   const RowQuantArgs none{};
   switch (best) {
-    case 0: return launch_split<void, 1, 1, 2, true>(a, none, dma, stream);
-    case 1: return launch_split<void, 1, 1, 2, false>(a, none, dma, stream);
-    case 2: return launch_split<void, 2, 2, 1, false>(a, none, dma, stream);
-    case 3: return launch_split<void, 4, 2, 1, false>(a, none, dma, stream);
-    case 4: return launch_split_dma<void, 4, 4, 1, false>(a, none, 0, stream);
-    case 5: return launch_tiles<I8Cfg<64, 64, 2, 2, 4>>(a, dma, stream);
-    case 6: return launch_tiles<I8Cfg<128, 128, 2, 4, 3>>(a, dma, stream);
-    case 7: return launch_tiles<I8Cfg<128, 256, 2, 4, 3>>(a, dma, stream);
-    default: return launch_tiles<I8Cfg<256, 256, 2, 4, 2>>(a, dma, stream);
+    case 0: return launch_split<void, 1, 1, 2, true>(a, none, w, stream);
+    case 1: return launch_split<void, 1, 1, 2, false>(a, none, w, stream);
+    case 2: return launch_split<void, 2, 2, 1, false>(a, none, w, stream);
+    case 3: return launch_split<void, 4, 2, 1, false>(a, none, w, stream);
+    case 4:
+      return w == 4 ? launch_split_dma<void, 4, 4, 1, false, 4>(a, none, 0, stream)
+                    : launch_split_dma<void, 4, 4, 1, false>(a, none, 0, stream);
+    case 5: return launch_tiles<I8Cfg<64, 64, 2, 2, 4>>(a, w, stream);
+    case 6: return launch_tiles<I8Cfg<128, 128, 2, 4, 3>>(a, w, stream);
+    case 7: return launch_tiles<I8Cfg<128, 256, 2, 4, 3>>(a, w, stream);
+    default: return launch_tiles<I8Cfg<256, 256, 2, 4, 2>>(a, w, stream);
   }
 }
 

@@ -269,3 +269,26 @@ def test_refusals():
         ds.row_quant_i8(x.half())
     with pytest.raises(ds.Dsfp8Error):
         ds.silu_mul_row_quant_i8(x, x[:, :16])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (3, 8, 20), (16, 33, 132), (20, 96, 500), (33, 50, 2044), (70, 260, 604),
+                                   (100, 7000, 1004), (130, 1300, 36), (600, 700, 1028), (700, 4100, 516),
+                                   (2000, 1100, 508), (2100, 4200, 260)])
+def test_gemm_four_byte_alignment(M, N, K):
+    """Rows that start at multiples of 4 bytes only, values beyond each row's end that must not count."""
+    a, b = i8((M, K), 20), i8((N, K), 21)
+    a_s, b_s = np.full(M, 0.01, np.float32), np.full(N, 0.02, np.float32)
+    da, db = dev_i8(a, K + 4 + (-K % 8), 4), dev_i8(b, K + 4, 12)
+    for d in (da, db):
+        rows, ld = d.shape[0], d.stride(0)
+        d.as_strided((rows, ld - K), (ld, 1), d.storage_offset() + K).fill_(99)
+    c = ds.gemm_i8(da, torch.from_numpy(a_s).cuda(), db, torch.from_numpy(b_s).cuda())
+    assert np.array_equal(host_bits16(c), Q8.gemm(a, a_s, b, b_s))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (2, 5000, 1004), (9, 40, 20), (40, 200, 1000)])
+def test_linear_four_byte_alignment(M, N, K):
+    x, w = bits((M, K), 22), i8((N, K), 23)
+    w_s = np.full(N, 0.02, np.float32)
+    c = ds.linear_i8(dev_bf16(x), dev_i8(w, K + 4, 4), torch.from_numpy(w_s).cuda())
+    assert np.array_equal(host_bits16(c), Q8.linear(x, w, w_s))
