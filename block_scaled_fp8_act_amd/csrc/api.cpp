@@ -596,6 +596,7 @@ dsfp8_status linear_i8(const void* x, int64_t ldx, const void* u, int64_t ldu, c
   DSFP8_TRY(gemm_i8_args(y, ldy, s, B, ldb, b_s, C, ldc, fused ? 0 : M, N, K, g));
   DSFP8_TRY(check_mat(C, M, N, ldc, 2));
   g.M = M;
+  g.a_padded = true;
   dsfp8::RowQuantArgs q;
   DSFP8_TRY(row_quant_args(x, false, ldx, u, ldu, fused ? 0 : M, K, y, ldy, s, q));
   q.M = M;

@@ -235,7 +235,6 @@ struct I8Cfg {
   static constexpr int TM = WM / 32, TN = WN / 32;
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LOADS = A_INSTR + B_INSTR;
-  static constexpr int RING = STAGES * STAGE_BYTES;
   static constexpr int C_BYTES = 32 * WN * 2;  // 32 rows of a wave's output
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole 1 KB segments per wave");
   static_assert(WM % 32 == 0 && WN % 32 == 0, "32x32 subtiles");
@@ -245,7 +244,7 @@ struct I8Cfg {
 
 template <class CF>
 struct I8Loader {
-  static constexpr int LOADS = CF::LOADS;
+  static constexpr int LOADS = CF::LOADS, STAGE_BYTES = CF::STAGE_BYTES;
   i32x4 rsA, rsB;
   uint32_t off[CF::LOADS];
   uint32_t kc;  // byte within the K-block of every load's chunk (a wave's rows agree modulo 16)
@@ -279,6 +278,7 @@ struct I8Loader {
                                           (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 1024);
     dma_b128(a ? rsA : rsB, at, in ? off[n] : kOob, kbyte);
   }
+  __device__ __forceinline__ void finish(uint8_t*, int) const {}
 };
 
 // The same with four bytes per lane, for rows that are only 4-byte aligned (K a
@@ -286,7 +286,7 @@ struct I8Loader {
 // descriptor's end by itself.
 template <class CF>
 struct I8Loader4 {
-  static constexpr int A_INSTR = 4 * CF::A_INSTR, LOADS = 4 * CF::LOADS;
+  static constexpr int A_INSTR = 4 * CF::A_INSTR, LOADS = 4 * CF::LOADS, STAGE_BYTES = CF::STAGE_BYTES;
   static_assert(LOADS * (CF::STAGES - 2) < 64, "the waits of the K loop");
   i32x4 rsA, rsB;
   uint32_t offA, offB, stepA, stepB;  // of the wave's first row, and from load to load
@@ -320,11 +320,12 @@ struct I8Loader4 {
     const uint32_t at = lds0 + (uint32_t)(stage * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) + i * CF::NW * 256);
     dma_b32(a ? rsA : rsB, at, kbyte + k < K ? off + k : kOob, kbyte);
   }
+  __device__ __forceinline__ void finish(uint8_t*, int) const {}
 };
 
 template <class CF>
 struct I8RegLoader {
-  static constexpr int LOADS = CF::LOADS;
+  static constexpr int LOADS = CF::LOADS, STAGE_BYTES = CF::STAGE_BYTES;
   const int8_t* row[CF::LOADS];
   u32x4 v[CF::LOADS];
   uint32_t at[CF::LOADS];
@@ -361,6 +362,89 @@ struct I8RegLoader {
   }
 };
 
+// A's rows 16-byte aligned and readable up to the next multiple of 16, B's at any
+// address: of B the aligned dwords that hold a row's bytes are loaded, so that
+// the row lies in LDS behind the 0 to 3 bytes before it in memory, and whoever
+// reads a fragment shifts it into place.  A K-block's last fragments then end up
+// to 3 bytes into the next K-block: those dwords are fetched once more, into an
+// area of one dword per row behind the stage (one load per wave).  Rows step by
+// multiples of 4 from load to load, subtile to subtile and tile to tile, so a
+// lane's misalignment never changes.
+template <class CF>
+struct I8LoaderShift {
+  static constexpr int A_INSTR = CF::A_INSTR, LOADS = CF::A_INSTR + 4 * CF::B_INSTR + 1;
+  static constexpr int STAGE_BYTES = CF::STAGE_BYTES + CF::NW * 256;
+  static_assert(LOADS * (CF::STAGES - 2) < 64, "the waits of the K loop");
+  static_assert(CF::NW == 4 || CF::NW == 8, "a load's rows of B and the next's differ by 8 or 16");
+  static_assert(CF::BN <= 64 * CF::NW, "a lane per row of B");
+  i32x4 rsA, rsB;
+  uint32_t offA[A_INSTR], kcA, KA;
+  uint32_t mis, ld, K;                   // B: its first row's misalignment, the row stride
+  uint32_t offB, stepB, endB, kcB;       // the lane's row in the first load, the step; first byte past the row
+  uint32_t offT, endT;
+  uint32_t lds0;
+
+  __device__ __forceinline__ void init(const GemmI8Args& p, int64_t m0, int64_t n0, uint8_t* smem) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t ra = p.M - m0 < CF::BM ? p.M - m0 : CF::BM, rb = p.N - n0 < CF::BN ? p.N - n0 : CF::BN;
+    K = (uint32_t)p.K;
+    KA = (K + 15) & ~15u;
+    rsA = make_rsrc(p.A + m0 * p.lda, (uint32_t)((ra - 1) * p.lda) + KA);
+    kcA = (uint32_t)((lane & 7) ^ swz_key(wave * 8 + (lane >> 3))) * 16;
+#pragma unroll
+    for (int n = 0; n < A_INSTR; ++n) {
+      const int r = (wave + CF::NW * n) * 8 + (lane >> 3);
+      offA[n] = r < ra ? (uint32_t)(r * p.lda) + kcA : kOob;
+    }
+    const int8_t* B = p.B + n0 * p.ldb;
+    mis = (uint32_t)(reinterpret_cast<uintptr_t>(B) & 3);
+    ld = (uint32_t)p.ldb;
+    rsB = make_rsrc(B - mis, (uint32_t)((mis + (rb - 1) * p.ldb + p.K + 3) & ~(int64_t)3));
+    const int r = 2 * wave + (lane >> 5);
+    kcB = (uint32_t)(((lane & 31) >> 2) ^ swz_key(r)) * 16 + 4 * (lane & 3);
+    offB = (mis + r * ld) & ~3u;
+    endB = ((mis + r * ld) & 3) + K;
+    stepB = 2 * CF::NW * ld;
+    const int rt = 64 * wave + lane;
+    offT = (mis + rt * ld) & ~3u;
+    endT = rt < CF::BN ? ((mis + rt * ld) & 3) + K : 0;
+    lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem)) + (uint32_t)wave * 256;
+  }
+
+  // B's K-block is part of the lane's offset, which the descriptor checks: a row
+  // past the matrix may begin in the last row's last dword.
+  template <bool>
+  __device__ __forceinline__ void issue(int n, int kb, int stage) const {
+    const uint32_t kbyte = (uint32_t)kb * BK, at = lds0 + (uint32_t)(stage * STAGE_BYTES);
+    if (n < A_INSTR) {
+      const uint32_t wave = threadIdx.x >> 6;
+      dma_b128(rsA, at + (uint32_t)__builtin_amdgcn_readfirstlane((int)wave) * 768 + (uint32_t)(n * CF::NW * 1024),
+               kbyte + kcA < KA ? offA[n] : kOob, kbyte);
+    } else if (n < LOADS - 1) {
+      const int i = n - A_INSTR;
+      const uint32_t k = kbyte + (kcB ^ (CF::NW == 4 ? 16u * (i & 1) : 0u));
+      dma_b32(rsB, at + (uint32_t)(CF::A_BYTES + i * CF::NW * 256), k < endB ? offB + (uint32_t)i * stepB + k : kOob, 0);
+    } else {
+      const uint32_t k = kbyte + BK;
+      dma_b32(rsB, at + CF::STAGE_BYTES, k < endT ? offT + k : kOob, 0);
+    }
+  }
+
+  // The dword with a row's last bytes may hold some of the next row's: clear
+  // them, so that the last K-block's sums are those of the rows alone.
+  __device__ __forceinline__ void finish(uint8_t* stage, int kb) const {
+    const int r = threadIdx.x;
+    const uint32_t end = ((mis + (uint32_t)r * ld) & 3) + K, d = (end >> 2) - 32u * kb;
+    if (r < CF::BN && (end & 3)) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(d < 32 ? stage + CF::A_BYTES + swz(r, (int)d >> 2) + 4 * (d & 3)
+                                                        : stage + CF::STAGE_BYTES + 4 * r);
+      *at &= (1u << (8 * (end & 3))) - 1;
+    }
+    __syncthreads();
+  }
+};
+
 // Where a lane's operand fragments lie in a stage: row r of a 32-row slice is
 // held by lanes r and r + 32, the two 16-byte halves of each 32 bytes of K.
 // Computed once per kernel, not once per K-block (+2.8% on 4096x18432x7168).
@@ -369,7 +453,7 @@ struct I8Frag {
   int at, bt;
   int lf[4];
 
-  __device__ __forceinline__ I8Frag() {
+  __device__ __forceinline__ explicit I8Frag(const GemmI8Args&) {
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int fr = lane & 31, fg = lane >> 5;
@@ -378,23 +462,55 @@ struct I8Frag {
 #pragma unroll
     for (int h = 0; h < 4; ++h) lf[h] = fr * BK + (((2 * h + fg) ^ swz_key(fr)) << 4);
   }
+  // Fragment h of the wave's 32-row slice i of A, or j of B.
+  __device__ __forceinline__ v4i a(const uint8_t* stage, int i, int h) const {
+    return *reinterpret_cast<const v4i*>(stage + at + i * 32 * BK + lf[h]);
+  }
+  __device__ __forceinline__ v4i b(const uint8_t* stage, int j, int h) const {
+    return *reinterpret_cast<const v4i*>(stage + bt + j * 32 * BK + lf[h]);
+  }
+};
+
+// The same where B's rows lie behind 0 to 3 bytes: the dword after each fragment,
+// which for the last of a K-block lies in the area behind the stage, and the shift.
+template <class CF>
+struct I8FragShift : I8Frag<CF> {
+  int bn[4], next;  // next: from 32-row slice to slice, for the K-block's last fragment
+  uint32_t shift;
+
+  __device__ __forceinline__ explicit I8FragShift(const GemmI8Args& p) : I8Frag<CF>(p) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int fr = lane & 31, fg = lane >> 5;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int c = 2 * h + fg + 1;
+      bn[h] = c < 8 ? this->bt + fr * BK + ((c ^ swz_key(fr)) << 4)
+                    : CF::STAGE_BYTES + 4 * (wave % CF::WAVES_N * CF::WN + fr);
+    }
+    next = fg ? 32 * 4 : 32 * BK;
+    shift = (uint32_t)(reinterpret_cast<uintptr_t>(p.B + fr * p.ldb) & 3);
+  }
+  __device__ __forceinline__ v4i b(const uint8_t* stage, int j, int h) const {
+    const v4i w = I8Frag<CF>::b(stage, j, h);
+    const int n = *reinterpret_cast<const int*>(stage + bn[h] + j * (h < 3 ? 32 * BK : next));
+    return v4i{(int)__builtin_amdgcn_alignbyte(w[1], w[0], shift), (int)__builtin_amdgcn_alignbyte(w[2], w[1], shift),
+               (int)__builtin_amdgcn_alignbyte(w[3], w[2], shift), (int)__builtin_amdgcn_alignbyte(n, w[3], shift)};
+  }
 };
 
 // The MFMAs of one K-block from its LDS stage; step(s) is called after each of
 // the 4 TM groups of them.
-template <class CF, class Step>
-__device__ __forceinline__ void i8_block(const uint8_t* stage, const I8Frag<CF>& f, v16i (&acc)[CF::TM][CF::TN],
-                                         Step&& step) {
-  const uint8_t* at = stage + f.at;
-  const uint8_t* bt = stage + f.bt;
+template <class CF, class FR, class Step>
+__device__ __forceinline__ void i8_block(const uint8_t* stage, const FR& f, v16i (&acc)[CF::TM][CF::TN], Step&& step) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     v4i fb[CF::TN];
 #pragma unroll
-    for (int j = 0; j < CF::TN; ++j) fb[j] = *reinterpret_cast<const v4i*>(bt + j * 32 * BK + f.lf[h]);
+    for (int j = 0; j < CF::TN; ++j) fb[j] = f.b(stage, j, h);
 #pragma unroll
     for (int i = 0; i < CF::TM; ++i) {
-      const v4i fa = *reinterpret_cast<const v4i*>(at + i * 32 * BK + f.lf[h]);
+      const v4i fa = f.a(stage, i, h);
 #pragma unroll
       for (int j = 0; j < CF::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa, acc[i][j], 0, 0, 0);
       step(h * CF::TM + i);
@@ -403,8 +519,8 @@ __device__ __forceinline__ void i8_block(const uint8_t* stage, const I8Frag<CF>&
 }
 
 // The K loop of one tile; K-blocks 0 .. STAGES - 2 are already on their way.
-template <class CF, bool KFULL, class LD>
-__device__ __forceinline__ void i8_k_loop(const LD& ld, const I8Frag<CF>& f, int nkb, const uint8_t* smem,
+template <class CF, bool KFULL, class LD, class FR>
+__device__ __forceinline__ void i8_k_loop(const LD& ld, const FR& f, int nkb, uint8_t* smem,
                                           v16i (&acc)[CF::TM][CF::TN]) {
   constexpr int PER = (LD::LOADS + 4 * CF::TM - 1) / (4 * CF::TM);
   for (int kb = 0; kb < nkb; ++kb) {
@@ -415,8 +531,10 @@ __device__ __forceinline__ void i8_k_loop(const LD& ld, const I8Frag<CF>& f, int
     else if (CF::STAGES >= 3 && later >= 1) wait_vmcnt<LD::LOADS * (CF::STAGES >= 3 ? 1 : 0)>();
     else wait_vmcnt<0>();
     __syncthreads();
+    uint8_t* stage = smem + (kb % CF::STAGES) * LD::STAGE_BYTES;
+    if (kb == nkb - 1) ld.finish(stage, kb);
     const int kn = kb + CF::STAGES - 1;
-    i8_block<CF>(smem + (kb % CF::STAGES) * CF::STAGE_BYTES, f, acc, [&](int s) __attribute__((always_inline)) {
+    i8_block<CF>(stage, f, acc, [&](int s) __attribute__((always_inline)) {
       if (kn >= nkb) return;
 #pragma unroll
       for (int n = s * PER; n < (s + 1) * PER && n < LD::LOADS; ++n)
@@ -460,7 +578,6 @@ __device__ __forceinline__ void i8_store(const GemmI8Args& p, int64_t m0, int64_
   const int64_t row0 = m0 + wave / CF::WAVES_N * CF::WM, col0 = n0 + wave % CF::WAVES_N * CF::WN;
   uint8_t* st = area + wave * CF::C_BYTES;
   constexpr int CPR = CF::WN / 8, IT = 32 * CPR / 64, MASK = CPR < 8 ? CPR - 1 : 7;
-  const bool vec = (reinterpret_cast<uintptr_t>(p.C) & 15) == 0 && p.ldc % 8 == 0;
 #pragma unroll
   for (int i = 0; i < CF::TM; ++i) {
 #pragma unroll
@@ -486,8 +603,8 @@ __device__ __forceinline__ void i8_store(const GemmI8Args& p, int64_t m0, int64_
       const int64_t row = row0 + 32 * i + (lane + 64 * it) / CPR, col = col0 + (lane + 64 * it) % CPR * 8;
       if (row >= p.M || col >= p.N) continue;
       uint16_t* dst = p.C + row * p.ldc + col;
-      if (vec && col + 8 <= p.N) {
-        *reinterpret_cast<u32x4*>(dst) = v[it];
+      if (col + 8 <= p.N) {
+        *reinterpret_cast<u32x4u*>(dst) = v[it];
       } else {
         const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
         for (int e = 0; e < 8 && col + e < p.N; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
@@ -506,8 +623,15 @@ __device__ __forceinline__ void i8_zero(v16i (&acc)[CF::TM][CF::TN]) {
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 }
 
-// direct-to-LDS (K a multiple of 128, of 16; of 4, in loads of 4 bytes), through registers
-enum Feed { kDmaFull, kDma, kDma4, kRegs };
+// The operands: 16-byte aligned (K a multiple of 128, or of 16), 4-byte aligned
+// (K a multiple of 4), A 16-byte aligned and padded, any (through registers).
+enum Feed { kDmaFull, kDma, kDma4, kShift, kRegs };
+
+template <class CF, Feed FEED>
+using I8Feed = typename std::conditional<
+    FEED == kRegs, I8RegLoader<CF>,
+    typename std::conditional<FEED == kShift, I8LoaderShift<CF>,
+                              typename std::conditional<FEED == kDma4, I8Loader4<CF>, I8Loader<CF>>::type>::type>::type;
 
 // One workgroup per tile, or (with direct-to-LDS loads and room in LDS beside
 // the ring for the output's staging) one per CU that walks its XCD's tiles:
@@ -516,18 +640,18 @@ enum Feed { kDmaFull, kDma, kDma4, kRegs };
 // cover them, so that the store waits for none of the next tile's loads.
 template <class CF, Feed FEED>
 __global__ __launch_bounds__(CF::kThreads) void gemm_i8_kernel(GemmI8Args p) {
-  constexpr bool AHEAD = FEED != kRegs && CF::RING + CF::NW * CF::C_BYTES <= 160 * 1024;
-  constexpr int OUT = AHEAD ? CF::RING : 0;
-  constexpr int LDS = OUT + CF::NW * CF::C_BYTES > CF::RING ? OUT + CF::NW * CF::C_BYTES : CF::RING;
+  constexpr int RING = CF::STAGES * I8Feed<CF, FEED>::STAGE_BYTES;
+  constexpr bool AHEAD = FEED != kRegs && RING + CF::NW * CF::C_BYTES <= 160 * 1024;
+  constexpr int OUT = AHEAD ? RING : 0;
+  constexpr int LDS = OUT + CF::NW * CF::C_BYTES > RING ? OUT + CF::NW * CF::C_BYTES : RING;
   __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
   const int64_t tiles_m = (p.M + CF::BM - 1) / CF::BM, tiles_n = (p.N + CF::BN - 1) / CF::BN;
   const int64_t total = tiles_m * tiles_n;
   const int nkb = (int)((p.K + BK - 1) / BK);
-  const I8Frag<CF> f;
+  const typename std::conditional<FEED == kShift, I8FragShift<CF>, I8Frag<CF>>::type f(p);
   int64_t tm, tn, pid = blockIdx.x;
   tile_of(pid, tiles_m, tiles_n, tm, tn);
-  typename std::conditional<FEED == kRegs, I8RegLoader<CF>,
-                            typename std::conditional<FEED == kDma4, I8Loader4<CF>, I8Loader<CF>>::type>::type ld;
+  I8Feed<CF, FEED> ld;
   auto begin = [&]() __attribute__((always_inline)) {
     ld.init(p, tm * CF::BM, tn * CF::BN, smem);
     if constexpr (FEED != kRegs) {
@@ -804,7 +928,6 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
       for (int v = 0; v < 4; ++v) atomicAdd(&sum[((i * FN + j) * 4 + v) * 64 + lane], acc[i][j][v]);
   __syncthreads();
   constexpr int CPR = CF::TN / 4;  // runs of four columns per row
-  const bool vec = (reinterpret_cast<uintptr_t>(p.C) & 7) == 0 && p.ldc % 4 == 0;
   for (int q = threadIdx.x; q < CF::TM * CPR; q += 64 * kSplitWaves) {
     const int r = q / CPR, c4 = q % CPR;
     const int64_t row = m0 + r, col = n0 + 4 * c4;
@@ -818,8 +941,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
     w[0] = pack_bf16x2(y[0], y[1]);
     w[1] = pack_bf16x2(y[2], y[3]);
     uint16_t* dst = p.C + row * p.ldc + col;
-    if (vec && col + 4 <= p.N) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    if (col + 4 <= p.N) {
+      *reinterpret_cast<u32x2u*>(dst) = u32x2u{w[0], w[1]};
     } else {
       for (int v = 0; v < 4 && col + v < p.N; ++v) dst[v] = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
     }
@@ -898,7 +1021,8 @@ hipError_t launch_tiles(const GemmI8Args& a, int w, hipStream_t stream) {
   // the large tile: one workgroup per CU, a multiple of the XCDs
   const int64_t most = CF::BM * CF::BN == 65536 ? (device_cu_count() + kXcds - 1) / kXcds * kXcds : kMaxGrid;
   const dim3 grid((unsigned)(t < most ? t : most)), blk(CF::kThreads);
-  if (w == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kRegs>), grid, blk, 0, stream, a);
+  if (w == 0 && a.a_padded && a.ldb < (1 << 23)) hipLaunchKernelGGL((gemm_i8_kernel<CF, kShift>), grid, blk, 0, stream, a);
+  else if (w == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kRegs>), grid, blk, 0, stream, a);
   else if (w == 4) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDma4>), grid, blk, 0, stream, a);
   else if (a.K % BK == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDmaFull>), grid, blk, 0, stream, a);
   else hipLaunchKernelGGL((gemm_i8_kernel<CF, kDma>), grid, blk, 0, stream, a);

@@ -146,6 +146,9 @@ struct GemmI8Args {
   uint16_t* C;
   int64_t ldc;
   int64_t M, N, K;
+  // A lies in 16-byte aligned rows that may be read up to K rounded up to 16,
+  // less than 8 MB apart
+  bool a_padded;
 };
 
 // A routed-expert layer for a few tokens.
