@@ -219,10 +219,13 @@ __device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t k, int64_t K)
 // are runs of four columns of one row.
 //
 // Operands whose rows are aligned to 4 bytes alone take the same path in loads
-// of 4 bytes (through registers instead, 333x2500x1000 took 11.0 us against 7.7,
-// and 4096x7168x2052 179 against 90).  All others go through registers
-// (I8RegLoader): the next K-block's chunks are loaded before the MFMAs of the
-// current one and written to the other stage after them.
+// of 4 bytes (through registers instead, 333x2500x1000 took 11.0 us against 7.7).
+// A weight with rows at any address is loaded as aligned dwords where the
+// activations are the quantiser's (I8LoaderShift: 700x4097x4099 with its
+// quantisation 41.9 us against 48.9 through registers, 4096x7169x2051 101.6
+// against 105.6).  Other operands go through registers (I8RegLoader): the next
+// K-block's chunks are loaded before the MFMAs of the current one and written to
+// the other stage after them.
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 
@@ -568,7 +571,8 @@ struct I8Scales {
 
 // Scale and round to bf16, and store 32 rows at a time through an LDS area of
 // the wave's own (chunks of 16 bytes XOR-ed with the row), so that rows leave
-// as 16-byte writes where the output allows.
+// as 16-byte writes, at any address (as 2-byte writes where ldc or C is not
+// 16-byte aligned, 4096x7169x2051 took 141 us against 105).
 template <class CF>
 __device__ __forceinline__ void i8_store(const GemmI8Args& p, int64_t m0, int64_t n0, const I8Scales<CF>& sc,
                                          const v16i (&acc)[CF::TM][CF::TN], uint8_t* area) {
@@ -1009,7 +1013,10 @@ inline bool dma4_ok(const void* p, int64_t ld, int64_t K) {
   return K % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 3) == 0 && ld % 4 == 0 && ld < (1 << 23);
 }
 
-// Bytes per lane of the operands' direct-to-LDS loads; 0: through registers.
+// For loads of B's aligned dwords.
+inline bool shifted(const GemmI8Args& a) { return a.a_padded && a.ldb < (1 << 23); }
+
+// Bytes per lane of the operands' direct-to-LDS loads; 0: neither holds.
 inline int feed_bytes(const GemmI8Args& a, bool with_a) {
   if ((!with_a || dma_ok(a.A, a.lda, a.K)) && dma_ok(a.B, a.ldb, a.K)) return 16;
   return (!with_a || dma4_ok(a.A, a.lda, a.K)) && dma4_ok(a.B, a.ldb, a.K) ? 4 : 0;
@@ -1021,7 +1028,7 @@ hipError_t launch_tiles(const GemmI8Args& a, int w, hipStream_t stream) {
   // the large tile: one workgroup per CU, a multiple of the XCDs
   const int64_t most = CF::BM * CF::BN == 65536 ? (device_cu_count() + kXcds - 1) / kXcds * kXcds : kMaxGrid;
   const dim3 grid((unsigned)(t < most ? t : most)), blk(CF::kThreads);
-  if (w == 0 && a.a_padded && a.ldb < (1 << 23)) hipLaunchKernelGGL((gemm_i8_kernel<CF, kShift>), grid, blk, 0, stream, a);
+  if (w == 0 && shifted(a)) hipLaunchKernelGGL((gemm_i8_kernel<CF, kShift>), grid, blk, 0, stream, a);
   else if (w == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kRegs>), grid, blk, 0, stream, a);
   else if (w == 4) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDma4>), grid, blk, 0, stream, a);
   else if (a.K % BK == 0) hipLaunchKernelGGL((gemm_i8_kernel<CF, kDmaFull>), grid, blk, 0, stream, a);
@@ -1051,13 +1058,14 @@ hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, int w, hipSt
 // once, so it works through its share of the tiles in rounds; a round costs
 // 1 us, a K-block of a tile per_kb (an eighth of the K-blocks for the split
 // variants, whose eight waves share them), the launch and the store `fixed`;
-// for direct-to-LDS operands in loads of 16 and of 4 bytes, and for operands
-// through registers.  The constants are fitted to 250 products (1 to 4096 rows,
-// ten weights from 512x512 to 18432x7168), 118 with rows aligned to 4 bytes
-// alone and 162 with odd sizes, each timed with every variant: the choice takes
-// 2.9% (1.1%, 4.1%) longer than the fastest variant in the geometric mean; the
-// best single variant would take 60% (-, 67%) longer.  resident = 0: not for
-// such operands (the 64x64 split variant spills with its loads in registers).
+// for direct-to-LDS operands in loads of 16 and of 4 bytes, with B's aligned
+// dwords, and through registers (the split variants load the third kind through
+// registers too).  The constants are fitted to 250 products (1 to 4096 rows, ten
+// weights from 512x512 to 18432x7168), 118 with rows aligned to 4 bytes alone and
+// twice 110 with odd sizes, each timed with every variant: the choice takes 2.9%
+// (1.1%, 2.4%, 2.2%) longer than the fastest variant in the geometric mean; the
+// best single variant would take 60% (29%, 70%, 67%) longer.  resident = 0: not
+// for such operands (the 64x64 split variant spills with its loads in registers).
 struct Cost {
   int resident;
   float fixed, per_kb;
@@ -1065,20 +1073,29 @@ struct Cost {
 struct Variant {
   int bm, bn;
   bool split;
-  Cost dma, dma4, regs;
+  Cost dma, dma4, shift, regs;
 };
-constexpr Variant kVariants[] = {{16, 8, true, {2, 1.30f, 0.327f}, {2, 1.99f, 0.280f}, {2, 1.57f, 0.575f}},
-                                 {16, 16, true, {2, 1.38f, 0.470f}, {2, 1.80f, 0.433f}, {2, 1.68f, 0.799f}},
-                                 {32, 32, true, {2, 1.52f, 0.966f}, {2, 2.19f, 0.761f}, {1, 2.53f, 1.870f}},
-                                 {64, 32, true, {1, 1.69f, 1.465f}, {1, 2.14f, 1.658f}, {1, 3.43f, 2.845f}},
-                                 {64, 64, true, {1, 2.60f, 2.164f}, {1, 3.35f, 2.380f}, {0, 0.0f, 0.0f}},
-                                 {64, 64, false, {2, 2.62f, 0.271f}, {2, 3.31f, 0.435f}, {2, 4.93f, 0.608f}},
-                                 {128, 128, false, {1, 2.49f, 0.607f}, {1, 3.14f, 0.953f}, {1, 5.42f, 1.550f}},
-                                 {128, 256, false, {1, 3.54f, 0.897f}, {1, 4.54f, 1.432f}, {1, 7.28f, 2.135f}},
-                                 {256, 256, false, {1, 4.72f, 1.556f}, {1, 6.71f, 2.282f}, {1, 19.67f, 2.625f}}};
+constexpr Variant kVariants[] = {{16, 8, true, {2, 1.30f, 0.327f}, {2, 1.99f, 0.280f},
+                                  {2, 2.27f, 0.305f}, {2, 2.22f, 0.412f}},
+                                 {16, 16, true, {2, 1.38f, 0.470f}, {2, 1.80f, 0.433f},
+                                  {2, 2.46f, 0.488f}, {2, 2.46f, 0.588f}},
+                                 {32, 32, true, {2, 1.52f, 0.966f}, {2, 2.19f, 0.761f},
+                                  {1, 3.56f, 1.150f}, {1, 3.48f, 1.416f}},
+                                 {64, 32, true, {1, 1.69f, 1.465f}, {1, 2.14f, 1.658f},
+                                  {1, 4.65f, 1.668f}, {1, 4.57f, 2.171f}},
+                                 {64, 64, true, {1, 2.60f, 2.164f}, {1, 3.35f, 2.380f},
+                                  {0, 0.0f, 0.0f}, {0, 0.0f, 0.0f}},
+                                 {64, 64, false, {2, 2.62f, 0.271f}, {2, 3.31f, 0.435f},
+                                  {2, 3.98f, 0.471f}, {2, 4.01f, 0.556f}},
+                                 {128, 128, false, {1, 2.49f, 0.607f}, {1, 3.14f, 0.953f},
+                                  {1, 2.96f, 0.998f}, {1, 2.31f, 1.388f}},
+                                 {128, 256, false, {1, 3.54f, 0.897f}, {1, 4.54f, 1.432f},
+                                  {1, 4.13f, 1.595f}, {1, 3.77f, 1.912f}},
+                                 {256, 256, false, {1, 4.72f, 1.556f}, {1, 6.71f, 2.282f},
+                                  {1, 5.64f, 2.178f}, {1, 6.72f, 2.484f}}};
 
 float variant_us(const Variant& v, const GemmI8Args& a, int w, int cus) {
-  const Cost& c = w == 16 ? v.dma : w == 4 ? v.dma4 : v.regs;
+  const Cost& c = w == 16 ? v.dma : w == 4 ? v.dma4 : shifted(a) ? v.shift : v.regs;
   const int64_t tiles = (a.M + v.bm - 1) / v.bm * ((a.N + v.bn - 1) / v.bn);
   // a split launch has one workgroup per tile
   if (c.resident == 0 || (v.split && tiles > kMaxGrid)) return 1e30f;
