@@ -117,6 +117,9 @@ __device__ __forceinline__ u32x2u codes8(const float (&v)[8], float inv) {
 // registers between the maximum and the codes, so it is read once (NC = 0: a
 // longer row is read twice).  A row's last chunk starts at K - 8: where it
 // overlaps the one before, the same codes are written twice.  K >= 8.
+// Bound by memory: bf16 [4096, 7168] 16.9 us, 5.2 TB/s of its 88 MB (reading the
+// row twice, 54.9 us), gated [4096, 18432] 73 us, 5.2 TB/s (275 us); a few rows
+// are bound by the launch and one trip to memory (32 rows of 7168: 3.5 us).
 template <Src SRC, int TPR, int NC>
 __global__ __launch_bounds__(256) void row_quant_kernel(RowQuantArgs a) {
   constexpr int RPB = 256 / TPR;
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(256) void row_quant_kernel(RowQuantArgs a) {
   }
 }
 
-// Rows of fewer than 8 elements: one thread each.
+// Rows of fewer than 8 elements: one thread each, bound by the launch.
 __global__ __launch_bounds__(256) void row_quant_short_kernel(RowQuantArgs a) {
   for (int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x; m < a.M; m += (int64_t)gridDim.x * 256) {
     float v[8];
@@ -217,6 +220,11 @@ __device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t k, int64_t K)
 // loop, so the accumulators stay where the matrix instruction leaves them.
 // The weight fragment is the instruction's first operand, so a lane's results
 // are runs of four columns of one row.
+// Large products are bound by the matrix cores at the clock that the card's power
+// allows: 4096x18432x7168 455 us (2380 TOPS) and 4096x7168x18432 430 us (2520),
+// in 256x256 tiles of eight 128x64 waves; waves of 64x128, sixteen of 64x64 or
+// four of 128x128 were slower.  Smaller tiles serve products whose 256x256 tiles
+// would leave CUs idle (kVariants).
 //
 // Operands whose rows are aligned to 4 bytes alone take the same path in loads
 // of 4 bytes (through registers instead, 333x2500x1000 took 11.0 us against 7.7).
@@ -705,6 +713,9 @@ __global__ __launch_bounds__(CF::kThreads) void gemm_i8_kernel(GemmI8Args p) {
 // hold one K-block of the tile's rows, so no wave waits for another until the
 // sums are added up at the end, by integer additions in LDS, whose order does
 // not matter.  All of a wave's first D K-blocks are in flight at once.
+// Bound by the latency of a trip to memory and by what one CU loads: the product
+// 32x1536x7168 takes 5.1 us (16x16 tiles, 192 workgroups), 64x7168x2048 6.2 us,
+// 333x2500x1000 8.1 us, and the fused layer 1x1536x7168 6.5 us for 11 MB.
 //
 // FUSED: the activations come as the quantiser's input and every workgroup
 // quantises all M <= 16 rows of it itself, while its first weights are on
@@ -955,7 +966,8 @@ __global__ __launch_bounds__(64 * kSplitWaves) void gemm_i8_split_kernel(GemmI8A
 
 // ---- K < 16 ----------------------------------------------------------------------------
 
-// A row is shorter than one load: one output per thread, byte by byte.
+// A row is shorter than one load: one output per thread, byte by byte.  Bound by
+// the launch for what such K is used for.
 __global__ __launch_bounds__(256) void gemm_i8_short_kernel(GemmI8Args p) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M * p.N; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / p.N, n = i - m * p.N;
