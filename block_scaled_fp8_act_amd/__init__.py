@@ -409,12 +409,17 @@ def moe_combine(yr, indices, weights, token_rows, out=None):
 def _is_mat(t, dtype, dim=2):
     """What `_mat` asks for, as one expression for calls whose cost counts."""
     return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == dim
-            and (t.stride(dim - 1) == 1 or t.numel() == 0))
+            and (t.is_contiguous() or t.stride(dim - 1) == 1 or t.numel() == 0))
 
 
 def _need(t, name, dtype, dim=2):
     if not _is_mat(t, dtype, dim):
         _mat(t, name, (dtype,), dim)
+
+
+def _row(t, n):
+    """`_ld` of a matrix whose last dimension is n."""
+    return n if t.is_contiguous() else _ld(t)
 
 
 def _same_device(dev, **others):
@@ -518,15 +523,16 @@ def _linear_i8(name, x, u, w, w_s, out, workspace):
         raise Dsfp8Error(f"the input and w disagree on K: {K} vs {K2}")
     _vec_f32(w_s, N, "w_s")
     dev = x.get_device()
-    _same_device(dev, w=w, w_s=w_s)
+    if w.get_device() != dev or w_s.get_device() != dev:
+        _same_device(dev, w=w, w_s=w_s)
     lib = _lib.load()
     c = x.new_empty((M, N)) if out is None else _out(out, (M, N), torch.bfloat16, x.device, "out")
     ws, wp, wn = _workspace(workspace, lib.dsfp8_linear_i8_workspace_bytes(M, N, K, 0 if u is None else 1), x)
-    tail = (w.data_ptr(), _ld(w), w_s.data_ptr(), c.data_ptr(), _ld(c), M, N, K, wp, wn)
+    tail = (w.data_ptr(), _row(w, K), w_s.data_ptr(), c.data_ptr(), _row(c, N), M, N, K, wp, wn)
     if u is None:
-        _launch(name, lib.dsfp8_linear_i8, dev, x.data_ptr(), _ld(x), *tail)
+        _launch(name, lib.dsfp8_linear_i8, dev, x.data_ptr(), _row(x, K), *tail)
     else:
-        _launch(name, lib.dsfp8_silu_mul_linear_i8, dev, x.data_ptr(), _ld(x), u.data_ptr(), _ld(u), *tail)
+        _launch(name, lib.dsfp8_silu_mul_linear_i8, dev, x.data_ptr(), _row(x, K), u.data_ptr(), _row(u, K), *tail)
     return c
 
 
@@ -564,9 +570,8 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     _need(x, "x", torch.bfloat16)
     _mat(w13, "w13", (torch.uint8, torch.int8, torch.float8_e4m3fn), dim=3)
     i8 = w13.dtype == torch.int8
-    if not i8:
-        w13, w2 = _bytes(w13), _bytes(w2)
-    _need(w2, "w2", w13.dtype, 3)
+    if not _is_mat(w2, w13.dtype, 3):
+        _mat(w2, "w2", (torch.int8,) if i8 else (torch.uint8, torch.float8_e4m3fn), dim=3)
     if not _is_mat(indices, torch.int32):
         _int32_mat(indices, "indices")
     _need(weights, "weights", torch.bfloat16)
@@ -585,7 +590,7 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     if w13_s.shape != want13 or w2_s.shape != want2:
         raise Dsfp8Error(f"scales must be w13_s {want13} and w2_s {want2}, got {tuple(w13_s.shape)} and "
                          f"{tuple(w2_s.shape)}")
-    if E > 1:
+    if E > 1 and not (w13.is_contiguous() and w2.is_contiguous() and w13_s.is_contiguous() and w2_s.is_contiguous()):
         for name, t in (("w13", w13), ("w2", w2)) if i8 else (("w13", w13), ("w2", w2), ("w13_s", w13_s),
                                                               ("w2_s", w2_s)):
             st = t.stride()
@@ -598,7 +603,8 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     lib = _lib.load()
     out = x.new_empty((T, D)) if out is None else _out(out, (T, D), torch.bfloat16, x.device, "out")
     ws, wp, wn = _workspace(workspace, lib.dsfp8_moe_few_workspace_bytes(T, k, F), x)
-    _launch("moe_few", lib.dsfp8_moe_few, dev, x.data_ptr(), _ld(x), w13.data_ptr(), _ld(w13), w13_s.data_ptr(),
-            _ld(w13_s), w2.data_ptr(), _ld(w2), w2_s.data_ptr(), _ld(w2_s), 1 if i8 else 0, indices.data_ptr(),
-            _ld(indices), weights.data_ptr(), _ld(weights), T, k, E, D, F, out.data_ptr(), _ld(out), wp, wn)
+    _launch("moe_few", lib.dsfp8_moe_few, dev, x.data_ptr(), _row(x, D), w13.data_ptr(), _row(w13, D),
+            w13_s.data_ptr(), _row(w13_s, want13[-1]), w2.data_ptr(), _row(w2, F), w2_s.data_ptr(),
+            _row(w2_s, want2[-1]), 1 if i8 else 0, indices.data_ptr(), _row(indices, k), weights.data_ptr(),
+            _row(weights, k), T, k, E, D, F, out.data_ptr(), _row(out, D), wp, wn)
     return out
