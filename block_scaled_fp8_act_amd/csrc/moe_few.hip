@@ -41,6 +41,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x4d __attribute__((ext_vector_type(4), aligned(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -256,6 +257,7 @@ struct Panel {
 template <int NB, bool DMA>
 struct Stream {
   u32x4 w[NB][2];  // the step's fragments: lane (r, g) elements 32g .. 32g+31 of row r
+  uint32_t behind[DMA ? 1 : NB], shift[DMA ? 1 : NB];  // the dword after them, and where in the dwords they begin
   uint32_t lds;
   const uint8_t* slot;
   uint32_t voff[2], kc[2];
@@ -292,7 +294,17 @@ struct Stream {
       const int r = 16 * i + (lane & 15);
       const uint8_t* row = p.base + (r < p.rows ? r : 0) * ld;
       const int64_t kk = k + 32 * (lane >> 4);
-      if (k + BK <= K) {
+      shift[b] = behind[b] = 0;
+      if (k + BK <= K && ((reinterpret_cast<uintptr_t>(p.base) | (uintptr_t)ld) & 3) != 0) {
+        // The aligned dwords that hold the 32 bytes, shifted in take(): loads at
+        // any other address pass at half the rate (2 tokens, 8 experts of
+        // 5001 x 1501, 87.1 -> 61.3 us; 16 tokens, 2049 x 700, 63.4 -> 44.8).
+        shift[b] = (uint32_t)(reinterpret_cast<uintptr_t>(row + kk) & 3);
+        const uint8_t* at = row + kk - shift[b];
+        w[b][0] = *reinterpret_cast<const u32x4d*>(at);
+        w[b][1] = *reinterpret_cast<const u32x4d*>(at + 16);
+        behind[b] = *reinterpret_cast<const uint32_t*>(at + (shift[b] ? 32 : 28));
+      } else if (k + BK <= K) {
         w[b][0] = load16<1, false>(row, kk, K);
         w[b][1] = load16<1, false>(row, kk + 16, K);
       } else {
@@ -314,6 +326,14 @@ struct Stream {
         for (int h = 0; h < 2; ++h)
           w[b][h] = *reinterpret_cast<const u32x4*>(slot + b * 2048 + swz(fr, 2 * fg + h));
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t next = e < 7 ? w[b][(e + 1) >> 2][(e + 1) & 3] : behind[b];
+          w[b][e >> 2][e & 3] = __builtin_amdgcn_alignbyte(next, w[b][e >> 2][e & 3], shift[b]);
+        }
     }
   }
 };
