@@ -281,9 +281,15 @@ struct Stream {
       const bool edge = !p.whole || k + BK > K;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t v = voff[h];
-        if (edge) v = 16 * i + 8 * h + (lane >> 3) < p.rows && k + kc[h] < K ? v : kOob;
-        const uint32_t to = lds + (uint32_t)(b * 2048 + h * 1024), from = (uint32_t)(16 * i * ld) + k;
+        uint32_t v = voff[h], from = (uint32_t)(16 * i * ld) + k;
+        if (edge) {
+          // all of it in the lane's offset: a block that begins past the panel's
+          // last row would have a scalar offset above the descriptor's size, and
+          // a check that subtracts it from the size would wrap
+          v = 16 * i + 8 * h + (lane >> 3) < p.rows && k + kc[h] < K ? v + from : kOob;
+          from = 0;
+        }
+        const uint32_t to = lds + (uint32_t)(b * 2048 + h * 1024);
         // nontemporal where nothing is read again: one token 78.1 -> 72.3 us,
         // 16 tokens 521.7 -> 485.1; with it also for experts of several
         // units, 64 tokens over 8 experts took 84.3 against 69.8 us
