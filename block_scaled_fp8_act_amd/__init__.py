@@ -566,7 +566,9 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     either e4m3 (uint8 or float8_e4m3fn) with 128x128 block scales ``w13_s
     [E, ceil(2F/128), ceil(D/128)]`` and ``w2_s [E, ceil(D/128), ceil(F/128)]``, or
     int8 with channel scales ``w13_s [E, 2F]`` and ``w2_s [E, D]``; ``indices``
-    int32 and ``weights`` bf16 ``[T, k]``.  Activations are not quantised."""
+    int32 and ``weights`` bf16 ``[T, k]``.  Activations are not quantised.  The
+    same call gives the same bytes; another routing of the other tokens may
+    change the order of a token's fp32 sums."""
     _need(x, "x", torch.bfloat16)
     _mat(w13, "w13", (torch.uint8, torch.int8, torch.float8_e4m3fn), dim=3)
     i8 = w13.dtype == torch.int8

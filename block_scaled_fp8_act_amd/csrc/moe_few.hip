@@ -26,7 +26,8 @@
 //         elements of F) of all units are dealt to the sixteen waves in equal
 //         consecutive ranges; a wave keeps its sums for all tokens in
 //         registers over its whole range, and the waves join once at the end
-//         in a fixed order, so no sum depends on timing.
+//         in a fixed order, so no sum depends on timing.  The ranges, and with
+//         them where a token's sums are cut, follow from all tokens' indices.
 //
 // Which experts are hit is found by every workgroup for itself from the
 // indices, so nothing has to be sorted first and the host waits for nothing.

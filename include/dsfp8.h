@@ -527,11 +527,14 @@ size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gate
  * weights of experts that some token chose are read.  Weights are the stored
  * values times their scales, activations are not quantised (they are not what
  * such a layer waits for): every sum is fp32, h is carried with 16
- * significant bits, and the output is rounded once.  The result of a token
- * depends on that token alone, repeated calls give the same bytes, and a
- * token none of whose experts lie in [0, E) (an expert-parallel rank's
- * indices are relative to its first expert) gets zeros.  A token may name an
- * expert more than once; its weights add up.
+ * significant bits, and the output is rounded once.  Repeated calls give the
+ * same bytes.  Other tokens' values never enter a token's result, but which
+ * experts they name sets where its fp32 sums over F and j are cut and in what
+ * order the parts are added: with other indices for the rest of the call (or
+ * another T) its bytes may differ by that rounding.  A token none of whose
+ * experts lie in [0, E) (an expert-parallel rank's indices are relative to
+ * its first expert) gets zeros.  A token may name an expert more than once;
+ * its weights add up.
  *
  *   x        bf16 [T, D], row stride ldx                    (device, read)
  *   W13      [E, 2F, D]: w1 in rows 0..F-1 of each expert, w3 in rows

@@ -273,3 +273,24 @@ def test_row_tiles_past_the_last_row(T, E, k, D, Fh, fmt):
     out = run(x, ws, idx, wb)
     check(out, x, ws, idx, wb)
     assert torch.equal(out, run(x, ws, idx, wb)), "repeated calls give the same bytes"
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("T", [6, 40])
+def test_other_tokens_values_and_routing(T, fmt):
+    """Token 0 of a call: the same bytes whatever the other tokens hold while all indices stay; within the bound when
+    the others are routed elsewhere, nowhere, or left out, which moves the cuts of its sums."""
+    E, k, D, Fh = 8, 3, 640, 384
+    ws = weights(E, D, Fh, fmt)
+    x = I.activations((T, D), CID, 800)
+    idx, wb = routing(T, E, k, 40)
+    first = run(x, ws, idx, wb)
+    check(first, x, ws, idx, wb)
+    other_x, other_wb = I.activations((T, D), CID, 801, std=50.0), routing(T, E, k, 41)[1]
+    other_x[0], other_wb[0] = x[0], wb[0]
+    assert torch.equal(run(other_x, ws, idx, other_wb)[0], first[0])
+    for i in range(4):
+        other = routing(T, E, k, 42 + i)[0] if i < 3 else np.full((T, k), -1, np.int32)
+        other[0] = idx[0]
+        check(run(x, ws, other, wb), x, ws, other, wb, f"routing {i}")
+    check(run(x[:1], ws, idx[:1], wb[:1]), x[:1], ws, idx[:1], wb[:1], "alone")
