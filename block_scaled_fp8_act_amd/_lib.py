@@ -45,6 +45,7 @@ SIGNATURES = {
     "dsfp8_linear_i8": (_i, [_p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _p, _sz, _p]),
     "dsfp8_silu_mul_linear_i8": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _p, _sz, _p]),
     "dsfp8_linear_i8_workspace_bytes": (_sz, [_i64, _i64, _i64, _i]),
+    "dsfp8_i8_variant": (_i, [_i, _p, _i64, _p, _i64, _i64, _i64, _i64, _p]),
     "dsfp8_moe_few": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _i64, _i64,
                            _i64, _i64, _i64, _p, _i64, _p, _sz, _p]),
     "dsfp8_moe_few_workspace_bytes": (_sz, [_i64, _i64, _i64]),

@@ -653,6 +653,30 @@ dsfp8_status dsfp8_silu_mul_linear_i8(const void* g, int64_t ldg, const void* u,
   return linear_i8(g, ldg, u, ldu, B, ldb, b_s, C, ldc, M, N, K, workspace, workspace_bytes, stream);
 }
 
+dsfp8_status dsfp8_i8_variant(int call, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t M, int64_t N,
+                              int64_t K, int32_t* variant) {
+  if (variant == nullptr) return DSFP8_ERR_NULL;
+  if (call < 0 || call > 2 || !dim_ok(M) || !dim_ok(N) || K < 0 || K > kMaxI8K) return DSFP8_ERR_SHAPE;
+  dsfp8::GemmI8Args a{};
+  a.A = call == 0 ? static_cast<const int8_t*>(A) : nullptr;
+  a.lda = call == 0 ? lda : pad16(K);
+  a.a_padded = call != 0;
+  a.B = static_cast<const int8_t*>(B);
+  a.ldb = ldb;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  dsfp8::I8Variant v{DSFP8_I8_NONE, 0, 0, 0};
+  if (M > 0 && N > 0)
+    v = call != 0 && dsfp8::linear_i8_fused(M, N, K, call == 2) ? dsfp8::linear_i8_fused_variant(a)
+                                                                : dsfp8::gemm_i8_variant(a);
+  variant[0] = v.kind;
+  variant[1] = v.rows;
+  variant[2] = v.columns;
+  variant[3] = v.feed;
+  return DSFP8_OK;
+}
+
 // ---- routed experts for a few tokens ----------------------------------------------------
 
 size_t dsfp8_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F) {

@@ -1134,13 +1134,38 @@ bool linear_i8_fused(int64_t M, int64_t N, int64_t K, bool gated) {
 }
 
 hipError_t launch_linear_i8_fused(const GemmI8Args& g, const RowQuantArgs& q, hipStream_t stream) {
-  const bool half = (g.N + 15) / 16 < device_cu_count();
-  const int w = feed_bytes(g, false);
+  const I8Variant v = linear_i8_fused_variant(g);
+  const bool half = v.columns == 8;
+  const int w = v.feed;
   if (q.u != nullptr)
     return half ? launch_split<Gated, 1, 1, 3, true>(g, q, w, stream)
                 : launch_split<Gated, 1, 1, 3, false>(g, q, w, stream);
   return half ? launch_split<Plain, 1, 1, 3, true>(g, q, w, stream)
               : launch_split<Plain, 1, 1, 3, false>(g, q, w, stream);
+}
+
+namespace {
+
+// The cheapest variant for operands that are loaded w bytes at a time.
+int choose(const GemmI8Args& a, int w) {
+  const int cus = device_cu_count();
+  int best = 0;
+  for (int i = 1; i < (int)(sizeof(kVariants) / sizeof(kVariants[0])); ++i)
+    if (variant_us(kVariants[i], a, w, cus) < variant_us(kVariants[best], a, w, cus)) best = i;
+  return best;
+}
+
+}  // namespace
+
+I8Variant gemm_i8_variant(const GemmI8Args& a) {
+  if (a.K < 16) return {DSFP8_I8_SHORT, 0, 0, 0};
+  const int w = feed_bytes(a, true);
+  const Variant& v = kVariants[choose(a, w)];
+  return {v.split ? DSFP8_I8_SPLIT : DSFP8_I8_TILES, v.bm, v.bn, w == 0 && !v.split && shifted(a) ? 1 : w};
+}
+
+I8Variant linear_i8_fused_variant(const GemmI8Args& a) {
+  return {DSFP8_I8_FUSED, 16, (a.N + 15) / 16 < device_cu_count() ? 8 : 16, feed_bytes(a, false)};
 }
 
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
@@ -1152,12 +1177,8 @@ hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
     return hipGetLastError();
   }
   const int w = feed_bytes(a, true);
-  const int cus = device_cu_count();
-  int best = 0;
-  for (int i = 1; i < (int)(sizeof(kVariants) / sizeof(kVariants[0])); ++i)
-    if (variant_us(kVariants[i], a, w, cus) < variant_us(kVariants[best], a, w, cus)) best = i;
   const RowQuantArgs none{};
-  switch (best) {
+  switch (choose(a, w)) {
     case 0: return launch_split<void, 1, 1, 2, true>(a, none, w, stream);
     case 1: return launch_split<void, 1, 1, 2, false>(a, none, w, stream);
     case 2: return launch_split<void, 2, 2, 1, false>(a, none, w, stream);

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/dsfp8.h"
+
 namespace dsfp8 {
 
 struct ActQuantArgs {
@@ -175,6 +177,13 @@ struct MoeFewArgs {
   int64_t ldo;
   void* work;
 };
+
+// Which kernel serves a product: dsfp8_i8_variant's four numbers.
+struct I8Variant {
+  int kind, rows, columns, feed;
+};
+I8Variant gemm_i8_variant(const GemmI8Args& a);
+I8Variant linear_i8_fused_variant(const GemmI8Args& a);
 
 hipError_t launch_row_quant_i8(const RowQuantArgs& a, hipStream_t stream);
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream);

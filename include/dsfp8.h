@@ -62,7 +62,7 @@
 extern "C" {
 #endif
 
-#define DSFP8_ABI_VERSION 7
+#define DSFP8_ABI_VERSION 8
 #define DSFP8_BLOCK 128
 
 typedef int dsfp8_status;
@@ -516,6 +516,29 @@ dsfp8_status dsfp8_silu_mul_linear_i8(const void* g, int64_t ldg, const void* u,
 
 /* gated: nonzero for dsfp8_silu_mul_linear_i8. */
 size_t dsfp8_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated);
+
+/*
+ * Which kernel serves an int8 product, for tests and profiles (a host call;
+ * nothing is launched and no memory but `variant` is accessed: A and B matter
+ * by their alignment alone).  call: 0 dsfp8_gemm_i8, 1 dsfp8_linear_i8,
+ * 2 dsfp8_silu_mul_linear_i8 (A and lda are then not used).
+ *   variant[0]  kind: one of the values below
+ *   variant[1], variant[2]  rows and columns of a workgroup's output tile
+ *   variant[3]  bytes per lane of the operands' direct-to-LDS loads: 16 or 4;
+ *            1: a weight with rows at any address as aligned dwords; 0: through
+ *            registers
+ * The tile sizes follow the current device's number of CUs.
+ * Errors: NULL, SHAPE.
+ */
+enum {
+  DSFP8_I8_NONE = 0,  /* nothing to do */
+  DSFP8_I8_TILES = 1, /* a workgroup per tile, or per CU and walking the tiles */
+  DSFP8_I8_SPLIT = 2, /* K split over the waves of a workgroup */
+  DSFP8_I8_FUSED = 3, /* as SPLIT, the quantisation in the same launch */
+  DSFP8_I8_SHORT = 4  /* K < 16 */
+};
+dsfp8_status dsfp8_i8_variant(int call, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t M,
+                              int64_t N, int64_t K, int32_t* variant);
 
 /*
  * A whole routed-expert layer for a few tokens ([AG] 6.4 / 8.4 with the
