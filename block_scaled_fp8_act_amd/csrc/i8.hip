@@ -1077,7 +1077,8 @@ hipError_t launch_split(const GemmI8Args& a, const RowQuantArgs& x, int w, hipSt
 // twice 110 with odd sizes, each timed with every variant: the choice takes 2.9%
 // (1.1%, 2.4%, 2.2%) longer than the fastest variant in the geometric mean; the
 // best single variant would take 60% (29%, 70%, 67%) longer.  resident = 0: not
-// for such operands (the 64x64 split variant spills with its loads in registers).
+// for such operands (the 64x64 split variant spills with its loads in registers;
+// with loads of 4 bytes the 64x32 one, at 2.14 and 1.658, was never the cheapest).
 struct Cost {
   int resident;
   float fixed, per_kb;
@@ -1093,7 +1094,7 @@ constexpr Variant kVariants[] = {{16, 8, true, {2, 1.30f, 0.327f}, {2, 1.99f, 0.
                                   {2, 2.46f, 0.488f}, {2, 2.46f, 0.588f}},
                                  {32, 32, true, {2, 1.52f, 0.966f}, {2, 2.19f, 0.761f},
                                   {1, 3.56f, 1.150f}, {1, 3.48f, 1.416f}},
-                                 {64, 32, true, {1, 1.69f, 1.465f}, {1, 2.14f, 1.658f},
+                                 {64, 32, true, {1, 1.69f, 1.465f}, {0, 0.0f, 0.0f},
                                   {1, 4.65f, 1.668f}, {1, 4.57f, 2.171f}},
                                  {64, 64, true, {1, 2.60f, 2.164f}, {1, 3.35f, 2.380f},
                                   {0, 0.0f, 0.0f}, {0, 0.0f, 0.0f}},
@@ -1182,7 +1183,9 @@ hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t stream) {
     case 0: return launch_split<void, 1, 1, 2, true>(a, none, w, stream);
     case 1: return launch_split<void, 1, 1, 2, false>(a, none, w, stream);
     case 2: return launch_split<void, 2, 2, 1, false>(a, none, w, stream);
-    case 3: return launch_split<void, 4, 2, 1, false>(a, none, w, stream);
+    case 3:
+      return w == 16 ? launch_split_dma<void, 4, 2, 1, false>(a, none, 0, stream)
+                     : launch_split_dma<void, 4, 2, 1, false, 0>(a, none, 0, stream);
     case 4:
       return w == 4 ? launch_split_dma<void, 4, 4, 1, false, 4>(a, none, 0, stream)
                     : launch_split_dma<void, 4, 4, 1, false>(a, none, 0, stream);
