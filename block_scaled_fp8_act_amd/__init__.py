@@ -67,13 +67,14 @@ def _mat(t, name, dtypes, dim=2):
         raise Dsfp8Error(f"{name} must have dtype in {dtypes}, got {t.dtype}")
     if t.dim() != dim:
         raise Dsfp8Error(f"{name} must be {dim}-D, got {t.dim()} dimensions")
-    if t.numel() > 0 and t.stride(-1) != 1:
+    if t.numel() > 0 and t.stride(-1) != 1 and not t.is_contiguous():
         raise Dsfp8Error(f"{name}: the last dimension needs stride 1")
     return t
 
 
 def _ld(t):
-    return t.stride(-2) if t.numel() > 0 else t.shape[-1]
+    """Row stride; a contiguous tensor's own says nothing where it has a single row."""
+    return t.shape[-1] if t.is_contiguous() or t.numel() == 0 else t.stride(-2)
 
 
 def _scale_strides(t):

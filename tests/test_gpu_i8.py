@@ -292,3 +292,31 @@ def test_linear_four_byte_alignment(M, N, K):
     w_s = np.full(N, 0.02, np.float32)
     c = ds.linear_i8(dev_bf16(x), dev_i8(w, K + 4, 4), torch.from_numpy(w_s).cuda())
     assert np.array_equal(host_bits16(c), Q8.linear(x, w, w_s))
+
+
+def test_single_rows_and_columns_of_any_stride():
+    """A row or a column cut out by a transpose is contiguous, whatever stride torch gives its other dimension."""
+    K, N = 200, 40
+    b = bits((1, K), 24)
+    row = dev_bf16(b).reshape(K, 1).t()
+    assert row.shape == (1, K) and row.stride() == (1, 1)
+    w, w_s = i8((N, K), 25), np.full(N, 0.02, np.float32)
+    dw, dw_s = dev_i8(w), torch.from_numpy(w_s).cuda()
+    y, s = ds.row_quant_i8(row)
+    yr, sr = Q8.row_quant(F.bf16_to_f32(b))
+    assert np.array_equal(y.cpu().numpy(), yr) and np.array_equal(s.cpu().numpy(), sr)
+    want = Q8.linear(b, w, w_s)
+    assert np.array_equal(host_bits16(ds.linear_i8(row, dw, dw_s)), want)
+    assert np.array_equal(host_bits16(ds.gemm_i8(y.reshape(K, 1).t(), s, dw, dw_s)), want)
+    out = torch.empty((N, 1), dtype=torch.bfloat16, device="cuda").t()
+    assert np.array_equal(host_bits16(ds.gemm_i8(y, s, dw, dw_s, out=out)), want)
+    one = dw[:1].reshape(K, 1).t()
+    assert np.array_equal(host_bits16(ds.gemm_i8(y, s, one, dw_s[:1])), want[:, :1])
+    h, hs = ds.silu_mul_row_quant_i8(row, row)
+    h0, hs0 = ds.silu_mul_row_quant_i8(row.contiguous().clone(), row.contiguous().clone())
+    assert torch.equal(h, h0) and torch.equal(hs, hs0)
+    column = dev_bf16(bits((K, 1), 26)).reshape(1, K).t()
+    assert column.stride() == (1, K)
+    yc, sc = ds.row_quant_i8(column)
+    yr, sr = Q8.row_quant(F.bf16_to_f32(bits((K, 1), 26)))
+    assert np.array_equal(yc.cpu().numpy(), yr) and np.array_equal(sc.cpu().numpy(), sr)
