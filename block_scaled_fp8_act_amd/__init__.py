@@ -423,6 +423,19 @@ def _row(t, n):
     return n if t.is_contiguous() else _ld(t)
 
 
+def _expert_ld(t, name):
+    """Row stride of stacked matrices [E, rows, columns], whose rows must be evenly spaced over the experts."""
+    if t.is_contiguous() or t.numel() == 0:
+        return t.shape[2]
+    E, rows, _ = t.shape
+    of_expert, of_row, _ = t.stride()
+    if E == 1:
+        return of_row
+    if rows > 1 and of_expert != rows * of_row:
+        raise Dsfp8Error(f"{name}: experts must follow each other row by row")
+    return of_expert // rows
+
+
 def _same_device(dev, **others):
     for name, o in others.items():
         if o.get_device() != dev:
@@ -593,12 +606,9 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     if w13_s.shape != want13 or w2_s.shape != want2:
         raise Dsfp8Error(f"scales must be w13_s {want13} and w2_s {want2}, got {tuple(w13_s.shape)} and "
                          f"{tuple(w2_s.shape)}")
-    if E > 1 and not (w13.is_contiguous() and w2.is_contiguous() and w13_s.is_contiguous() and w2_s.is_contiguous()):
-        for name, t in (("w13", w13), ("w2", w2)) if i8 else (("w13", w13), ("w2", w2), ("w13_s", w13_s),
-                                                              ("w2_s", w2_s)):
-            st = t.stride()
-            if st[0] != t.shape[1] * st[1] and t.numel() > 0:
-                raise Dsfp8Error(f"{name}: experts must follow each other row by row")
+    ld13, ld2 = _expert_ld(w13, "w13"), _expert_ld(w2, "w2")
+    lds13 = _row(w13_s, F2) if i8 else _expert_ld(w13_s, "w13_s")
+    lds2 = _row(w2_s, D) if i8 else _expert_ld(w2_s, "w2_s")
     dev = x.get_device()
     if not (w13.get_device() == w2.get_device() == w13_s.get_device() == w2_s.get_device() == indices.get_device()
             == weights.get_device() == dev):
@@ -606,8 +616,7 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
     lib = _lib.load()
     out = x.new_empty((T, D)) if out is None else _out(out, (T, D), torch.bfloat16, x.device, "out")
     ws, wp, wn = _workspace(workspace, lib.dsfp8_moe_few_workspace_bytes(T, k, F), x)
-    _launch("moe_few", lib.dsfp8_moe_few, dev, x.data_ptr(), _row(x, D), w13.data_ptr(), _row(w13, D),
-            w13_s.data_ptr(), _row(w13_s, want13[-1]), w2.data_ptr(), _row(w2, F), w2_s.data_ptr(),
-            _row(w2_s, want2[-1]), 1 if i8 else 0, indices.data_ptr(), _row(indices, k), weights.data_ptr(),
-            _row(weights, k), T, k, E, D, F, out.data_ptr(), _row(out, D), wp, wn)
+    _launch("moe_few", lib.dsfp8_moe_few, dev, x.data_ptr(), _row(x, D), w13.data_ptr(), ld13, w13_s.data_ptr(), lds13,
+            w2.data_ptr(), ld2, w2_s.data_ptr(), lds2, 1 if i8 else 0, indices.data_ptr(), _row(indices, k),
+            weights.data_ptr(), _row(weights, k), T, k, E, D, F, out.data_ptr(), _row(out, D), wp, wn)
     return out

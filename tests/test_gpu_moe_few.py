@@ -294,3 +294,17 @@ def test_other_tokens_values_and_routing(T, fmt):
         other[0] = idx[0]
         check(run(x, ws, other, wb), x, ws, other, wb, f"routing {i}")
     check(run(x[:1], ws, idx[:1], wb[:1]), x[:1], ws, idx[:1], wb[:1], "alone")
+
+
+def test_block_scales_inside_larger_ones():
+    """Experts with a single row of block scales each, taken out of a larger grid."""
+    T, E, k, D, Fh = 4, 3, 2, 128, 64
+    ws = weights(E, D, Fh, "e4m3")
+    x = I.activations((T, D), CID, 820)
+    idx, wb = routing(T, E, k, 50)
+    s13, s2 = dev(ws[1]), dev(ws[3])
+    assert s13.shape == (E, 1, 1) and s2.shape == (E, 1, 1)
+    grid = torch.full((E, 3, 5), float("nan"), device="cuda")
+    grid[:, :1, :1], grid[:, 2:, 4:] = s13, s2
+    got = ds.moe_few(dev_bf16(x), dev(ws[0]), grid[:, :1, :1], dev(ws[2]), grid[:, 2:, 4:], dev(idx), dev_bf16(wb))
+    check(got, x, ws, idx, wb)
