@@ -17,8 +17,9 @@ include/dsfp8.h for the exact contracts.
 
 int8 tensors are ``torch.int8`` with one fp32 scale per row (a token of an
 activation, an output channel of a weight).  The workspaces that the calls
-below allocate with torch may be passed in instead (``workspace=``), so that a
-serving loop allocates nothing.
+below allocate with torch may be passed in instead (``workspace=``, of at least
+the bytes that the calls' ``*_workspace_bytes`` say), so that a serving loop
+allocates nothing.
 """
 
 import torch
@@ -558,6 +559,11 @@ def linear_i8(x, w, w_s, out=None, workspace=None):
     return _linear_i8("linear_i8", x, None, w, w_s, out, workspace)
 
 
+def linear_i8_workspace_bytes(M, N, K, gated=False):
+    """Bytes of ``workspace`` that :func:`linear_i8` (``gated``: :func:`silu_mul_linear_i8`) needs; 0 for few rows."""
+    return _lib.load().dsfp8_linear_i8_workspace_bytes(M, N, K, 1 if gated else 0)
+
+
 def silu_mul_linear_i8(g, u, w, w_s, out=None, workspace=None):
     """The gated form of :func:`linear_i8`, the down-projection of a feed-forward
     layer: ``gemm_i8(*silu_mul_row_quant_i8(g, u), w, w_s)`` in one call."""
@@ -568,6 +574,11 @@ def silu_mul_linear_i8(g, u, w, w_s, out=None, workspace=None):
 # ---- routed experts for a few tokens ------------------------------------------------------
 
 MOE_FEW_MAX_TOKENS = 64
+
+
+def moe_few_workspace_bytes(T, k, F):
+    """Bytes of ``workspace`` that :func:`moe_few` needs for T tokens of k experts with F hidden columns."""
+    return _lib.load().dsfp8_moe_few_workspace_bytes(T, k, F)
 
 
 def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None):

@@ -24,23 +24,28 @@ import block_scaled_fp8_act_amd as ds  # noqa: E402
 class DecodeMoeLayer:
     """The layer's weights and, for a fixed number of tokens, its buffers.
 
-    ``routed = (w13, w13_s, w2, w2_s)`` as ``moe_few`` takes them; ``shared`` the same for one int8 expert: ``w13 [2F, D]``,
-    ``w13_s [2F]``, ``w2 [D, F]``, ``w2_s [D]``."""
+    ``routed = (w13, w13_s, w2, w2_s)`` as ``moe_few`` takes them; ``shared`` likewise for one int8 expert: ``w13 [2F, D]``,
+    ``w13_s [2F]``, ``w2 [D, F]``, ``w2_s [D]``.  ``topk``: the most experts a token is routed to."""
 
-    def __init__(self, tokens, routed, shared):
+    def __init__(self, tokens, routed, shared, topk=16):
         self.routed, self.shared = routed, shared
         D, device = routed[0].shape[2], routed[0].device
-        self.gate_up = torch.empty((tokens, shared[0].shape[0]), dtype=torch.bfloat16, device=device)
+        F2, F = shared[0].shape[0], shared[2].shape[1]
+        self.gate_up = torch.empty((tokens, F2), dtype=torch.bfloat16, device=device)
         self.y = torch.empty((tokens, D), dtype=torch.bfloat16, device=device)
         self.out = torch.empty((tokens, D), dtype=torch.bfloat16, device=device)
+        # scratch memory of the three calls, which follow each other on one stream
+        need = max(ds.moe_few_workspace_bytes(tokens, topk, routed[2].shape[2]),
+                   ds.linear_i8_workspace_bytes(tokens, F2, D), ds.linear_i8_workspace_bytes(tokens, D, F, gated=True))
+        self.work = torch.empty(need, dtype=torch.uint8, device=device)
 
     def __call__(self, x, indices, weights):
         """bf16 ``[tokens, D]`` for bf16 ``x [tokens, D]``, int32 ``indices`` and bf16 ``weights [tokens, k]``."""
         w13, w13_s, w2, w2_s = self.shared
         F = w2.shape[1]
-        ds.moe_few(x, *self.routed, indices, weights, out=self.out)
-        ds.linear_i8(x, w13, w13_s, out=self.gate_up)
-        ds.silu_mul_linear_i8(self.gate_up[:, :F], self.gate_up[:, F:], w2, w2_s, out=self.y)
+        ds.moe_few(x, *self.routed, indices, weights, out=self.out, workspace=self.work)
+        ds.linear_i8(x, w13, w13_s, out=self.gate_up, workspace=self.work)
+        ds.silu_mul_linear_i8(self.gate_up[:, :F], self.gate_up[:, F:], w2, w2_s, out=self.y, workspace=self.work)
         return self.out.add_(self.y)
 
 
@@ -100,7 +105,7 @@ def main():
     routed = random_weights(a.experts, 2 * a.inter, a.dim, a.routed, dev) + \
         random_weights(a.experts, a.dim, a.inter, a.routed, dev)
     up, down = random_weights(1, 2 * a.inter, a.dim, "int8", dev), random_weights(1, a.dim, a.inter, "int8", dev)
-    layer = DecodeMoeLayer(a.tokens, routed, (up[0][0], up[1][0], down[0][0], down[1][0]))
+    layer = DecodeMoeLayer(a.tokens, routed, (up[0][0], up[1][0], down[0][0], down[1][0]), a.topk)
     x = torch.randn((a.tokens, a.dim), device=dev).bfloat16()
     score, indices = torch.randn((a.tokens, a.experts), device=dev).sigmoid().topk(a.topk)
     weights, indices = (score / score.sum(1, keepdim=True)).bfloat16(), indices.int()

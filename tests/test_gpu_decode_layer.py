@@ -86,3 +86,21 @@ def test_layer(T, E, k, D, Fh, fmt):
         graph.replay()
         assert torch.equal(layer.out, out)
         assert torch.equal(layer(*args), out)
+
+
+@pytest.mark.parametrize("T,topk", [(1, None), (24, None), (40, 2)])
+def test_a_step_allocates_nothing(T, topk):
+    """Every buffer of the layer, its scratch memory included, is there once the layer is."""
+    ex = example()
+    E, k, D, Fh = 4, 2, 384, 256
+    dev = torch.device("cuda")
+    routed = ex.random_weights(E, 2 * Fh, D, "e4m3", dev) + ex.random_weights(E, D, Fh, "e4m3", dev)
+    up, down = ex.random_weights(1, 2 * Fh, D, "int8", dev), ex.random_weights(1, D, Fh, "int8", dev)
+    shared = (up[0][0], up[1][0], down[0][0], down[1][0])
+    layer = ex.DecodeMoeLayer(T, routed, shared) if topk is None else ex.DecodeMoeLayer(T, routed, shared, topk)
+    x = torch.randn((T, D), device=dev).bfloat16()
+    idx = torch.randint(0, E, (T, k), device=dev, dtype=torch.int32)
+    wt = torch.rand((T, k), device=dev).bfloat16()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    layer(x, idx, wt)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
