@@ -24,7 +24,7 @@ import block_scaled_fp8_act_amd as ds  # noqa: E402
 class DecodeMoeLayer:
     """The layer's weights and, for a fixed number of tokens, its buffers.
 
-    ``routed = (w13, w13_s, w2, w2_s)`` as ``moe_few`` takes them; ``shared`` likewise for one int8 expert: ``w13 [2F, D]``,
+    ``routed = (w13, w13_s, w2, w2_s)`` as ``moe_few`` takes them; ``shared`` is one int8 expert: ``w13 [2F, D]``,
     ``w13_s [2F]``, ``w2 [D, F]``, ``w2_s [D]``.  ``topk``: the most experts a token is routed to."""
 
     def __init__(self, tokens, routed, shared, topk=16):

@@ -459,8 +459,11 @@ dsfp8_status dsfp8_row_quant_i8(const void* x, int dtype, int64_t M, int64_t K, 
 
 /*
  * The same of x[m,i] = SiLU(g[m,i]) * u[m,i], SiLU(v) = v / (1 + e^-v),
- * evaluated in fp32 and not rounded in between (the hardware's exponential
- * and reciprocal, each within a few fp32 ulp).
+ * evaluated in fp32 and not rounded in between.  With the hardware's
+ * exponential and reciprocal x is within (|g| + 8) * 2^-23 of its value,
+ * relative to it: the exponential's argument is rounded once, so its error
+ * grows with |g|.  Below g = -87, where 1 / (1 + e^-g) is no normal number, x
+ * may be 0.
  *   g, u   bf16 [M, I], row strides ldg, ldu (device, read; may be the halves
  *          of one [M, 2I] product)
  * Errors: as dsfp8_row_quant_i8.
@@ -550,7 +553,8 @@ dsfp8_status dsfp8_i8_variant(int call, const void* A, int64_t lda, const void* 
  * weights of experts that some token chose are read.  Weights are the stored
  * values times their scales, activations are not quantised (they are not what
  * such a layer waits for): every sum is fp32, h is carried with 16
- * significant bits, and the output is rounded once.  Repeated calls give the
+ * significant bits (its gate as accurate as dsfp8_silu_mul_row_quant_i8's),
+ * and the output is rounded once.  Repeated calls give the
  * same bytes.  Other tokens' values never enter a token's result, but which
  * experts they name sets where its fp32 sums over F and j are cut and in what
  * order the parts are added: with other indices for the rest of the call (or

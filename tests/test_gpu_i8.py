@@ -320,3 +320,19 @@ def test_single_rows_and_columns_of_any_stride():
     yc, sc = ds.row_quant_i8(column)
     yr, sr = Q8.row_quant(F.bf16_to_f32(bits((K, 1), 26)))
     assert np.array_equal(yc.cpu().numpy(), yr) and np.array_equal(sc.cpu().numpy(), sr)
+
+
+def test_silu_mul_accuracy_over_the_gate():
+    """One value per row, which the row's scale shows: relative to it within (|g| + 8) 2^-23, and 2^-23 for the
+    division by 127 and the scale's rounding."""
+    g = F.f32_to_bf16(np.linspace(-86.0, 86.0, 345).astype(np.float32))
+    M = g.size
+    gs, us = np.zeros((M, 64), np.uint16), np.zeros((M, 64), np.uint16)
+    gs[:, 17], us[:, 17] = g, F.f32_to_bf16(np.full(M, 2.0 ** 60, np.float32))
+    _, s = ds.silu_mul_row_quant_i8(dev_bf16(gs), dev_bf16(us))
+    h = np.abs(Q8.silu_mul(gs, us)).max(1)
+    keep = h > 0
+    assert keep.sum() >= M - 1
+    got = s.cpu().numpy().astype(np.float64) * 127
+    bound = (np.abs(F.bf16_to_f32(g).astype(np.float64)) + 8) * 2.0 ** -23 + 2.0 ** -23
+    assert np.all((np.abs(got / np.maximum(h, 2.0 ** -100) - 1) <= bound)[keep])
