@@ -485,7 +485,7 @@ dsfp8_status dsfp8_silu_mul_row_quant_i8(const void* g, int64_t ldg, const void*
  *   b_s    fp32 [N]                                     (device, read)
  *   C      bf16 [M, N], row stride ldc                  (device, written)
  * K <= 131071, the largest for which no sum of int8 products (-128 included)
- * leaves 32 bits.  K = 0 writes zeros.
+ * leaves 32 bits.  With K = 0 every sum is 0, so finite scales give zeros.
  * Errors: NULL, SHAPE, LD, ALIGN, LAUNCH.
  */
 dsfp8_status dsfp8_gemm_i8(const void* A, int64_t lda, const float* a_s, const void* B, int64_t ldb,

@@ -336,3 +336,11 @@ def test_silu_mul_accuracy_over_the_gate():
     got = s.cpu().numpy().astype(np.float64) * 127
     bound = (np.abs(F.bf16_to_f32(g).astype(np.float64)) + 8) * 2.0 ** -23 + 2.0 ** -23
     assert np.all((np.abs(got / np.maximum(h, 2.0 ** -100) - 1) <= bound)[keep])
+
+
+def test_gemm_without_k_shows_bad_scales():
+    """An empty sum is 0, and 0 times a scale that is not finite is NaN, as the formula has it."""
+    a, b = (torch.empty((n, 0), dtype=torch.int8, device="cuda") for n in (2, 3))
+    a_s, b_s = torch.ones(2, device="cuda"), torch.tensor([1.0, float("inf"), 2.0], device="cuda")
+    c = ds.gemm_i8(a, a_s, b, b_s).float().cpu().numpy()
+    assert not c[:, [0, 2]].any() and np.isnan(c[:, 1]).all()
