@@ -119,8 +119,9 @@ __device__ __forceinline__ u32x2u codes8(const float (&v)[8], float inv) {
 // longer row is read twice).  A row's last chunk starts at K - 8: where it
 // overlaps the one before, the same codes are written twice.  K >= 8.
 // Bound by memory: bf16 [4096, 7168] 16.9 us, 5.2 TB/s of its 88 MB (reading the
-// row twice, 54.9 us), gated [4096, 18432] 73 us, 5.2 TB/s (275 us); a few rows
-// are bound by the launch and one trip to memory (32 rows of 7168: 3.5 us).
+// row twice, 54.9 us), gated [4096, 18432] 68-73 us, 5.2-5.5 TB/s (275 us), fp32
+// [4096, 7168] 26.7 us, 5.5 TB/s of 147 MB; a few rows are bound by the launch and
+// one trip to memory (32 rows of 7168: 3.5 us).
 template <Src SRC, int TPR, int NC>
 __global__ __launch_bounds__(256) void row_quant_kernel(RowQuantArgs a) {
   constexpr int RPB = 256 / TPR;
@@ -714,9 +715,11 @@ __global__ __launch_bounds__(CF::kThreads) void gemm_i8_kernel(GemmI8Args p) {
 // hold one K-block of the tile's rows, so no wave waits for another until the
 // sums are added up at the end, by integer additions in LDS, whose order does
 // not matter.  All of a wave's first D K-blocks are in flight at once.
-// Bound by the latency of a trip to memory and by what one CU loads: the product
-// 32x1536x7168 takes 5.1 us (16x16 tiles, 192 workgroups), 64x7168x2048 6.2 us,
-// 333x2500x1000 8.1 us, and the fused layer 1x1536x7168 6.5 us for 11 MB.
+// Bound by trips to memory one after the other, as many as a wave's share of the
+// K-blocks has of D, and by what one CU loads: the product 32x1536x7168 takes 5.1-5.3
+// us (16x16 tiles, 192 workgroups, 7 K-blocks in 2 slots), 64x7168x2048 6.2-7.0 us (2
+// in 1), 333x2500x1000 8.1 us, and the fused layer 1x1536x7168 6.3-6.5 us for 11 MB (7
+// in 3, of which the first 3 are on their way beside the quantisation).
 //
 // FUSED: the activations come as the quantiser's input and every workgroup
 // quantises all M <= 16 rows of it itself, while its first weights are on
@@ -1128,7 +1131,10 @@ float variant_us(const Variant& v, const GemmI8Args& a, int w, int cus) {
 // elements in every workgroup as much where M K, doubled for the gated input and
 // times the rounds of workgroups, is about 16384 (1x1536x7168 6.6 against 8.7 us,
 // 4x7168x2048 8.0 against 8.7, but 8x7168x2048 9.4 against 8.8 and 2x18432x7168
-// 30.8 against 29.4).
+// 30.8 against 29.4; gated 2x7168x2048 8.8 against 8.3 for twice its rows in two
+// launches, which from Python take 4 us more).
+// The rounds are those of 256 CUs, on any device: the workspace's size follows
+// from the same rule, and that has to be a function of the sizes alone.
 bool linear_i8_fused(int64_t M, int64_t N, int64_t K, bool gated) {
   if (M < 1 || M > 16 || K < 16 || M * K > kFusedCodes) return false;  // what the kernel has room for
   const int64_t rounds = ((N + 15) / 16 + 255) / 256;

@@ -345,7 +345,12 @@ struct Stream {
   }
 };
 
-// SiLU(g) * u, split into the two bf16 values hi + lo.
+// SiLU(g) * u, split into the two bf16 values hi + lo: 16 significant bits of it,
+// an error of 2^-17 each and 2.5e-6 of a sum over 2048 of them, where the output's
+// rounding to bf16 is 1.7e-3.  The two parts for eight tokens fill the sixteen
+// columns of one matrix instruction; a third part, for all 24 bits, would need a
+// second product per block, and products of their own for two parts already held
+// the stream of weights up.
 __device__ __forceinline__ void split_gate(float g, float u, uint16_t& hi, uint16_t& lo) {
   const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
   const float top = bf16_lo(pack_bf16x2(h, 0.0f));
@@ -355,9 +360,10 @@ __device__ __forceinline__ void split_gate(float g, float u, uint16_t& hi, uint1
 }
 
 // Bound by the weights' bytes.  256 experts of 7168 x 2048, e4m3, 8 per token: one
-// token 37 us for 235 MB (6.3 TB/s), 16 tokens (69 units) 312 us (6.5 TB/s); 64
-// tokens over 32 experts 86 us.  Rows that are not 16-byte aligned come through
-// registers: 5 tokens, 8 experts of 1000 x 714, 7.9 us.
+// token 37-39 us for 235 MB (6.0-6.3 TB/s; a read alone reaches 7.1), 16 tokens
+// (69 experts hit) 316 us (6.4 TB/s); 64 tokens, 17 of 32 experts hit, 83 us (6.0
+// TB/s).  Rows that are not 16-byte aligned come through registers: 5 tokens, 8
+// experts of 1000 x 714, 7.9-8.1 us.
 template <bool I8, bool DMA>
 __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(MoeFewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kUpWaves * kUpSlot];
@@ -516,7 +522,9 @@ __global__ __launch_bounds__(64 * kUpWaves, DMA ? 4 : 2) void moe_few_up_kernel(
 // `rows` output columns per workgroup in RT row tiles of 16 (rows a multiple of
 // 4); CT column tiles of 16 tokens.
 // Bound by the weights' bytes, and with one token by filling the CUs: for the
-// sizes above 24 us for 117 MB (4.9 TB/s), 174 us (5.8 TB/s), 70 us and 7.9 us.
+// sizes above 23-24 us for 117 MB (5.0 TB/s), 167 us (6.1 TB/s), 64 us (3.9 TB/s:
+// an expert of nine tokens or more is several units, whose weights pass through
+// LDS and are widened once for each) and 6.7-7.9 us.
 // Interleaving the units among the waves instead of consecutive ranges, two
 // K-blocks in flight per wave, and 16-row tiles with two workgroups per CU were
 // the same or slower.
