@@ -457,7 +457,8 @@ def _workspace(ws, need, t):
             return None, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=t.device)
         return ws, ws.data_ptr(), need
-    if not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != t.get_device():
+    if (not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous()
+            or ws.get_device() != t.get_device()):
         raise Dsfp8Error(f"workspace must be a contiguous uint8 tensor on {t.device}")
     return ws, ws.data_ptr(), ws.numel()
 

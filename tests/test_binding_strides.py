@@ -1,5 +1,5 @@
-"""The row strides that the binding passes on, from torch's strides (no GPU): torch gives a dimension of one element
-any stride, which says nothing about where the rows lie."""
+"""What the binding makes of its arguments (no GPU).  Row strides: torch gives a dimension of one element any stride,
+which says nothing about where the rows lie."""
 
 import pytest
 import torch
@@ -31,3 +31,9 @@ def test_stacked_row_stride():
         ds._expert_ld(whole[:, :2], "w")
     with pytest.raises(ds.Dsfp8Error):
         ds._expert_ld(whole[:, ::2], "w")
+
+
+@pytest.mark.parametrize("bad", [64, [0] * 64, torch.zeros(64, dtype=torch.uint8)])
+def test_workspace_that_is_no_device_tensor(bad):
+    with pytest.raises(ds.Dsfp8Error):
+        ds._workspace(bad, 16, torch.zeros(1))
