@@ -262,8 +262,8 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("T,E,k,D,Fh", [(3, 3, 2, 256, 144), (18, 2, 2, 512, 16), (2, 2, 1, 4224, 64), (3, 2, 1, 4112, 48),
-                                        (17, 2, 2, 5008, 16), (1, 1, 1, 16, 16)])
+@pytest.mark.parametrize("T,E,k,D,Fh", [(3, 3, 2, 256, 144), (18, 2, 2, 512, 16), (2, 2, 1, 4224, 64),
+                                        (3, 2, 1, 4112, 48), (17, 2, 2, 5008, 16), (1, 1, 1, 16, 16)])
 def test_row_tiles_past_the_last_row(T, E, k, D, Fh, fmt):
     """16-byte aligned weights whose last task of 32 rows, or last workgroup of up to 32 output columns, has 16 rows
     or fewer, so that its second tile of 16 rows lies past the matrix altogether."""

@@ -172,7 +172,7 @@ def same(c, want, buf=None, ld=0, offset=0):
     assert torch.equal(c, want), f"{int((c != want).sum())} of {c.numel()} elements differ"
     if buf is not None:
         between = buf[offset:offset + c.shape[0] * ld].view(c.shape[0], ld)[:, c.shape[1]:]
-        assert bool((between == 7.0).all()) and bool((buf[:offset] == 7.0).all()), "elements around the rows were written"
+        assert bool((between == 7.0).all()) and bool((buf[:offset] == 7.0).all()), "elements outside were written"
 
 
 @pytest.mark.gpu
