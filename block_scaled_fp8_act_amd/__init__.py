@@ -632,3 +632,296 @@ def moe_few(x, w13, w13_s, w2, w2_s, indices, weights, out=None, workspace=None)
             w2.data_ptr(), ld2, w2_s.data_ptr(), lds2, 1 if i8 else 0, indices.data_ptr(), _row(indices, k),
             weights.data_ptr(), _row(weights, k), T, k, E, D, F, out.data_ptr(), _row(out, D), wp, wn)
     return out
+
+
+# ---- MXFP4 ---------------------------------------------------------------------------------
+
+MX_BLOCK = 32
+_MX_VIEWS = tuple(getattr(torch, n) for n in ("float4_e2m1fn_x2", "float8_e8m0fnu") if hasattr(torch, n))
+
+
+def mxblocks(n):
+    return (int(n) + MX_BLOCK - 1) // MX_BLOCK
+
+
+def mxfp4_empty(M, K, device, lead=()):
+    """Storage for MXFP4 rows: codes uint8 ``[*lead, M, 16 * ceil(K/32)]`` and scale bytes uint8
+    ``[*lead, M, ceil(K/32)]`` whose rows are a multiple of 16 bytes apart, as the products read them."""
+    kb = mxblocks(K)
+    q = torch.empty((*lead, M, 16 * kb), dtype=torch.uint8, device=device)
+    s = torch.empty((*lead, M, (kb + 15) // 16 * 16), dtype=torch.uint8, device=device)
+    return q, (s if kb % 16 == 0 else s[..., :kb])
+
+
+def _mx(q, s, what, dim=2):
+    """Checked codes and scales of MXFP4 rows: ``(q, row stride, s, row stride)``."""
+    if isinstance(q, torch.Tensor) and q.dtype in _MX_VIEWS:
+        q = q.view(torch.uint8)
+    if isinstance(s, torch.Tensor) and s.dtype in _MX_VIEWS:
+        s = s.view(torch.uint8)
+    _need(q, what, torch.uint8, dim)
+    _need(s, what + "_s", torch.uint8, dim)
+    kb = s.shape[-1]
+    if q.shape[:-1] != s.shape[:-1] or q.shape[-1] != 16 * kb:
+        raise Dsfp8Error(f"{what} and {what}_s must be [..., 16 * blocks] and [..., blocks], got {tuple(q.shape)} and "
+                         f"{tuple(s.shape)}")
+    ldq, pad = _mx_ld(q, what), (kb + 15) & ~15
+    if s.numel() == 0:
+        return q, ldq, s, pad
+    rows = s.numel() // kb
+    lds = pad if rows == 1 else _mx_ld(s, what + "_s")
+    if lds % 16 or s.untyped_storage().nbytes() < s.storage_offset() + (rows - 1) * lds + pad:
+        raise Dsfp8Error(f"{what}_s: rows of scales must be a multiple of 16 bytes apart, with room for {pad} bytes "
+                         "each (mxfp4_empty allocates them so)")
+    if ldq % 16:
+        raise Dsfp8Error(f"{what}: rows of codes must be a multiple of 16 bytes apart")
+    return q, ldq, s, lds
+
+
+def _mx_ld(t, what):
+    return _row(t, t.shape[-1]) if t.dim() == 2 else _expert_ld(t, what)
+
+
+def _mx_out(out, M, K, device):
+    if out is None:
+        return mxfp4_empty(M, K, device)
+    q, s = out
+    kb = mxblocks(K)
+    _mat(q, "y", (torch.uint8,))
+    _mat(s, "s", (torch.uint8,))
+    if q.shape != (M, 16 * kb) or s.shape != (M, kb) or q.device != device or s.device != device:
+        raise Dsfp8Error(f"out must be uint8 {(M, 16 * kb)} and {(M, kb)} on {device}, got {tuple(q.shape)} on "
+                         f"{q.device} and {tuple(s.shape)} on {s.device}")
+    return q, s
+
+
+def mxfp4_quant(x, out=None):
+    """Quantise fp32 or bf16 ``x [M, K]`` to MXFP4, in blocks of 32 columns.
+
+    Returns ``(q uint8 [M, 16 * ceil(K/32)], s uint8 [M, ceil(K/32)])``: two e2m1
+    codes a byte, the lower column in the low half (columns past K hold 0), and a
+    scale byte per block, for x ~= code * 2^(s - 127).  ``out`` may supply ``(q,
+    s)`` as :func:`mxfp4_empty` gives them."""
+    _mat(x, "x", (torch.float32, torch.bfloat16))
+    M, K = x.shape
+    q, s = _mx_out(out, M, K, x.device)
+    _, ldq, _, lds = _mx(q, s, "y")
+    _launch("mxfp4_quant", _lib.load().dsfp8_mxfp4_quant, x.get_device(), x.data_ptr(),
+            0 if x.dtype == torch.float32 else 1, M, K, _row(x, K), q.data_ptr(), ldq, s.data_ptr(), lds)
+    return q, s
+
+
+def silu_mul_mxfp4_quant(g, u, out=None):
+    """``mxfp4_quant(SiLU(g) * u)`` in one pass over bf16 ``g`` and ``u`` (the gate is
+    evaluated in fp32 and not rounded before the quantisation)."""
+    _gate_pair(g, u)
+    M, K = g.shape
+    q, s = _mx_out(out, M, K, g.device)
+    _, ldq, _, lds = _mx(q, s, "y")
+    _launch("silu_mul_mxfp4_quant", _lib.load().dsfp8_silu_mul_mxfp4_quant, g.get_device(), g.data_ptr(), _row(g, K),
+            u.data_ptr(), _row(u, K), M, K, q.data_ptr(), ldq, s.data_ptr(), lds)
+    return q, s
+
+
+def mxfp4_dequant(q, s, K=None, out=None):
+    """bf16 ``[M, K]``: the values of MXFP4 rows (K: their columns, by default all of their blocks')."""
+    q, ldq, s, lds = _mx(q, s, "q")
+    M, kb = s.shape
+    K = MX_BLOCK * kb if K is None else int(K)
+    if mxblocks(K) != kb:
+        raise Dsfp8Error(f"{kb} blocks hold {MX_BLOCK * (kb - 1) + 1} to {MX_BLOCK * kb} columns, not {K}")
+    _same_device(q.get_device(), s=s)
+    out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device) if out is None else _out(
+        out, (M, K), torch.bfloat16, q.device, "out")
+    _launch("mxfp4_dequant", _lib.load().dsfp8_mxfp4_dequant, q.get_device(), q.data_ptr(), ldq, s.data_ptr(), lds, M, K,
+            out.data_ptr(), _row(out, K))
+    return out
+
+
+def gemm_mxfp4(a, a_s, b, b_s, out=None):
+    """bf16 ``C [M, N] = A W^T`` of MXFP4 rows ``(a, a_s)`` and an MXFP4 weight of N rows ``(b, b_s)``, both as
+    :func:`mxfp4_quant` returns them."""
+    a, lda, a_s, ldas = _mx(a, a_s, "a")
+    b, ldb, b_s, ldbs = _mx(b, b_s, "b")
+    M, kb = a_s.shape
+    N = b_s.shape[0]
+    if b_s.shape[1] != kb:
+        raise Dsfp8Error(f"a and b disagree on K: {kb} vs {b_s.shape[1]} blocks")
+    dev = a.get_device()
+    _same_device(dev, a_s=a_s, b=b, b_s=b_s)
+    c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device) if out is None else _out(
+        out, (M, N), torch.bfloat16, a.device, "out")
+    _launch("gemm_mxfp4", _lib.load().dsfp8_gemm_mxfp4, dev, a.data_ptr(), lda, a_s.data_ptr(), ldas, b.data_ptr(), ldb,
+            b_s.data_ptr(), ldbs, c.data_ptr(), _row(c, N), M, N, MX_BLOCK * kb)
+    return c
+
+
+def linear_mxfp4_workspace_bytes(M, N, K):
+    """Bytes of ``workspace`` that :func:`linear_mxfp4` needs; 0 for few rows."""
+    return _lib.load().dsfp8_linear_mxfp4_workspace_bytes(M, N, K)
+
+
+def linear_mxfp4(x, w, w_s, out=None, workspace=None):
+    """bf16 ``[M, N]``: ``gemm_mxfp4(*mxfp4_quant(x), w, w_s)`` in one call, for bf16 ``x [M, K]`` and an MXFP4
+    weight of N rows (as ``mxfp4_quant`` of the real weight gives it)."""
+    _need(x, "x", torch.bfloat16)
+    w, ldw, w_s, ldws = _mx(w, w_s, "w")
+    M, K = x.shape
+    N = w_s.shape[0]
+    if w_s.shape[1] != mxblocks(K):
+        raise Dsfp8Error(f"x has {K} columns, {mxblocks(K)} blocks, and w {w_s.shape[1]} blocks")
+    dev = x.get_device()
+    if w.get_device() != dev or w_s.get_device() != dev:
+        _same_device(dev, w=w, w_s=w_s)
+    lib = _lib.load()
+    c = x.new_empty((M, N)) if out is None else _out(out, (M, N), torch.bfloat16, x.device, "out")
+    ws, wp, wn = _workspace(workspace, lib.dsfp8_linear_mxfp4_workspace_bytes(M, N, K), x)
+    _launch("linear_mxfp4", lib.dsfp8_linear_mxfp4, dev, x.data_ptr(), _row(x, K), w.data_ptr(), ldw, w_s.data_ptr(), ldws,
+            c.data_ptr(), _row(c, N), M, N, K, wp, wn)
+    return c
+
+
+def _int32_vec(t, n, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise Dsfp8Error(f"{name} must be a contiguous 1-D int32 CUDA tensor")
+    if n is not None and t.numel() != n:
+        raise Dsfp8Error(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def grouped_gemm_mxfp4(a, a_s, b, b_s, offsets, rows=None, out=None):
+    """:func:`gemm_mxfp4` over per-expert row ranges: product rows ``offsets[e]:offsets[e+1]`` use the weight
+    ``(b[e], b_s[e])``, codes ``[E, N, 16 * blocks]`` and scales ``[E, N, blocks]``; ``offsets`` int32 ``[E+1]`` on
+    the device.  With ``rows`` (int32 ``[M_total]``) product row r reads row ``rows[r]`` of ``a`` (clamped), so the
+    tokens' quantised rows feed the experts without a gathered copy.  Returns bf16 ``[M_total, N]``; rows past
+    ``offsets[E]`` are left as they were (unspecified in a new output)."""
+    a, lda, a_s, ldas = _mx(a, a_s, "a")
+    b, ldb, b_s, ldbs = _mx(b, b_s, "b", dim=3)
+    E, N, kb = b_s.shape
+    if a_s.shape[1] != kb:
+        raise Dsfp8Error(f"a and b disagree on K: {a_s.shape[1]} vs {kb} blocks")
+    _int32_vec(offsets, E + 1, "offsets")
+    M = a.shape[0]
+    dev = a.get_device()
+    _same_device(dev, a_s=a_s, b=b, b_s=b_s, offsets=offsets)
+    if rows is not None:
+        _int32_vec(rows, None, "rows")
+        _same_device(dev, rows=rows)
+        M = rows.numel()
+    c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device) if out is None else _out(
+        out, (M, N), torch.bfloat16, a.device, "out")
+    _launch("grouped_gemm_mxfp4", _lib.load().dsfp8_grouped_gemm_mxfp4, dev, a.data_ptr(), a.shape[0], lda,
+            a_s.data_ptr(), ldas, rows.data_ptr() if rows is not None else None, b.data_ptr(), ldb, b_s.data_ptr(), ldbs,
+            offsets.data_ptr(), E, M, N, MX_BLOCK * kb, c.data_ptr(), _row(c, N))
+    return c
+
+
+# ---- the choice of experts -------------------------------------------------------------------
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def moe_gate(logits, k, bias=None, score="sigmoid", groups=1, top_groups=None, renormalize=True, scale=1.0, out=None):
+    """The experts of each token: ``(indices int32 [T, k], weights bf16 [T, k])``, as the routed-expert calls take
+    them, from the router's ``logits`` (fp32 or bf16 ``[T, E]``).
+
+    ``score`` is "sigmoid" or "softmax"; ``bias`` (fp32 ``[E]``) is added for the choice alone.  With ``groups`` > 1
+    only the experts of the ``top_groups`` best of ``groups`` equal groups are considered (a group's score: its best
+    expert's, with a bias the sum of its two best).  Experts come in decreasing order, the lowest index first among
+    equals.  ``weights`` are the chosen experts' scores times ``scale``, divided by their sum if ``renormalize``.
+    An expert with a logit of -inf is never chosen; slots without an expert hold index -1 and weight 0."""
+    if not _is_mat(logits, torch.float32):
+        _mat(logits, "logits", (torch.float32, torch.bfloat16))
+    if score not in _SCORES:
+        raise Dsfp8Error(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    T, E = logits.shape
+    dev = logits.get_device()
+    if bias is not None:
+        _vec_f32(bias, E, "bias")
+        _same_device(dev, bias=bias)
+    if out is None:
+        indices, weights = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.bfloat16)
+    else:
+        indices = _out(out[0], (T, k), torch.int32, logits.device, "indices")
+        weights = _out(out[1], (T, k), torch.bfloat16, logits.device, "weights")
+    _launch("moe_gate", _lib.load().dsfp8_moe_gate, dev, logits.data_ptr(), 0 if logits.dtype == torch.float32 else 1,
+            _row(logits, E), bias.data_ptr() if bias is not None else None, T, E, k, groups,
+            groups if top_groups is None else top_groups, _SCORES[score], 1 if renormalize else 0, scale,
+            indices.data_ptr(), _row(indices, k), weights.data_ptr(), _row(weights, k))
+    return indices, weights
+
+
+# ---- norms around a residual connection --------------------------------------------------------
+
+_NORM_FMT = {None: 0, "e4m3": 1, "e4m3_ue8m0": 2, "mxfp4": 3}
+
+
+def _norm_weight(w, D, name, dtype):
+    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != dtype or w.shape != (D,) or (D > 1 and w.stride(0) != 1):
+        raise Dsfp8Error(f"{name} must be a {dtype} CUDA tensor of shape ({D},) with stride 1")
+
+
+def add_rms_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.0, eps=1e-6, quant=None, out=None):
+    """``y = rmsnorm(h) * weight`` with ``h = residual + scale * gate * t`` and ``t = x`` or, with ``post_weight``,
+    ``rmsnorm(x) * post_weight``: the norm after a block (optional), its residual connection, and the norm before the
+    next block, in one pass.  Without ``residual``, ``h = x`` (and no post_weight, gate or scale).
+
+    ``x``, ``residual`` bf16 ``[T, D]``; ``gate`` bf16 ``[T, D]`` or ``[D]``; the weights ``[D]``, both bf16 or both
+    fp32.  ``quant``: None for a bf16 y, "e4m3" or "e4m3_ue8m0" for :func:`act_quant`'s codes and scales of y, "mxfp4"
+    for :func:`mxfp4_quant`'s.  Returns ``y`` or ``(y, s)``, followed by the new residual stream h (bf16) if there is
+    a ``residual``.  ``out`` may supply the same tuple (``(y,)`` for y alone); its h may be ``residual`` itself."""
+    _need(x, "x", torch.bfloat16)
+    T, D = x.shape
+    dev = x.get_device()
+    if quant not in _NORM_FMT:
+        raise Dsfp8Error(f"quant must be one of {list(_NORM_FMT)}, got {quant!r}")
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise Dsfp8Error("weight must be a bfloat16 or float32 tensor")
+    _norm_weight(weight, D, "weight", weight.dtype)
+    _same_device(dev, weight=weight)
+    rp = gp = pp = None
+    ldr = ldg = 0
+    if post_weight is not None:
+        _norm_weight(post_weight, D, "post_weight", weight.dtype)
+        _same_device(dev, post_weight=post_weight)
+        pp = post_weight.data_ptr()
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16)
+        if residual.shape != x.shape:
+            raise Dsfp8Error(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
+        _same_device(dev, residual=residual)
+        rp, ldr = residual.data_ptr(), _row(residual, D)
+    if gate is not None:
+        g = gate[None] if isinstance(gate, torch.Tensor) and gate.dim() == 1 else gate
+        _need(g, "gate", torch.bfloat16)
+        if g.shape != (1 if gate.dim() == 1 else T, D):
+            raise Dsfp8Error(f"gate must be {(T, D)} or {(D,)}, got {tuple(gate.shape)}")
+        _same_device(dev, gate=gate)
+        gp = g.data_ptr()
+        ldg = 0 if gate.dim() == 1 or (T > 1 and g.stride(0) == 0) else _row(g, D)
+    want = (1 if quant is None else 2) + (residual is not None)
+    o = (None,) * want if out is None else tuple(out)
+    if len(o) != want:
+        raise Dsfp8Error(f"out must hold {want} tensors, got {len(o)}")
+    s, sp, srs, sks = None, None, 0, 0
+    if quant is None:
+        y = x.new_empty((T, D)) if o[0] is None else _out(o[0], (T, D), torch.bfloat16, x.device, "y")
+        ldy = _row(y, D)
+    elif quant == "mxfp4":
+        y, s = _mx_out(None if o[0] is None else o[:2], T, D, x.device)
+        _, ldy, _, srs = _mx(y, s, "y")
+        sp, sks = s.data_ptr(), 1
+    else:
+        y = _out(o[0], (T, D), torch.uint8, x.device, "y")
+        s = _scales_out(o[1], T, kblocks(D), x.device)
+        ldy = _row(y, D)
+        sp, (srs, sks) = s.data_ptr(), _scale_strides(s)
+    hp, h, ldh = None, None, 0
+    if residual is not None:
+        h = x.new_empty((T, D)) if o[-1] is None else _out(o[-1], (T, D), torch.bfloat16, x.device, "h")
+        hp, ldh = h.data_ptr(), _row(h, D)
+    _launch("add_rms_norm", _lib.load().dsfp8_add_rms_norm, dev, x.data_ptr(), _row(x, D), rp, ldr, gp, ldg, pp,
+            weight.data_ptr(), 0 if weight.dtype == torch.float32 else 1, scale, eps, T, D, hp, ldh, y.data_ptr(), ldy,
+            _NORM_FMT[quant], sp, srs, sks)
+    got = (y,) if s is None else (y, s)
+    got = got if h is None else got + (h,)
+    return got if len(got) > 1 else y

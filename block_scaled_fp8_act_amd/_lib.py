@@ -10,6 +10,7 @@ _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_f = ctypes.c_float
 
 # name -> (restype, argtypes), in header order.
 SIGNATURES = {
@@ -49,6 +50,17 @@ SIGNATURES = {
     "dsfp8_moe_few": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i64, _p, _i64, _i64, _i64,
                            _i64, _i64, _i64, _p, _i64, _p, _sz, _p]),
     "dsfp8_moe_few_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dsfp8_mxfp4_quant": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p]),
+    "dsfp8_silu_mul_mxfp4_quant": (_i, [_p, _i64, _p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p]),
+    "dsfp8_mxfp4_dequant": (_i, [_p, _i64, _p, _i64, _i64, _i64, _p, _i64, _p]),
+    "dsfp8_gemm_mxfp4": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p]),
+    "dsfp8_linear_mxfp4": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _sz, _p]),
+    "dsfp8_linear_mxfp4_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dsfp8_grouped_gemm_mxfp4": (_i, [_p, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64,
+                                      _p, _i64, _p]),
+    "dsfp8_moe_gate": (_i, [_p, _i, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i, _i, _f, _p, _i64, _p, _i64, _p]),
+    "dsfp8_add_rms_norm": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i, _f, _f, _i64, _i64, _p, _i64, _p, _i64, _i,
+                                _p, _i64, _i64, _p]),
 }
 
 _lib = None

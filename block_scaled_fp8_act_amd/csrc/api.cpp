@@ -96,6 +96,7 @@ const char* dsfp8_status_string(dsfp8_status st) {
     case DSFP8_ERR_DTYPE: return "unknown element type";
     case DSFP8_ERR_UNSUPPORTED: return "the fused form does not support this operand layout";
     case DSFP8_ERR_SCRATCH: return "the problem needs more scratch than the library's static buffer holds";
+    case DSFP8_ERR_SCORE: return "unknown score function";
     default: return "unknown status";
   }
 }
@@ -732,6 +733,243 @@ dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx, const void* W13, int64_t 
   a.ldo = ldo;
   a.work = workspace;
   return launched(dsfp8::launch_moe_few(a, stream));
+}
+
+// ---- MXFP4 ------------------------------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMxMaxLd = (int64_t)1 << 23;  // a tile's rows within one 32-bit descriptor
+
+inline int64_t mx_blocks(int64_t K) { return (K + 31) / 32; }
+inline int64_t mx_pad(int64_t K) { return (mx_blocks(K) + 15) / 16 * 16; }  // bytes of a row of scales
+
+// Codes and scales of `rows` rows of K columns.
+dsfp8_status check_mx(const void* q, int64_t ldq, const void* s, int64_t lds, int64_t rows, int64_t K) {
+  if (ldq % 16 != 0 || lds % 16 != 0) return DSFP8_ERR_LD;
+  DSFP8_TRY(check_mat(q, rows, 16 * mx_blocks(K), ldq, 16));
+  return check_mat(s, rows, mx_pad(K), lds, 16);
+}
+
+dsfp8_status mx_quant_args(const void* x, bool f32, int64_t ldx, const void* u, int64_t ldu, int64_t M, int64_t K,
+                           void* y, int64_t ldy, void* s, int64_t lds, dsfp8::MxQuantArgs& a) {
+  DSFP8_TRY(check_mat(x, M, K, ldx, f32 ? 4 : 2));
+  if (u != nullptr) DSFP8_TRY(check_mat(u, M, K, ldu, 2));
+  DSFP8_TRY(check_mx(y, ldy, s, lds, M, K));
+  a = dsfp8::MxQuantArgs{};
+  a.x = x;
+  a.f32 = f32;
+  a.ldx = ldx;
+  a.u = static_cast<const uint16_t*>(u);
+  a.ldu = ldu;
+  a.M = M;
+  a.K = K;
+  a.y = static_cast<uint8_t*>(y);
+  a.ldy = ldy;
+  a.s = static_cast<uint8_t*>(s);
+  a.lds = lds;
+  return DSFP8_OK;
+}
+
+dsfp8_status mx_gemm_args(const void* A, int64_t a_rows, int64_t lda, const void* a_s, int64_t ldas, const void* B,
+                          int64_t ldb, const void* b_s, int64_t ldbs, int64_t b_rows, void* C, int64_t ldc, int64_t M,
+                          int64_t N, int64_t K, dsfp8::MxGemmArgs& a) {
+  DSFP8_TRY(check_mx(A, lda, a_s, ldas, a_rows, K));
+  DSFP8_TRY(check_mx(B, ldb, b_s, ldbs, b_rows, K));
+  DSFP8_TRY(check_mat(C, M, N, ldc, 2));
+  if (lda >= kMxMaxLd || ldb >= kMxMaxLd || ldas >= kMxMaxLd || ldbs >= kMxMaxLd) return DSFP8_ERR_UNSUPPORTED;
+  a = dsfp8::MxGemmArgs{};
+  a.A = static_cast<const uint8_t*>(A);
+  a.lda = lda;
+  a.a_s = static_cast<const uint8_t*>(a_s);
+  a.ldas = ldas;
+  a.B = static_cast<const uint8_t*>(B);
+  a.ldb = ldb;
+  a.b_s = static_cast<const uint8_t*>(b_s);
+  a.ldbs = ldbs;
+  a.C = static_cast<uint16_t*>(C);
+  a.ldc = ldc;
+  a.M = M;
+  a.N = N;
+  a.KB = mx_blocks(K);
+  a.a_rows = a_rows;
+  return DSFP8_OK;
+}
+
+}  // namespace
+
+dsfp8_status dsfp8_mxfp4_quant(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx, void* y, int64_t ldy,
+                               void* s, int64_t lds, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
+  if (dtype != DSFP8_DTYPE_F32 && dtype != DSFP8_DTYPE_BF16) return DSFP8_ERR_DTYPE;
+  dsfp8::MxQuantArgs a;
+  DSFP8_TRY(mx_quant_args(x, dtype == DSFP8_DTYPE_F32, ldx, nullptr, 0, M, K, y, ldy, s, lds, a));
+  return launched(dsfp8::launch_mx_quant(a, stream));
+}
+
+dsfp8_status dsfp8_silu_mul_mxfp4_quant(const void* g, int64_t ldg, const void* u, int64_t ldu, int64_t M, int64_t I,
+                                        void* y, int64_t ldy, void* s, int64_t lds, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(I)) return DSFP8_ERR_SHAPE;
+  if (u == nullptr && M > 0 && I > 0) return DSFP8_ERR_NULL;
+  dsfp8::MxQuantArgs a;
+  DSFP8_TRY(mx_quant_args(g, false, ldg, u, ldu, M, I, y, ldy, s, lds, a));
+  return launched(dsfp8::launch_mx_quant(a, stream));
+}
+
+dsfp8_status dsfp8_mxfp4_dequant(const void* q, int64_t ldq, const void* s, int64_t lds, int64_t M, int64_t K,
+                                 void* out, int64_t ldo, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
+  DSFP8_TRY(check_mx(q, ldq, s, lds, M, K));
+  DSFP8_TRY(check_mat(out, M, K, ldo, 2));
+  dsfp8::MxDequantArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.ldq = ldq;
+  a.s = static_cast<const uint8_t*>(s);
+  a.lds = lds;
+  a.M = M;
+  a.K = K;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  return launched(dsfp8::launch_mx_dequant(a, stream));
+}
+
+dsfp8_status dsfp8_gemm_mxfp4(const void* A, int64_t lda, const void* a_s, int64_t ldas, const void* B, int64_t ldb,
+                              const void* b_s, int64_t ldbs, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                              hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
+  dsfp8::MxGemmArgs a;
+  DSFP8_TRY(mx_gemm_args(A, M, lda, a_s, ldas, B, ldb, b_s, ldbs, N, C, ldc, M, N, K, a));
+  return launched(dsfp8::launch_mx_gemm(a, stream));
+}
+
+size_t dsfp8_linear_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K) || 16 * mx_blocks(K) >= kMxMaxLd) return 0;
+  if (dsfp8::linear_mx_fused(M, N, K)) return 0;
+  return (size_t)(M * (16 * mx_blocks(K) + mx_pad(K)));
+}
+
+dsfp8_status dsfp8_linear_mxfp4(const void* x, int64_t ldx, const void* B, int64_t ldb, const void* b_s, int64_t ldbs,
+                                void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
+  DSFP8_TRY(check_mat(x, M, K, ldx, 2));
+  const bool fused = dsfp8::linear_mx_fused(M, N, K);
+  const size_t need = dsfp8_linear_mxfp4_workspace_bytes(M, N, K);
+  if (workspace_bytes < need) return DSFP8_ERR_WORKSPACE;
+  if (workspace == nullptr && need > 0) return DSFP8_ERR_NULL;
+  if (!al(workspace, 16)) return DSFP8_ERR_ALIGN;
+  const int64_t ldy = 16 * mx_blocks(K), lds = mx_pad(K), rows = fused ? 0 : M;
+  uint8_t* y = static_cast<uint8_t*>(workspace);
+  uint8_t* s = y + rows * ldy;
+  dsfp8::MxGemmArgs g;
+  DSFP8_TRY(mx_gemm_args(y, rows, ldy, s, lds, B, ldb, b_s, ldbs, N, C, ldc, M, N, K, g));
+  dsfp8::MxQuantArgs q;
+  DSFP8_TRY(mx_quant_args(x, false, ldx, nullptr, 0, rows, K, y, ldy, s, lds, q));
+  q.M = M;
+  if (M == 0 || N == 0) return DSFP8_OK;
+  if (fused) return launched(dsfp8::launch_linear_mx_fused(g, q, stream));
+  const dsfp8_status st = launched(dsfp8::launch_mx_quant(q, stream));
+  return st == DSFP8_OK ? launched(dsfp8::launch_mx_gemm(g, stream)) : st;
+}
+
+dsfp8_status dsfp8_grouped_gemm_mxfp4(const void* A, int64_t a_rows, int64_t lda, const void* a_s, int64_t ldas,
+                                      const int32_t* rows, const void* B, int64_t ldb, const void* b_s, int64_t ldbs,
+                                      const int32_t* offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
+                                      void* C, int64_t ldc, hipStream_t stream) {
+  if (!dim_ok(a_rows) || !dim_ok(M_total) || !dim_ok(N) || !dim_ok(K) || E < 1 || E > kMaxExperts)
+    return DSFP8_ERR_SHAPE;
+  if (M_total > 0 && a_rows < (rows != nullptr ? 1 : M_total)) return DSFP8_ERR_SHAPE;
+  if (offsets == nullptr) return DSFP8_ERR_NULL;
+  if (!al(offsets, 4) || !al(rows, 4)) return DSFP8_ERR_ALIGN;
+  dsfp8::MxGemmArgs a;
+  DSFP8_TRY(mx_gemm_args(A, a_rows, lda, a_s, ldas, B, ldb, b_s, ldbs, E * N, C, ldc, M_total, N, K, a));
+  if (rows != nullptr && a_rows * (lda > ldas ? lda : ldas) >= kMaxDim) return DSFP8_ERR_UNSUPPORTED;
+  a.offsets = offsets;
+  a.E = E;
+  a.rows = rows;
+  return launched(dsfp8::launch_mx_gemm(a, stream));
+}
+
+// ---- gate -------------------------------------------------------------------------------
+
+dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const float* bias, int64_t T, int64_t E,
+                            int64_t k, int64_t groups, int64_t top_groups, int score, int renormalize, float scale,
+                            int32_t* indices, int64_t ldi, void* weights, int64_t ldw, hipStream_t stream) {
+  if (dtype != DSFP8_DTYPE_F32 && dtype != DSFP8_DTYPE_BF16) return DSFP8_ERR_DTYPE;
+  if (score != DSFP8_SCORE_SIGMOID && score != DSFP8_SCORE_SOFTMAX) return DSFP8_ERR_SCORE;
+  if (!dim_ok(T) || E < 1 || E > dsfp8::kMaxRouteExperts || k < 1 || k > 16) return DSFP8_ERR_SHAPE;
+  if (groups < 1 || groups > 64 || E % groups != 0 || top_groups < 1 || top_groups > groups) return DSFP8_ERR_SHAPE;
+  if (k > top_groups * (E / groups)) return DSFP8_ERR_SHAPE;
+  DSFP8_TRY(check_mat(logits, T, E, ldl, dtype == DSFP8_DTYPE_F32 ? 4 : 2));
+  DSFP8_TRY(check_mat(indices, T, k, ldi, 4));
+  DSFP8_TRY(check_mat(weights, T, k, ldw, 2));
+  if (!al(bias, 4)) return DSFP8_ERR_ALIGN;
+  dsfp8::GateArgs a{};
+  a.logits = logits;
+  a.bf16_in = dtype == DSFP8_DTYPE_BF16;
+  a.ldl = ldl;
+  a.bias = bias;
+  a.T = T;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.groups = (int)groups;
+  a.top_groups = (int)top_groups;
+  a.softmax = score == DSFP8_SCORE_SOFTMAX;
+  a.renormalize = renormalize != 0;
+  a.scale = scale;
+  a.indices = indices;
+  a.ldi = ldi;
+  a.weights = static_cast<uint16_t*>(weights);
+  a.ldw = ldw;
+  return launched(dsfp8::launch_gate(a, stream));
+}
+
+// ---- norm -------------------------------------------------------------------------------
+
+dsfp8_status dsfp8_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* gate,
+                                int64_t ldg, const void* post_weight, const void* weight, int w_dtype, float scale,
+                                float eps, int64_t T, int64_t D, void* h, int64_t ldh, void* y, int64_t ldy, int y_fmt,
+                                void* s, int64_t s_row_stride, int64_t s_kb_stride, hipStream_t stream) {
+  if (w_dtype != DSFP8_DTYPE_F32 && w_dtype != DSFP8_DTYPE_BF16) return DSFP8_ERR_DTYPE;
+  if (y_fmt < DSFP8_NORM_BF16 || y_fmt > DSFP8_NORM_MXFP4) return DSFP8_ERR_DTYPE;
+  if (!dim_ok(T) || D < 0 || D > 65536 || !(eps >= 0.0f)) return DSFP8_ERR_SHAPE;
+  if (residual == nullptr && T > 0 && D > 0 && (post_weight != nullptr || gate != nullptr || scale != 1.0f))
+    return DSFP8_ERR_SHAPE;
+  DSFP8_TRY(check_mat(x, T, D, ldx, 2));
+  if (residual != nullptr) {
+    DSFP8_TRY(check_mat(residual, T, D, ldr, 2));
+    DSFP8_TRY(check_mat(h, T, D, ldh, 2));
+    if (gate != nullptr) DSFP8_TRY(check_mat(gate, ldg == 0 ? 1 : T, D, ldg == 0 ? D : ldg, 2));
+  }
+  const size_t wb = w_dtype == DSFP8_DTYPE_F32 ? 4 : 2;
+  DSFP8_TRY(check_mat(weight, T, D, D, wb));
+  if (!al(post_weight, wb)) return DSFP8_ERR_ALIGN;
+  if (y_fmt == DSFP8_NORM_BF16) DSFP8_TRY(check_mat(y, T, D, ldy, 2));
+  else if (y_fmt == DSFP8_NORM_MXFP4) DSFP8_TRY(check_mx(y, ldy, s, s_row_stride, T, D));
+  else DSFP8_TRY(check_quant_out(T, D, y, ldy, static_cast<float*>(s), s_row_stride, s_kb_stride));
+  dsfp8::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ldr = ldr;
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.ldg = ldg;
+  a.post_w = post_weight;
+  a.w = weight;
+  a.w_f32 = w_dtype == DSFP8_DTYPE_F32;
+  a.scale = scale;
+  a.eps = eps;
+  a.T = T;
+  a.D = D;
+  a.h = static_cast<uint16_t*>(h);
+  a.ldh = ldh;
+  a.y = y;
+  a.ldy = ldy;
+  a.fmt = y_fmt;
+  a.s = s;
+  a.s_rs = s_row_stride;
+  a.s_ks = s_kb_stride;
+  return launched(dsfp8::launch_norm(a, stream));
 }
 
 }  // extern "C"

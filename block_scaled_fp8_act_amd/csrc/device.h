@@ -160,12 +160,58 @@ __device__ __forceinline__ float max_row16(float v) {
   return v;
 }
 
+// The same of unsigned integers.
+__device__ __forceinline__ uint32_t max_row16_u32(uint32_t v) {
+  auto over = [&](int o) __attribute__((always_inline)) { v = (uint32_t)o > v ? (uint32_t)o : v; };
+  over(__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, false));
+  over(__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, false));
+  over(__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));
+  over(__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false));
+  return v;
+}
+
 // Maximum over the whole wavefront (64 lanes), returned in every lane.
 __device__ __forceinline__ float max_wave(float v) {
   v = max_row16(v);
   v = fmaxf(v, __shfl_xor(v, 16));
   v = fmaxf(v, __shfl_xor(v, 32));
   return v;
+}
+
+// ---- MXFP4: blocks of 32 columns ----------------------------------------------------
+
+// Scale byte of a block from its largest |x| as a bit pattern (the exponent
+// field minus 2; 255, NaN, for a block with a NaN or an infinity), and the
+// scale itself (2^-127 is not a normal number, but the conversions take it).
+__device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
+  const uint32_t f = top >> 23;
+  return f == 255 ? 255u : (f > 2 ? f - 2 : 0u);
+}
+__device__ __forceinline__ float mx_scale_f32(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
+
+// The largest |v| as a bit pattern over a lane's 8 values and the 4 lanes (an
+// aligned quad) that share a block.
+__device__ __forceinline__ uint32_t mx_quad_top(const float (&v)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+    top = b > top ? b : top;
+  }
+  auto over = [&](int o) __attribute__((always_inline)) { top = (uint32_t)o > top ? (uint32_t)o : top; };
+  over(__builtin_amdgcn_update_dpp(0, (int)top, 0xb1, 0xf, 0xf, false));  // quad_perm [1,0,3,2]
+  over(__builtin_amdgcn_update_dpp(0, (int)top, 0x4e, 0xf, 0xf, false));  // quad_perm [2,3,0,1]
+  return top;
+}
+
+// Eight codes of v / scale, nearest-even and saturating, the lower column of a
+// pair in the low half of its byte.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float scale) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
 }
 
 }  // namespace dsfp8

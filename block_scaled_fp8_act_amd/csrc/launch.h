@@ -178,6 +178,98 @@ struct MoeFewArgs {
   void* work;
 };
 
+// MXFP4 quantisation of rows: blocks of 32 columns, one scale byte each.
+struct MxQuantArgs {
+  const void* x;       // fp32 or bf16 input (bf16 gate input when u != nullptr)
+  bool f32;
+  int64_t ldx;
+  const uint16_t* u;   // bf16 up-projection input of the gated form, or nullptr
+  int64_t ldu;
+  int64_t M, K;
+  uint8_t* y;          // [M, 16 ceil(K / 32)], row stride ldy in bytes
+  int64_t ldy;
+  uint8_t* s;          // [M, ceil(K / 32)], row stride lds
+  int64_t lds;
+};
+
+struct MxDequantArgs {
+  const uint8_t* q;
+  int64_t ldq;
+  const uint8_t* s;
+  int64_t lds;
+  int64_t M, K;
+  uint16_t* out;
+  int64_t ldo;
+};
+
+// Product of MXFP4 matrices of KB blocks a row; strides in bytes (C: elements).
+struct MxGemmArgs {
+  const uint8_t* A;
+  int64_t lda;
+  const uint8_t* a_s;
+  int64_t ldas;
+  const uint8_t* B;
+  int64_t ldb;
+  const uint8_t* b_s;
+  int64_t ldbs;
+  uint16_t* C;
+  int64_t ldc;
+  int64_t M, N, KB;
+  // grouped form: experts' row ranges, weights N * ldb and N * ldbs bytes apart
+  const int32_t* offsets;
+  int64_t E;
+  const int32_t* rows;  // product row r reads row rows[r] of A (clamped to [0, a_rows)), or nullptr
+  int64_t a_rows;
+};
+
+// Choice of a token's experts.
+struct GateArgs {
+  const void* logits;  // fp32 or bf16 [T, E]
+  bool bf16_in;
+  int64_t ldl;
+  const float* bias;   // [E] or nullptr
+  int64_t T;
+  int E, k, groups, top_groups;
+  bool softmax, renormalize;
+  float scale;
+  int32_t* indices;
+  int64_t ldi;
+  uint16_t* weights;
+  int64_t ldw;
+};
+
+// Norms around a residual connection.
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;  // or nullptr: h = x, and no h is written
+  int64_t ldr;
+  const uint16_t* gate;      // or nullptr
+  int64_t ldg;               // 0: one row for all tokens
+  const void* post_w;        // or nullptr
+  const void* w;
+  bool w_f32;
+  float scale, eps;
+  int64_t T, D;
+  uint16_t* h;
+  int64_t ldh;
+  void* y;
+  int64_t ldy;
+  int fmt;
+  void* s;
+  int64_t s_rs, s_ks;
+};
+
+hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t stream);
+hipError_t launch_mx_dequant(const MxDequantArgs& a, hipStream_t stream);
+hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
+// Quantisation and product in one launch, where linear_mx_fused says so; the
+// product's A and a_s are then not used.
+bool linear_mx_fused(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_mx_fused(const MxGemmArgs& g, const MxQuantArgs& q, hipStream_t stream);
+hipError_t launch_gate(const GateArgs& a, hipStream_t stream);
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
 // Which kernel serves a product: dsfp8_i8_variant's four numbers.
 struct I8Variant {
   int kind, rows, columns, feed;

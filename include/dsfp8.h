@@ -62,7 +62,7 @@
 extern "C" {
 #endif
 
-#define DSFP8_ABI_VERSION 8
+#define DSFP8_ABI_VERSION 9
 #define DSFP8_BLOCK 128
 
 typedef int dsfp8_status;
@@ -78,8 +78,9 @@ enum {
   DSFP8_ERR_LAUNCH = -7,     /* the HIP runtime reported a launch failure         */
   DSFP8_ERR_DTYPE = -8,      /* unknown input element type                        */
   DSFP8_ERR_UNSUPPORTED = -9, /* a fused form does not support this operand layout */
-  DSFP8_ERR_SCRATCH = -10     /* the problem exceeds the static scratch of a
+  DSFP8_ERR_SCRATCH = -10,    /* the problem exceeds the static scratch of a
                                  *_noalloc entry point                            */
+  DSFP8_ERR_SCORE = -11       /* unknown score function                           */
 };
 
 /* Scale formats.  UE8M0 rounds each scale value up to a power of two
@@ -87,7 +88,8 @@ enum {
  * stored as fp32. */
 enum { DSFP8_SCALE_FP32 = 0, DSFP8_SCALE_UE8M0 = 1 };
 
-/* Element types accepted by dsfp8_weight_quant and dsfp8_row_quant_i8. */
+/* Element types accepted by dsfp8_weight_quant, dsfp8_row_quant_i8,
+ * dsfp8_mxfp4_quant, dsfp8_moe_gate (logits) and dsfp8_add_rms_norm (weights). */
 enum { DSFP8_DTYPE_F32 = 0, DSFP8_DTYPE_BF16 = 1 };
 
 /* Stored weight formats accepted by dsfp8_moe_few: e4m3 with one scale per
@@ -592,6 +594,190 @@ dsfp8_status dsfp8_moe_few(const void* x, int64_t ldx,
                            hipStream_t stream);
 
 size_t dsfp8_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t F);
+
+/*
+ * MXFP4: the OCP microscaling format with e2m1 elements.  A row of K columns is
+ * stored as KM(K) = ceil(K/32) blocks of 32 columns, each with 16 bytes of codes
+ * and one scale byte:
+ *   codes   uint8 [M, 16 KM(K)]: column 2i of the row in the low half of byte i,
+ *           column 2i + 1 in the high half; a code is sign, two exponent bits,
+ *           one mantissa bit (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *           The columns of a last block past K hold code 0.
+ *   scales  uint8 [M, KM(K)]: e + 127 for the scale 2^e; 255 is NaN.
+ * An element's value is code * 2^e.  Rows of codes start at multiples of 16
+ * bytes and so do rows of scales: base addresses and row strides (in bytes) are
+ * multiples of 16, so a row of scales has room for KM(K) rounded up to 16
+ * bytes.  All of that room must be readable in a product's operands; what it
+ * holds past KM(K) does not matter, and the quantisers leave it as it is.
+ *
+ * Quantisation of rows (a token of an activation, or an output channel of a
+ * weight), per row m and block b of 32 columns:
+ *   e       = max(floor(log2 max |x|) - 2, -127)
+ *   q[m,k]  = e2m1(x[m,k] / 2^e)     (round to nearest, halfway cases to the
+ *                                     even code; beyond +-6 to +-6)
+ * A block of zeros has e = -127.  A block with a NaN or an infinity gets the
+ * scale byte 255 (its codes are then unspecified), so that products of that row
+ * show it and no other row changes.  The sign of a zero is kept.
+ *
+ *   x      fp32 or bf16 (dtype) [M, K], row stride ldx  (device, read)
+ *   y      codes [M, 16 KM(K)], row stride ldy          (device, written)
+ *   s      scales [M, KM(K)], row stride lds            (device, written)
+ * Errors: DTYPE, NULL, SHAPE, LD (a stride too small, or ldy or lds no multiple
+ * of 16), ALIGN (y or s not 16-byte aligned), LAUNCH.
+ */
+dsfp8_status dsfp8_mxfp4_quant(const void* x, int dtype, int64_t M, int64_t K, int64_t ldx,
+                               void* y, int64_t ldy, void* s, int64_t lds, hipStream_t stream);
+
+/*
+ * The same of x[m,i] = SiLU(g[m,i]) * u[m,i], evaluated in fp32 and not rounded
+ * in between, as accurate as dsfp8_silu_mul_row_quant_i8's.
+ *   g, u   bf16 [M, I], row strides ldg, ldu (device, read; may be the halves
+ *          of one [M, 2I] product)
+ * Errors: as dsfp8_mxfp4_quant.
+ */
+dsfp8_status dsfp8_silu_mul_mxfp4_quant(const void* g, int64_t ldg, const void* u, int64_t ldu,
+                                        int64_t M, int64_t I, void* y, int64_t ldy, void* s, int64_t lds,
+                                        hipStream_t stream);
+
+/*
+ * The values of MXFP4 rows: out[m,k] = bf16(code * 2^e), which is exact unless
+ * it is beyond bf16's range (then an infinity).
+ *   q, s   as above (device, read)
+ *   out    bf16 [M, K], row stride ldo                  (device, written)
+ * Errors: NULL, SHAPE, LD, ALIGN, LAUNCH.
+ */
+dsfp8_status dsfp8_mxfp4_dequant(const void* q, int64_t ldq, const void* s, int64_t lds, int64_t M, int64_t K,
+                                 void* out, int64_t ldo, hipStream_t stream);
+
+/*
+ * Product of MXFP4 matrices:
+ *   C[m, n] = bf16( sum_b 2^(ea[m,b] + eb[n,b]) sum_{k in block b} qa[m,k] qb[n,k] )
+ * accumulated in fp32; the order of accumulation is unspecified, but the same
+ * call gives the same bytes.
+ *   A, a_s   codes and scales of M rows, row strides lda, ldas  (device, read)
+ *   B, b_s   codes and scales of N rows (the weight)            (device, read)
+ *   C        bf16 [M, N], row stride ldc                        (device, written)
+ * K = 0 writes zeros.  Limits: lda, ldb < 2^23 (rows less than 8 MB apart).
+ * Errors: NULL, SHAPE, LD, ALIGN (an operand not 16-byte aligned, C not 2-byte
+ * aligned), UNSUPPORTED (the limits), LAUNCH.
+ */
+dsfp8_status dsfp8_gemm_mxfp4(const void* A, int64_t lda, const void* a_s, int64_t ldas,
+                              const void* B, int64_t ldb, const void* b_s, int64_t ldbs,
+                              void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * MXFP4 linear layer on bf16 rows, linear() of [AG] 6.3 with MXFP4 operands:
+ * dsfp8_gemm_mxfp4 of dsfp8_mxfp4_quant(x) with the weight (B, b_s).
+ *   x          bf16 [M, K], row stride ldx              (device, read)
+ *   B, b_s, C  as for dsfp8_gemm_mxfp4
+ *   workspace  at least dsfp8_linear_mxfp4_workspace_bytes bytes, 16-byte
+ *              aligned (scratch: the codes and scales of x; needs no
+ *              initialisation); 0 bytes, and NULL, for few rows, whose
+ *              quantisation is part of the product's launch
+ * Errors: NULL, SHAPE, LD, ALIGN, UNSUPPORTED, WORKSPACE, LAUNCH.
+ */
+dsfp8_status dsfp8_linear_mxfp4(const void* x, int64_t ldx, const void* B, int64_t ldb, const void* b_s, int64_t ldbs,
+                                void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dsfp8_linear_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * dsfp8_gemm_mxfp4 over per-expert row ranges ([AG] 6.4 / 8.4): rows
+ * offsets[e] .. offsets[e+1]-1 of the product use expert e's weight.
+ *   A, a_s   codes and scales of a_rows rows                    (device, read)
+ *   rows     int32 [M_total]: product row r is row rows[r] of A (each entry is
+ *            clamped to [0, a_rows)), or NULL: row r itself (a_rows >= M_total)
+ *                                                               (device, read)
+ *   B, b_s   codes and scales of E * N rows, expert e's from row e * N (device, read)
+ *   offsets  int32 [E+1] in device memory, as for dsfp8_grouped_gemm: not
+ *            validated, clamped to [0, M_total]                 (device, read)
+ *   C        bf16 [M_total, N], row stride ldc; rows of no expert (at or past
+ *            offsets[E]) are left as they were                  (device, written)
+ * Limits: those of dsfp8_gemm_mxfp4, 1 <= E <= 65536, and with rows
+ * a_rows * lda < 2^31.
+ * Errors: NULL, SHAPE (also rows == NULL with a_rows < M_total, a_rows < 1 with
+ * M_total > 0), LD, ALIGN, UNSUPPORTED, LAUNCH.
+ */
+dsfp8_status dsfp8_grouped_gemm_mxfp4(const void* A, int64_t a_rows, int64_t lda, const void* a_s, int64_t ldas,
+                                      const int32_t* rows, const void* B, int64_t ldb, const void* b_s, int64_t ldbs,
+                                      const int32_t* offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
+                                      void* C, int64_t ldc, hipStream_t stream);
+
+/*
+ * The gate of a routed-expert layer ([AG] 6.4, Gate): which k of E experts a token
+ * goes to, and with what weights, from the router's logits.
+ *   score[t,e] = sigmoid(logits[t,e])  or  softmax(logits[t])[e], evaluated
+ *                in 64 bits and rounded once to fp32
+ *   key[t,e]   = fp32(score + bias[e])  (score without a bias)
+ * An expert whose logit or key is -infinity is not available.  With groups > 1
+ * (groups of E / groups consecutive experts), a group's score is the sum of its
+ * two largest available keys with a bias and its largest without (one key
+ * counts alone), and only the experts of the top_groups groups of largest score
+ * stay available.  Of those, the k experts of largest key are taken, in
+ * decreasing order; among equal keys, and among groups of equal scores, the
+ * lowest index comes first.
+ *   w          = score of the chosen expert, without the bias
+ *   weights    = bf16(w / sum of the token's w * scale) with renormalize
+ *                (0 where the sum is 0), else bf16(w * scale)
+ * in fp32.  Where fewer than k experts are available the last slots get index
+ * -1, which the routed-expert calls take as no expert, and weight 0: a token
+ * whose logits are all -infinity (padding) goes to none.  A token whose scores
+ * or keys contain a NaN gets NaN weights and k distinct available experts.
+ *
+ *   logits   fp32 or bf16 (dtype) [T, E], row stride ldl  (device, read)
+ *   bias     fp32 [E], or NULL                            (device, read)
+ *   indices  int32 [T, k], row stride ldi                 (device, written)
+ *   weights  bf16 [T, k], row stride ldw                  (device, written)
+ * Limits: 1 <= k <= 16, 1 <= E <= 4096, 1 <= groups <= 64 and a divisor of E,
+ * 1 <= top_groups <= groups, k <= top_groups * (E / groups), T < 2^31.
+ * Errors: DTYPE, SHAPE (the limits), NULL, LD, ALIGN, SCORE (unknown score),
+ * LAUNCH.
+ */
+enum { DSFP8_SCORE_SIGMOID = 0, DSFP8_SCORE_SOFTMAX = 1 };
+dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const float* bias, int64_t T, int64_t E,
+                            int64_t k, int64_t groups, int64_t top_groups, int score, int renormalize, float scale,
+                            int32_t* indices, int64_t ldi, void* weights, int64_t ldw, hipStream_t stream);
+
+/*
+ * The RMS norms around a residual connection, with the quantisation of what
+ * the next block reads:
+ *   t = x[m]                                  post_weight NULL
+ *   t = x[m] / rms(x[m]) * post_weight        otherwise
+ *   h = residual[m] + scale * gate[m] * t     (gate NULL: 1; residual NULL: h = x[m])
+ *   y = h / rms(h) * weight,   rms(v) = sqrt(mean v^2 + eps)
+ * in fp32.  h is written rounded to bf16; y is taken from h before that
+ * rounding, and a quantised y is not rounded to bf16 in between.
+ *
+ *   x            bf16 [T, D], row stride ldx               (device, read)
+ *   residual     bf16 [T, D], row stride ldr, or NULL      (device, read)
+ *   gate         bf16 [T, D], row stride ldg, or one row for all tokens
+ *                (ldg = 0), or NULL                        (device, read)
+ *   post_weight  fp32 or bf16 (w_dtype) [D], or NULL       (device, read)
+ *   weight       fp32 or bf16 (w_dtype) [D]                (device, read)
+ *   h            bf16 [T, D], row stride ldh; not written, and may be NULL,
+ *                without a residual                        (device, written)
+ *   y, s         y_fmt BF16: y bf16 [T, D], row stride ldy; s is not used
+ *                E4M3, E4M3_UE8M0: y e4m3 [T, D], s fp32 [T, KB(D)] with strides
+ *                s_row_stride, s_kb_stride: dsfp8_act_quant of the fp32 y
+ *                (with IEEE divisions)
+ *                MXFP4: y codes [T, 16 KM(D)], s scales [T, KM(D)] with row
+ *                stride s_row_stride: dsfp8_mxfp4_quant of the fp32 y
+ *                                                          (device, written)
+ * A row with a NaN shows it in its outputs (a quantised y in its scales) and
+ * changes no other row.  h may be residual or x, and a bf16 y may be x, with the
+ * same stride; otherwise outputs must not overlap inputs.  Without a residual,
+ * post_weight and gate must be NULL and scale 1.
+ * Limits: D <= 65536, eps >= 0.
+ * Errors: DTYPE (w_dtype, y_fmt), SHAPE (the limits, a size that is negative, or
+ * an argument that needs a residual without one), NULL, LD, ALIGN, LAUNCH.
+ */
+enum { DSFP8_NORM_BF16 = 0, DSFP8_NORM_E4M3 = 1, DSFP8_NORM_E4M3_UE8M0 = 2, DSFP8_NORM_MXFP4 = 3 };
+dsfp8_status dsfp8_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                const void* gate, int64_t ldg, const void* post_weight, const void* weight,
+                                int w_dtype, float scale, float eps, int64_t T, int64_t D,
+                                void* h, int64_t ldh, void* y, int64_t ldy, int y_fmt,
+                                void* s, int64_t s_row_stride, int64_t s_kb_stride, hipStream_t stream);
 
 #ifdef __cplusplus
 }

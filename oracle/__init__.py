@@ -25,6 +25,10 @@ What it computes, and where the pages define it:
 * ``moe``      -- the routed-expert steps around the grouped product: the row
   order of the (token, slot) pairs, the gathered act_quant and the weighted
   bf16 combine (Admin Guide 6.4 and 8.4).
+* ``int8``, ``moe_few`` -- the int8 linear layer and the few-token expert layer.
+* ``mxfp4``    -- 4-bit microscaled rows: quantiser, values, product.
+* ``gate``     -- the choice of a token's experts and their weights.
+* ``norm``     -- the RMS norms around a residual connection.
 
 Precision: the pages fix fp32 for the quantisers (the data are converted to fp32 first), so
 those run in IEEE binary32 through NumPy float32 scalars/arrays, whose

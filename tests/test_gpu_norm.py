@@ -1,0 +1,213 @@
+"""GPU checks of the norms around a residual connection, element by element within the bounds that
+oracle/norm.py derives for an fp32 evaluation, plus half a step of each output's type."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_act_amd as ds
+from block_scaled_fp8_act_amd import inputs as I
+from oracle import formats as F
+from oracle import mxfp4 as MX
+from oracle import norm as NM
+
+from gpu_helpers import bf16_to_f64, dev_bf16, host_bits16, host_u8
+
+pytestmark = pytest.mark.gpu
+
+CID = 140
+
+
+def operands(T, D, seed, post=True, gate="row", residual=True, wtype=torch.bfloat16):
+    g = I.rng(CID, seed)
+    op = {"x": I.activations((T, D), CID, seed + 1, outlier_frac=0.01)}
+    op["residual"] = I.activations((T, D), CID, seed + 2) if residual else None
+    op["gate"] = {"none": None, "row": I.to_bf16_bits(g.random((T, D), np.float32)),
+                  "channel": I.to_bf16_bits(g.random(D, np.float32))}[gate]
+    w = [torch.from_numpy((1 + 0.2 * g.standard_normal(D)).astype(np.float32)).to(wtype) for _ in range(2)]
+    return op, w[0], w[1] if post else None
+
+
+def run(op, w, pw, **kw):
+    d = {n: None if v is None else dev_bf16(v) for n, v in op.items()}
+    return ds.add_rms_norm(d["x"], w.cuda(), residual=d["residual"], gate=d["gate"],
+                           post_weight=None if pw is None else pw.cuda(), **kw)
+
+
+def expected(op, w, pw, scale=1.0, eps=1e-6):
+    v = {n: None if b is None else bf16_to_f64(b) for n, b in op.items()}
+    return NM.forward(v["x"], w.double().numpy(), v["residual"], None if pw is None else pw.double().numpy(), v["gate"], scale, eps)
+
+
+def within(got, ref, bound, half, what):
+    err = np.abs(got - ref)
+    lim = bound + (np.abs(ref) + bound) * half + 2.0 ** -134
+    assert np.all(err <= lim), f"{what}: {float((err / lim).max()):.3f} of the bound"
+
+
+def check(got, op, w, pw, quant, D, **kw):
+    h, dh, y, dy = expected(op, w, pw, **kw)
+    got = got if isinstance(got, tuple) else (got,)
+    if op["residual"] is not None:
+        within(bf16_to_f64(host_bits16(got[-1])), h, dh, 2.0 ** -8, "h")
+    if quant is None:
+        return within(bf16_to_f64(host_bits16(got[0])), y, dy, 2.0 ** -8, "y")
+    block = 32 if quant == "mxfp4" else 128
+    T, nb = y.shape[0], -(-D // block)
+    top, dtop = (np.pad(v, ((0, 0), (0, nb * block - D))).reshape(T, nb, block).max(axis=2) for v in (np.abs(y), dy))
+    if quant == "mxfp4":
+        s = host_u8(got[1])
+        assert np.all((s == MX.scale_byte(top - dtop)) | (s == MX.scale_byte(top + dtop))), "scales"
+        unit = np.repeat(np.ldexp(1.0, s.astype(int) - 127), block, axis=1)[:, :D]
+        v = MX.values(host_u8(got[0]), s, D)
+        a = (np.abs(y) + dy) / unit     # half a step grows with the value
+        half = np.where(a < 2, 0.25, np.where(a < 4, 0.5, np.maximum(1.0, a - 6))) * unit
+        assert np.all(np.abs(v - y) <= half + dy), "codes"
+        assert not MX.unpack(host_u8(got[0]))[:, D:].any()
+    else:
+        s = got[1].cpu().numpy().astype(np.float64)
+        if quant == "e4m3":
+            ref = np.maximum(top, 1e-4) / 448
+            assert np.all(np.abs(s - ref) <= dtop / 448 + ref * 2.0 ** -23), "scales"
+        else:
+            lo, hi = (np.exp2(np.ceil(np.log2(np.maximum(t, 1e-4) / 448))) for t in (top * (1 - 2.0 ** -22) - dtop, top * (1 + 2.0 ** -22) + dtop))
+            assert np.all((s == lo) | (s == hi)), "scales"
+        sc = np.repeat(s, block, axis=1)[:, :D]
+        v = F.e4m3_decode(host_u8(got[0])).astype(np.float64) * sc
+        within(v, y, dy + sc * 2.0 ** -10, 2.0 ** -4 + 2.0 ** -22, "codes")
+
+
+# columns around a chunk of 8, a block of 32 and of 128, and the limits of each kernel
+SIZES = [(1, 1), (3, 7), (2, 8), (5, 33), (4, 127), (3, 129), (9, 511), (6, 512), (5, 513), (2, 1000), (3, 2048), (2, 2049),
+         (2, 4096), (3, 4100), (2, 7168), (2, 8192), (2, 8193), (1, 16384), (2, 16400), (1, 32769), (1, 65536), (70, 256)]
+
+
+@pytest.mark.parametrize("quant", [None, "e4m3", "e4m3_ue8m0", "mxfp4"])
+@pytest.mark.parametrize("T,D", SIZES)
+def test_sandwich(T, D, quant):
+    op, w, pw = operands(T, D, 10 * T + D)
+    got = run(op, w, pw, scale=0.5, quant=quant)
+    check(got, op, w, pw, quant, D, scale=0.5)
+    again = run(op, w, pw, scale=0.5, quant=quant)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("quant", [None, "e4m3", "mxfp4"])
+@pytest.mark.parametrize("residual,post,gate,wtype", [(False, False, "none", torch.bfloat16), (True, False, "none", torch.float32),
+                                                      (True, True, "none", torch.float32), (True, False, "channel", torch.bfloat16),
+                                                      (True, True, "channel", torch.float32), (True, False, "row", torch.bfloat16)])
+def test_forms(residual, post, gate, wtype, quant):
+    for T, D in [(5, 300), (3, 1537)]:
+        op, w, pw = operands(T, D, 77, post, gate, residual, wtype)
+        kw = dict(scale=0.22 if residual else 1.0, eps=1e-5)
+        check(run(op, w, pw, quant=quant, **kw), op, w, pw, quant, D, **kw)
+
+
+def test_rows_of_zeros_and_tiny_values():
+    """Zeros give zeros (eps keeps the root from zero); values whose squares vanish in fp32 do not disturb it."""
+    op, w, pw = operands(4, 200, 5)
+    op["x"][0] = 0
+    op["residual"][0] = 0
+    op["x"][1] = I.to_bf16_bits(np.full(200, 1e-30, np.float32))
+    op["residual"][1] = 0
+    for quant in (None, "mxfp4"):
+        got = run(op, w, pw, quant=quant)
+        y = bf16_to_f64(host_bits16(got[0])) if quant is None else MX.values(host_u8(got[0]), host_u8(got[1]), 200)
+        assert not y[0].any() and np.isfinite(y).all()
+        assert not host_bits16(got[-1])[0].any()
+    q, s, _ = run(op, w, pw, quant="e4m3")
+    assert np.all(s[0].cpu().numpy() == np.float32(1e-4) / np.float32(448)) and not q[0].any()
+
+
+@pytest.mark.parametrize("bad", [0x7fc0, 0x7f80])
+def test_nan_and_infinity_stay_in_their_row(bad):
+    op, w, pw = operands(5, 700, 6)
+    clean = {q: run(op, w, pw, quant=q) for q in (None, "e4m3", "e4m3_ue8m0", "mxfp4")}
+    op["x"][2, 699] = bad
+    for q, ref in clean.items():
+        got = run(op, w, pw, quant=q)
+        keep = [0, 1, 3, 4]
+        assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, ref))
+        if q is None:
+            assert torch.isnan(got[0][2].float()).any()
+        elif q == "mxfp4":
+            assert (got[1][2] == 255).any()
+        else:
+            assert not torch.isfinite(got[1][2]).all()
+
+
+def test_strides_in_place_and_out():
+    T, D = 6, 333
+    op, w, pw = operands(T, D, 7)
+    ref = run(op, w, pw)
+    d = {n: dev_bf16(v) for n, v in op.items()}
+
+    def wide(t):
+        b = torch.full((T, D + 9), 9.0, dtype=t.dtype, device="cuda")
+        b[:, 5:5 + D] = t
+        return b
+    W = {n: wide(t) for n, t in d.items()}
+    v = {n: b[:, 5:5 + D] for n, b in W.items()}
+    # h over the residual, y over x
+    y, h = ds.add_rms_norm(v["x"], w.cuda(), residual=v["residual"], gate=v["gate"], post_weight=pw.cuda(), out=(v["x"], v["residual"]))
+    assert torch.equal(y, ref[0]) and torch.equal(h, ref[1])
+    for b in W.values():
+        assert (b[:, :5] == 9).all() and (b[:, 5 + D:] == 9).all()
+    row_major = torch.full((T, 5), 9.0, device="cuda")
+    q, s, h = ds.add_rms_norm(d["x"], w.cuda(), residual=d["residual"], quant="e4m3",
+                              out=(None, row_major[:, :3], None))
+    q2, s2, h2 = ds.add_rms_norm(d["x"], w.cuda(), residual=d["residual"], quant="e4m3")
+    assert torch.equal(q, q2) and torch.equal(s, s2) and (row_major[:, 3:] == 9).all()
+    # a gate row for all tokens, given as an expanded matrix or as a vector
+    g = d["gate"][0]
+    a = ds.add_rms_norm(d["x"], w.cuda(), residual=d["residual"], gate=g)
+    b = ds.add_rms_norm(d["x"], w.cuda(), residual=d["residual"], gate=g[None].expand(T, D))
+    c = ds.add_rms_norm(d["x"], w.cuda(), residual=d["residual"], gate=g[None].expand(T, D).contiguous())
+    assert all(torch.equal(p, q) and torch.equal(p, r) for p, q, r in zip(a, b, c))
+
+
+def test_no_rows():
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    assert ds.add_rms_norm(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), w).shape == (0, 64)
+
+
+def test_graph():
+    T, D = 40, 2304
+    op, w, pw = operands(T, D, 8)
+    d = {n: dev_bf16(v) for n, v in op.items()}
+    wd, pd = w.cuda(), pw.cuda()
+    stream = d["residual"].clone()
+    q, s = ds.mxfp4_empty(T, D, "cuda")
+
+    def step():                     # the residual stream updated in place
+        ds.add_rms_norm(d["x"], wd, residual=stream, post_weight=pd, gate=d["gate"], quant="mxfp4", out=(q, s, stream))
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in range(4):
+        d["x"].copy_(dev_bf16(I.activations((T, D), CID, 20 + seed)))
+        before = stream.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        got = q.clone(), s.clone(), stream.clone()
+        stream.copy_(before)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], q) and torch.equal(got[1], s) and torch.equal(got[2], stream)
+
+
+def test_refusals():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for bad in (lambda: ds.add_rms_norm(x, w, gate=x), lambda: ds.add_rms_norm(x, w, post_weight=w), lambda: ds.add_rms_norm(x, w, scale=2.0),
+                lambda: ds.add_rms_norm(x, w[:63]), lambda: ds.add_rms_norm(x, w.half()), lambda: ds.add_rms_norm(x.float(), w),
+                lambda: ds.add_rms_norm(x, w, residual=x[:3]), lambda: ds.add_rms_norm(x, w, residual=x, post_weight=w.float()),
+                lambda: ds.add_rms_norm(x, w, residual=x, gate=w[:5]), lambda: ds.add_rms_norm(x, w, quant="int8"),
+                lambda: ds.add_rms_norm(x, w, eps=-1.0), lambda: ds.add_rms_norm(x.t(), w[:4]), lambda: ds.add_rms_norm(x.cpu(), w),
+                lambda: ds.add_rms_norm(x, w.cpu()), lambda: ds.add_rms_norm(x, w, residual=x, out=(x,)),
+                lambda: ds.add_rms_norm(torch.zeros((1, 65537), dtype=torch.bfloat16, device="cuda"),
+                                        torch.zeros(65537, dtype=torch.bfloat16, device="cuda"))):
+        with pytest.raises(ds.Dsfp8Error):
+            bad()
