@@ -10,6 +10,8 @@
 // (checked over every bf16 value and every scale).  A block that holds a NaN
 // or an infinity has the field 255 and gets the scale byte 255, the format's
 // NaN.
+#include <type_traits>
+
 #include "device.h"
 #include "launch.h"
 #include "tile.h"
@@ -211,41 +213,69 @@ __device__ __forceinline__ bool mx_find(const MxGemmArgs& p, int64_t want, MxTil
 // ---- tiles -----------------------------------------------------------------------------
 //
 // BM x BN tiles, each wave WM x WN of it in 32x32 subtiles of
-// v_mfma_scale_f32_32x32x64_f8f6f4.  A K-block is 128 bytes of a row, 256
-// columns: four matrix instructions deep.  Lane (fr, fg) of an instruction
-// holds 16 bytes, the 32 columns of one block of row fr, and that block's scale
-// byte, which the instruction applies.  The operands go through the same ring of LDS
-// stages as the other tiled products', filled by buffer_load ... lds and read
-// without bank conflicts through the XOR swizzle.  The scale bytes of two K-blocks
-// (16 bytes a row) are loaded together, one load per 64 rows, into a ring of
-// two buffers behind the stages.
+// v_mfma_scale_f32_32x32x64_f8f6f4.  Lane (fr, fg) of an instruction holds 16
+// bytes, the 32 columns of one block of row fr, and that block's scale byte, which
+// the instruction applies.
+//
+// The operands go through a ring of LDS stages, filled by buffer_load ... lds.
+// A stage holds 64 bytes of a row, 128 columns, two matrix instructions deep:
+// four of them take the room of two of 128 bytes, but three are in flight when
+// the fourth is used.  What bounds the large products is how soon the operands
+// arrive (a 256x256 tile without its matrix instructions took 86% of its time
+// with two stages of 128 bytes), so bytes in flight count.  The scale bytes of four
+// stages (16 bytes a row) are loaded together, one load per 64 rows, into a
+// ring of two buffers behind the stages.
+//
+// A matrix instruction of this format takes half as long as one of 8 bits, so
+// its operands are read one step (64 columns) ahead into registers, and over the
+// stages' border too: the barrier that hands over the next stage comes before
+// the second step of the current one, whose operands are in registers by then.
+// The stage it leaves is refilled behind that step's instructions.
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
+// Where 16-byte chunk c of row r lies, for rows of 64 or 128 bytes: chunk c ^ key.
+// The 8 rows of an aligned group of 8 lie in distinct 16-byte slots of 128 bytes of
+// banks, the 16 rows of an aligned group of 16 in distinct slots of 256 bytes.
+template <int ROW>
+__device__ __forceinline__ int mx_key(int r) {
+  return ROW == 128 ? swz_key(r) : ((r >> 1) & 3) ^ ((r >> 3) & 1);
+}
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int ROW_>
 struct MxCfg {
+  static constexpr int ROW = ROW_;              // bytes of a row in a stage
+  static constexpr int STEPS = ROW / 32;        // matrix instructions deep
+  static constexpr int PHASES = 256 / ROW;      // stages of one load of scales
+  static constexpr int RPI = 1024 / ROW;        // rows of one load instruction
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
   static constexpr int NW = WAVES_M * WAVES_N;
   static constexpr int kThreads = 64 * NW;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int TM = WM / 32, TN = WN / 32;
-  static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int A_BYTES = BM * ROW, B_BYTES = BN * ROW, STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LOADS = A_INSTR + B_INSTR;
   static constexpr int S_ROWS = BM + BN, S_INSTR = (S_ROWS / 64 + NW - 1) / NW;  // scale loads of a wave
-  static constexpr int S_BYTES = S_INSTR * NW * 1024;
+  static constexpr int S_BYTES = S_INSTR * NW * 1024, S_BUFS = (STAGES + PHASES - 2) / PHASES + 1;
   static constexpr int C_BYTES = 32 * WN * 2;  // 32 rows of a wave's output
-  static constexpr int RING = STAGES * STAGE_BYTES + 2 * S_BYTES;
+  static constexpr int RING = STAGES * STAGE_BYTES + S_BUFS * S_BYTES;
   static constexpr int LDS = RING > NW * C_BYTES ? RING : NW * C_BYTES;
+  // Scale loads that go with stages a .. b.
+  static constexpr int scales_in(int a, int b) {
+    return b < a ? 0 : (b / PHASES - (a + PHASES - 1) / PHASES + 1) * S_INSTR;
+  }
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole 1 KB segments per wave");
   static_assert(WM % 32 == 0 && WN % 32 == 0 && BM % 64 == 0 && BN % 64 == 0, "32x32 subtiles, scale loads of 64 rows");
-  static_assert(NW % 2 == 0, "a wave's segments start at rows that agree modulo 16");
-  static_assert(STAGES == 2 || STAGES == 3, "the waits of the K loop");
+  static_assert(STAGES >= 2 && (STAGES - 1) * LOADS + S_BUFS * S_INSTR < 64, "the waits of the K loop");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-template <class CF>
+template <class CF, bool GROUPED>
 struct MxLoader {
   i32x4 rsA, rsB, rsAS, rsBS;
-  uint32_t off[CF::LOADS], soff[CF::S_INSTR];
-  uint32_t kc;  // byte within the K-block of every load's chunk (a wave's rows agree modulo 16)
+  // A lane's row in load 0 of each operand and the step from load to load (a row
+  // past the matrix lies past the descriptor's end by itself); grouped rows may
+  // be anywhere.
+  uint32_t offA[GROUPED ? CF::A_INSTR : 1], offB, stepA, stepB, soff[CF::S_INSTR];
+  uint32_t kc;  // byte within the stage's row of every load's chunk (a wave's rows agree modulo 16)
   uint32_t lds0, sds0;
   uint32_t KR;  // bytes of a row's codes
   int wave;
@@ -256,24 +286,32 @@ struct MxLoader {
     KR = (uint32_t)(p.KB * 16);
     const int64_t ra = t.m1 - t.m0 < CF::BM ? t.m1 - t.m0 : CF::BM, rb = p.N - t.n0 < CF::BN ? p.N - t.n0 : CF::BN;
     // rows through an index: the whole matrix behind one descriptor
-    const int64_t m0 = p.rows ? 0 : t.m0, ha = p.rows ? p.a_rows : ra;
+    const bool at = GROUPED && p.rows;
+    const int64_t m0 = at ? 0 : t.m0, ha = at ? p.a_rows : ra;
     rsA = make_rsrc(p.A + m0 * p.lda, (uint32_t)((ha - 1) * p.lda) + KR);
     rsB = make_rsrc(t.B + t.n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb) + KR);
     rsAS = make_rsrc(p.a_s + m0 * p.ldas, (uint32_t)(ha * p.ldas));
     rsBS = make_rsrc(t.b_s + t.n0 * p.ldbs, (uint32_t)(rb * p.ldbs));
     auto a_row = [&](int64_t r) __attribute__((always_inline)) {
-      if (!p.rows) return (uint32_t)r;
+      if (!at) return (uint32_t)r;
       const int32_t v = p.rows[t.m0 + r];
       return (uint32_t)(v < 0 ? 0 : (v < p.a_rows ? v : p.a_rows - 1));
     };
-    kc = (uint32_t)((lane & 7) ^ swz_key(wave * 8 + (lane >> 3))) * 16;
+    constexpr int C = CF::ROW / 16;  // chunks of a row
+    const int r0 = wave * CF::RPI + lane / C;
+    kc = (uint32_t)((lane % C) ^ mx_key<CF::ROW>(r0)) * 16;
+    if constexpr (GROUPED) {
 #pragma unroll
-    for (int n = 0; n < CF::LOADS; ++n) {
-      const bool a = n < CF::A_INSTR;
-      const int r = (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 8 + (lane >> 3);
-      off[n] = kOob;
-      if (r < (a ? ra : rb)) off[n] = (a ? a_row(r) * (uint32_t)p.lda : (uint32_t)(r * p.ldb)) + kc;
+      for (int n = 0; n < CF::A_INSTR; ++n) {
+        const int r = r0 + CF::NW * CF::RPI * n;
+        offA[n] = r < ra ? a_row(r) * (uint32_t)p.lda + kc : kOob;
+      }
+    } else {
+      offA[0] = (uint32_t)(r0 * p.lda) + kc;
     }
+    offB = (uint32_t)(r0 * p.ldb) + kc;
+    stepA = (uint32_t)(CF::NW * CF::RPI * p.lda);
+    stepB = (uint32_t)(CF::NW * CF::RPI * p.ldb);
 #pragma unroll
     for (int n = 0; n < CF::S_INSTR; ++n) {
       const int g = (wave + CF::NW * n) * 64 + lane, r = g < CF::BM ? g : g - CF::BM;
@@ -285,31 +323,74 @@ struct MxLoader {
     sds0 = lds0 + (uint32_t)(CF::STAGES * CF::STAGE_BYTES + wave * 1024);
   }
 
-  // Load n of K-block kb; the scales go with every other K-block.
-  __device__ __forceinline__ void issue(int n, int kb, int stage) const {
+  // Load n of stage g of the row (g counts along K) into ring place `at`; one
+  // past the row's end fetches nothing (its lanes are out of range and read as zero).
+  __device__ __forceinline__ void issue(int n, int g, int place) const {
     const bool a = n < CF::A_INSTR;
-    const uint32_t kbyte = (uint32_t)kb * BK;
-    const uint32_t at = lds0 + (uint32_t)(stage * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) +
-                                          (wave + CF::NW * (a ? n : n - CF::A_INSTR)) * 1024);
-    dma_b128(a ? rsA : rsB, at, kbyte + kc < KR ? off[n] : kOob, kbyte);
+    const int i = a ? n : n - CF::A_INSTR;
+    const uint32_t kbyte = (uint32_t)g * CF::ROW;
+    const uint32_t at = lds0 + (uint32_t)(place * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) + (wave + CF::NW * i) * 1024);
+    const uint32_t off = !a ? offB + (uint32_t)i * stepB : (GROUPED ? offA[GROUPED ? i : 0] : offA[0] + (uint32_t)i * stepA);
+    dma_b128(a ? rsA : rsB, at, kbyte + kc < KR ? off : kOob, kbyte);
   }
-  __device__ __forceinline__ void issue_scales(int kb) const {
-    if (kb & 1) return;
+  // The scales of the PHASES stages from g, a multiple of that.
+  __device__ __forceinline__ void issue_scales(int g) const {
+    const bool in = (uint32_t)g * CF::ROW < KR;
+    const int q = g / CF::PHASES;
 #pragma unroll
     for (int n = 0; n < CF::S_INSTR; ++n)
       dma_b128((wave + CF::NW * n) * 64 < CF::BM ? rsAS : rsBS,
-               sds0 + (uint32_t)((kb >> 1 & 1) * CF::S_BYTES + CF::NW * n * 1024), soff[n], (uint32_t)(kb >> 1) * 16);
+               sds0 + (uint32_t)(q % CF::S_BUFS * CF::S_BYTES + CF::NW * n * 1024), in ? soff[n] : kOob, (uint32_t)q * 16);
   }
 };
 
-// The scale bytes of a short last K-block's missing blocks may hold anything;
-// their codes read as zero, but the scale byte 255 would make NaN of them.
+// A wave's operands: fragments of one step, and the scale bytes of a stage's two.
 template <class CF>
-__device__ __forceinline__ void mx_clear_tail(uint8_t* smem, int kb, int blocks) {
-  uint8_t* s = smem + CF::STAGES * CF::STAGE_BYTES + (kb >> 1 & 1) * CF::S_BYTES + 8 * (kb & 1);
-  for (int r = threadIdx.x; r < CF::S_ROWS; r += CF::kThreads)
-    *reinterpret_cast<uint64_t*>(s + r * 16) &= (1ull << (8 * blocks)) - 1;
-  __syncthreads();
+struct MxOperands {
+  const uint8_t* smem;
+  int at, bt, sat, sbt;  // in a stage, and in a buffer of scales
+  int lf[CF::STEPS];
+  int shift;
+
+  __device__ __forceinline__ explicit MxOperands(const uint8_t* smem) : smem(smem) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int fr = lane & 31, fg = lane >> 5;
+    const int wm = wave / CF::WAVES_N * CF::WM, wn = wave % CF::WAVES_N * CF::WN;
+    at = wm * CF::ROW;
+    bt = CF::A_BYTES + wn * CF::ROW;
+    sat = CF::STAGES * CF::STAGE_BYTES + (wm + fr) * 16;
+    sbt = CF::STAGES * CF::STAGE_BYTES + (CF::BM + wn + fr) * 16;
+    shift = 8 * fg;
+#pragma unroll
+    for (int h = 0; h < CF::STEPS; ++h) lf[h] = fr * CF::ROW + (((2 * h + fg) ^ mx_key<CF::ROW>(fr)) << 4);
+  }
+  __device__ __forceinline__ u32x4 a(int place, int h, int i) const {
+    return *reinterpret_cast<const u32x4*>(smem + place * CF::STAGE_BYTES + lf[h] + at + 32 * i * CF::ROW);
+  }
+  __device__ __forceinline__ u32x4 b(int place, int h, int j) const {
+    return *reinterpret_cast<const u32x4*>(smem + place * CF::STAGE_BYTES + lf[h] + bt + 32 * j * CF::ROW);
+  }
+  // Dword d of the rows' scales in stage g, for steps 2d and 2d + 1: step h uses
+  // byte 2h + fg of a row's, byte 0 or 2 of the dword shifted by fg bytes.  `mask`
+  // clears the blocks that a short last stage does not have: their codes read as
+  // zero, but their scale bytes may hold anything, and 255 would make NaN of them.
+  __device__ __forceinline__ void scales(int g, int d, uint32_t mask, uint32_t (&sa)[CF::TM], uint32_t (&sb)[CF::TN]) const {
+    const uint8_t* b = smem + g / CF::PHASES % CF::S_BUFS * CF::S_BYTES + g % CF::PHASES * (CF::ROW / 16) + 4 * d;
+#pragma unroll
+    for (int i = 0; i < CF::TM; ++i) sa[i] = (*reinterpret_cast<const uint32_t*>(b + sat + 32 * i * 16) & mask) >> shift;
+#pragma unroll
+    for (int j = 0; j < CF::TN; ++j) sb[j] = (*reinterpret_cast<const uint32_t*>(b + sbt + 32 * j * 16) & mask) >> shift;
+  }
+};
+
+// One step of a 32x32 subtile, the weight first, so that a lane's results are
+// runs of four columns of a row.
+template <int H>
+__device__ __forceinline__ v16f mx_mfma(u32x4 b, uint32_t sb, u32x4 a, uint32_t sa, v16f c) {
+  const v8i b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  const v8i a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, c, 4, 4, 2 * (H & 1), (int)sb, 2 * (H & 1), (int)sa);
 }
 
 // C values of a wave, rounded to bf16 and stored 32 rows at a time through an
@@ -357,19 +438,30 @@ __device__ __forceinline__ void mx_store(const MxGemmArgs& p, const MxTile& t, c
   }
 }
 
+// Step H of a stage; follow(i) is called behind the instructions of each
+// subtile row i, whose operand is then free.
+template <class CF, int H, class Follow>
+__device__ __forceinline__ void mx_step(v16f (&acc)[CF::TM][CF::TN], u32x4 (&fa)[CF::TM], const u32x4 (&fb)[CF::TN],
+                                        const uint32_t (&sa)[CF::TM], const uint32_t (&sb)[CF::TN], Follow&& follow) {
+#pragma unroll
+  for (int i = 0; i < CF::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < CF::TN; ++j) acc[i][j] = mx_mfma<H>(fb[j], sb[j], fa[i], sa[i], acc[i][j]);
+    follow(i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // One workgroup per tile (grouped: per CU, walking the tiles of every expert).
 template <class CF, bool GROUPED>
 __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS];
+  constexpr int S = CF::STAGES, L = CF::LOADS, PH = CF::PHASES;
   const int64_t tiles_n = (p.N + CF::BN - 1) / CF::BN;
-  const int nkb = (int)((p.KB + 7) / 8), tail = (int)(p.KB & 7);
-  const int lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int fr = lane & 31, fg = lane >> 5;
-  const int wm = wave / CF::WAVES_N * CF::WM, wn = wave % CF::WAVES_N * CF::WN;
-  int lf[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) lf[h] = fr * BK + (((2 * h + fg) ^ swz_key(fr)) << 4);
+  constexpr int SB = CF::ROW / 16;  // blocks of a stage
+  const int ng = (int)((p.KB + SB - 1) / SB), left = (int)(p.KB % SB);
+  const uint64_t tail = left ? (1ull << (8 * left)) - 1 : ~0ull;  // the blocks of the last stage
+  const MxOperands<CF> op(smem);
   for (int64_t pid = blockIdx.x;; pid += gridDim.x) {
     MxTile t;
     if constexpr (GROUPED) {
@@ -381,13 +473,8 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
       tile_of(pid, (p.M + CF::BM - 1) / CF::BM, tiles_n, tm, tn);
       t = MxTile{tm * CF::BM, p.M, tn * CF::BN, p.B, p.b_s};
     }
-    MxLoader<CF> ld;
+    MxLoader<CF, GROUPED> ld;
     ld.init(p, t, smem);
-    for (int s = 0; s < CF::STAGES - 1 && s < nkb; ++s) {
-#pragma unroll
-      for (int n = 0; n < CF::LOADS; ++n) ld.issue(n, s, s);
-      ld.issue_scales(s);
-    }
     v16f acc[CF::TM][CF::TN];
 #pragma unroll
     for (int i = 0; i < CF::TM; ++i)
@@ -395,58 +482,79 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
       for (int j = 0; j < CF::TN; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    constexpr int PER = (CF::LOADS + 4 * CF::TM - 1) / (4 * CF::TM);
-    for (int kb = 0; kb < nkb; ++kb) {
-      // Of the stages issued so far, only the one behind K-block kb may be missing.
-      if (CF::STAGES == 2 || kb + 1 >= nkb) wait_vmcnt<0>();
-      else if (kb & 1) wait_vmcnt<CF::LOADS + CF::S_INSTR>();
-      else wait_vmcnt<CF::LOADS>();
+    // The loop over the stages has no branch inside, since the compiler would
+    // move matrix instructions across it: loads past the row's end fetch nothing,
+    // and the same numbers of them are in flight at every wait.
+    if (ng > 0) {
+      u32x4 fa[CF::TM], fb[2][CF::TN];
+      uint32_t sa[2][CF::TM], sb[2][CF::TN];
+#pragma unroll
+      for (int g = 0; g < S; ++g) {
+#pragma unroll
+        for (int n = 0; n < L; ++n) ld.issue(n, g, g);
+        if (g % PH == 0) ld.issue_scales(g);
+      }
+      // stage 0 has arrived when only the S - 1 later ones may be missing
+      wait_vmcnt<(S - 1) * L + CF::scales_in(1, S - 1)>();
       __syncthreads();
-      if (tail && kb == nkb - 1) mx_clear_tail<CF>(smem, kb, tail);
-      const uint8_t* stage = smem + (kb % CF::STAGES) * CF::STAGE_BYTES;
-      const uint8_t* sc = smem + CF::STAGES * CF::STAGE_BYTES + (kb >> 1 & 1) * CF::S_BYTES + 8 * (kb & 1);
-      // Scale bytes of instruction h: byte 2h + fg of the row's eight.
-      uint32_t sa[CF::TM][2], sb[CF::TN][2];
 #pragma unroll
-      for (int i = 0; i < CF::TM; ++i) {
-        const uint2 w = *reinterpret_cast<const uint2*>(sc + (wm + 32 * i + fr) * 16);
-        sa[i][0] = w.x >> (8 * fg), sa[i][1] = w.y >> (8 * fg);
+      for (int j = 0; j < CF::TN; ++j) fb[0][j] = op.b(0, 0, j);
+#pragma unroll
+      for (int i = 0; i < CF::TM; ++i) fa[i] = op.a(0, 0, i);
+      op.scales(0, 0, ng == 1 ? (uint32_t)tail : ~0u, sa[0], sb[0]);
+      constexpr int PER = (L + CF::TM - 1) / CF::TM;
+      int place = 0;
+      auto run = [&](int g, auto phase) __attribute__((always_inline)) {  // phase: g % PHASES
+        constexpr int X = decltype(phase)::value;
+        // registers of the scales of the stage's first and last steps, and of the next stage's first
+        constexpr int C0 = CF::STEPS == 4 ? 0 : X & 1, C1 = CF::STEPS == 4 ? 1 : C0, C2 = CF::STEPS == 4 ? 0 : 1 - C0;
+        const int next = place + 1 == S ? 0 : place + 1;
+        auto ahead = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+          for (int j = 0; j < CF::TN; ++j) fb[h & 1][j] = op.b(place, h, j);
+        };
+        if constexpr (CF::STEPS == 4) {
+          op.scales(g, 1, g + 1 >= ng ? (uint32_t)(tail >> 32) : ~0u, sa[1], sb[1]);
+          ahead(1);
+          mx_step<CF, 0>(acc, fa, fb[0], sa[0], sb[0], [&](int i) { fa[i] = op.a(place, 1, i); });
+          ahead(2);
+          mx_step<CF, 1>(acc, fa, fb[1], sa[0], sb[0], [&](int i) { fa[i] = op.a(place, 2, i); });
+        }
+        ahead(CF::STEPS - 1);
+        mx_step<CF, 0>(acc, fa, fb[0], sa[C1], sb[C1], [&](int i) { fa[i] = op.a(place, CF::STEPS - 1, i); });
+        // stage g + 1, when g + 2 .. g + S - 1 are missing
+        wait_vmcnt<(S - 2) * L + CF::scales_in(X + 2, X + S - 1)>();
+        __syncthreads();
+        op.scales(g + 1, 0, g + 2 >= ng ? (uint32_t)tail : ~0u, sa[C2], sb[C2]);
+#pragma unroll
+        for (int j = 0; j < CF::TN; ++j) fb[0][j] = op.b(next, 0, j);
+        mx_step<CF, 1>(acc, fa, fb[1], sa[C1], sb[C1], [&](int i) __attribute__((always_inline)) {
+          fa[i] = op.a(next, 0, i);
+#pragma unroll
+          for (int n = i * PER; n < (i + 1) * PER && n < L; ++n) ld.issue(n, g + S, place);
+          if (i == CF::TM - 1 && (X + S) % PH == 0) ld.issue_scales(g + S);
+        });
+        place = next;
+      };
+      int g = 0;
+      for (; g + PH <= ng; g += PH) {
+        run(g, std::integral_constant<int, 0>{});
+        run(g + 1, std::integral_constant<int, 1>{});
+        if constexpr (PH == 4) {
+          run(g + 2, std::integral_constant<int, 2>{});
+          run(g + 3, std::integral_constant<int, 3>{});
+        }
       }
-#pragma unroll
-      for (int j = 0; j < CF::TN; ++j) {
-        const uint2 w = *reinterpret_cast<const uint2*>(sc + (CF::BM + wn + 32 * j + fr) * 16);
-        sb[j][0] = w.x >> (8 * fg), sb[j][1] = w.y >> (8 * fg);
-      }
-      const int kn = kb + CF::STAGES - 1;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        u32x4 fb[CF::TN];
-#pragma unroll
-        for (int j = 0; j < CF::TN; ++j)
-          fb[j] = *reinterpret_cast<const u32x4*>(stage + CF::A_BYTES + (wn + 32 * j) * BK + lf[h]);
-#pragma unroll
-        for (int i = 0; i < CF::TM; ++i) {
-          const u32x4 fa = *reinterpret_cast<const u32x4*>(stage + (wm + 32 * i) * BK + lf[h]);
-          const v8i a8 = {(int)fa[0], (int)fa[1], (int)fa[2], (int)fa[3], 0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < CF::TN; ++j) {
-            const v8i b8 = {(int)fb[j][0], (int)fb[j][1], (int)fb[j][2], (int)fb[j][3], 0, 0, 0, 0};
-            // the weight first, so that a lane's results are runs of four columns of a row
-            if (h & 1)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[i][j], 4, 4, 2, (int)sb[j][h >> 1],
-                                                                          2, (int)sa[i][h >> 1]);
-            else
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[i][j], 4, 4, 0, (int)sb[j][h >> 1],
-                                                                          0, (int)sa[i][h >> 1]);
-          }
-          if (kn < nkb) {
-            const int s = h * CF::TM + i;
-#pragma unroll
-            for (int n = s * PER; n < (s + 1) * PER && n < CF::LOADS; ++n) ld.issue(n, kn, kn % CF::STAGES);
-            if (s == 4 * CF::TM - 1) ld.issue_scales(kn);
+      if (g < ng) {
+        run(g, std::integral_constant<int, 0>{});
+        if constexpr (PH == 4) {
+          if (g + 1 < ng) {
+            run(g + 1, std::integral_constant<int, 1>{});
+            if (g + 2 < ng) run(g + 2, std::integral_constant<int, 2>{});
           }
         }
       }
+      wait_vmcnt<0>();
     }
     __syncthreads();
     mx_store<CF>(p, t, acc, smem);
@@ -524,8 +632,8 @@ static hipError_t launch_mx_tiles(const MxGemmArgs& a, hipStream_t stream) {
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int64_t t256 = (a.M + 255) / 256 * ((a.N + 255) / 256);
-  if (t256 >= device_cu_count()) return launch_mx_tiles<MxCfg<256, 256, 2, 4, 2>>(a, stream);
-  return launch_mx_tiles<MxCfg<64, 64, 2, 2, 2>>(a, stream);
+  if (t256 >= device_cu_count()) return launch_mx_tiles<MxCfg<256, 256, 2, 4, 2, 128>>(a, stream);
+  return launch_mx_tiles<MxCfg<64, 64, 2, 2, 4, 64>>(a, stream);
 }
 
 bool linear_mx_fused(int64_t, int64_t, int64_t) { return false; }
