@@ -563,6 +563,221 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
   }
 }
 
+// ---- few rows or few tiles: K split over the waves of a workgroup -----------------------
+//
+// A workgroup owns a 16 FM x 16 FN tile; its eight waves take the K-blocks of 128
+// bytes a row (256 columns) in turn, each through a ring of D LDS slots of its own
+// that hold one K-block of the tile's rows and of their scales, so no wave waits for another
+// until the sums are added up at the end, in the order of the waves.  All of a wave's
+// first D K-blocks are in flight at once.  v_mfma_scale_f32_16x16x128_f8f6f4: lane
+// (fr, fg) holds block fg of the four of row fr.
+//
+// FUSED: the activations come as bf16 rows and every workgroup quantises all M <=
+// 16 of them itself, while its first weights are on their way; codes and
+// scales stay in LDS.
+
+constexpr int kSplitWaves = 8;
+constexpr int kFusedBytes = 16384;  // room for the codes and scales of a fused launch
+
+// Bytes of a row of codes and of scales in LDS: whole K-blocks, and a few more so
+// that rows do not start in the same bank.
+__host__ __device__ constexpr int mx_code_ld(int nkb) { return nkb * BK + 16; }
+__host__ __device__ constexpr int mx_scale_ld(int nkb) { return nkb * 8 + 8; }
+
+template <int FM, int FN, int D, bool FUSED>
+struct SplitCfg {
+  static constexpr int TM = 16 * FM, TN = 16 * FN;
+  static constexpr int AROWS = FUSED ? 0 : TM, ROWS = AROWS + TN;
+  static constexpr int LOADS = ROWS / 8;  // 8 rows each
+  static constexpr int AS_LOADS = (AROWS + 31) / 32, S_LOADS = AS_LOADS + (TN + 31) / 32;  // scales of 32 rows each
+  static constexpr int SLOT = ROWS * BK + S_LOADS * 256;
+  static constexpr int RING = kSplitWaves * D * SLOT;
+  static constexpr int SUM = kSplitWaves * FM * FN * 1024;
+  static constexpr int LDS = (RING > SUM ? RING : SUM) + (FUSED ? kFusedBytes : 0);
+  static_assert(D <= 4 && (LOADS + S_LOADS) * (D - 1) < 64, "waits of the ring");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+template <int FM, int FN, int D, bool FUSED, bool GROUPED>
+__global__ __launch_bounds__(64 * kSplitWaves) void mx_split_kernel(MxGemmArgs p, MxQuantArgs x) {
+  static_assert(!(FUSED && GROUPED), "grouped operands are quantised already");
+  using CF = SplitCfg<FM, FN, D, FUSED>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int fr = lane & 15, fg = lane >> 4;
+  const uint32_t tiles_n = (uint32_t)((p.N + CF::TN - 1) / CF::TN);
+  const uint32_t tm = blockIdx.x / tiles_n;
+  MxTile t;
+  if constexpr (GROUPED) {
+    if (!mx_find<CF::TM>(p, tm, t)) return;
+  } else {
+    t = MxTile{FUSED ? 0 : (int64_t)tm * CF::TM, p.M, 0, p.B, p.b_s};
+  }
+  t.n0 = (int64_t)(blockIdx.x - tm * tiles_n) * CF::TN;
+  const int nkb = (int)((p.KB + 7) / 8);
+  const uint32_t KR = (uint32_t)(p.KB * 16);
+  const int64_t ra = t.m1 - t.m0 < CF::TM ? t.m1 - t.m0 : CF::TM, rb = p.N - t.n0 < CF::TN ? p.N - t.n0 : CF::TN;
+  const bool at = GROUPED && p.rows;
+  const int64_t m0 = at ? 0 : t.m0, ha = at ? p.a_rows : ra;
+  i32x4 rsA, rsAS;
+  if constexpr (!FUSED) {
+    rsA = make_rsrc(p.A + m0 * p.lda, (uint32_t)((ha - 1) * p.lda) + KR);
+    rsAS = make_rsrc(p.a_s + m0 * p.ldas, (uint32_t)(ha * p.ldas));
+  }
+  const i32x4 rsB = make_rsrc(t.B + t.n0 * p.ldb, (uint32_t)((rb - 1) * p.ldb) + KR);
+  const i32x4 rsBS = make_rsrc(t.b_s + t.n0 * p.ldbs, (uint32_t)(rb * p.ldbs));
+  auto a_row = [&](int r) __attribute__((always_inline)) {
+    if (!at) return (uint32_t)r;
+    const int32_t v = p.rows[t.m0 + r];
+    return (uint32_t)(v < 0 ? 0 : (v < p.a_rows ? v : p.a_rows - 1));
+  };
+  // Load n fetches rows 8n .. 8n + 7 of the slot (A's rows, then B's); a lane's
+  // chunk depends on the row modulo 16 alone.
+  const uint32_t kc[2] = {(uint32_t)((lane & 7) ^ swz_key(lane >> 3)) * 16,
+                          (uint32_t)((lane & 7) ^ swz_key(8 + (lane >> 3))) * 16};
+  uint32_t off[CF::LOADS];
+#pragma unroll
+  for (int n = 0; n < CF::LOADS; ++n) {
+    const bool a = 8 * n < CF::AROWS;
+    const int r = 8 * n - (a ? 0 : CF::AROWS) + (lane >> 3);
+    off[n] = kOob;
+    if (r < (a ? ra : rb)) off[n] = (a ? a_row(r) * (uint32_t)p.lda : (uint32_t)(r * p.ldb)) + kc[n & 1];
+  }
+  // Lane l of a load of scales: four of the eight bytes of row l / 2 (A's rows,
+  // then B's, in loads of their own).
+  uint32_t soff[CF::S_LOADS];
+#pragma unroll
+  for (int n = 0; n < CF::S_LOADS; ++n) {
+    const bool a = n < CF::AS_LOADS;
+    const int r = 32 * (a ? n : n - CF::AS_LOADS) + (lane >> 1);
+    soff[n] = kOob;
+    if (r < (a ? ra : rb)) soff[n] = (a ? a_row(r) * (uint32_t)p.ldas : (uint32_t)(r * p.ldbs)) + 4 * (lane & 1);
+  }
+  const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(smem)) + (uint32_t)(wave * D * CF::SLOT);
+  auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
+    const uint32_t kbyte = (uint32_t)kb * BK, to = lds0 + (uint32_t)(slot * CF::SLOT);
+#pragma unroll
+    for (int n = 0; n < CF::LOADS; ++n)
+      dma_b128(8 * n < CF::AROWS ? rsA : rsB, to + (uint32_t)(n * 1024), kbyte + kc[n & 1] < KR ? off[n] : kOob, kbyte);
+#pragma unroll
+    for (int n = 0; n < CF::S_LOADS; ++n)
+      dma_b32(n < CF::AS_LOADS ? rsAS : rsBS, to + (uint32_t)(CF::ROWS * BK + n * 256), soff[n], (uint32_t)kb * 8);
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (wave + d * kSplitWaves < nkb) issue(wave + d * kSplitWaves, d);
+
+  uint8_t* codes = smem + CF::LDS - (FUSED ? kFusedBytes : 0);
+  uint8_t* scales = codes + (FUSED ? (int)p.M * mx_code_ld(nkb) : 0);
+  if constexpr (FUSED) {
+    // Chunks of 8 columns of all rows, dealt to the threads in turn, four
+    // loads of a thread in flight.
+    constexpr int HOLD = 4;
+    const int per_row = (int)p.KB * 4, units = (int)p.M * per_row;
+    for (int u0 = threadIdx.x; u0 < units; u0 += HOLD * 64 * kSplitWaves) {
+      Chunk<kBf16> c[HOLD];
+      int m[HOLD], k[HOLD];
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        const int u = u0 + i * 64 * kSplitWaves;
+        m[i] = u / per_row;
+        k[i] = u - m[i] * per_row;
+        c[i].load(x, m[i], (int64_t)k[i] * 8, u < units);
+      }
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        float v[8];
+        c[i].values(v);
+        const uint32_t sc = mx_scale(mx_quad_top(v));
+        if (u0 + i * 64 * kSplitWaves < units) {
+          reinterpret_cast<uint32_t*>(codes + m[i] * mx_code_ld(nkb))[k[i]] = mx_codes8(v, mx_scale_f32(sc));
+          if ((k[i] & 3) == 0) scales[m[i] * mx_scale_ld(nkb) + (k[i] >> 2)] = (uint8_t)sc;
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  v4f acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint8_t* ring = smem + wave * D * CF::SLOT;
+  const int left = (int)(p.KB & 7);
+  for (int kb = wave, slot = 0; kb < nkb; kb += kSplitWaves) {
+    // loads of the later K-blocks in flight behind this one's
+    constexpr int PER = CF::LOADS + CF::S_LOADS;
+    const int later = (nkb - 1 - kb) / kSplitWaves;
+    if (D >= 4 && later >= 3) wait_vmcnt<PER * (D >= 4 ? 3 : 0)>();
+    else if (D >= 3 && later >= 2) wait_vmcnt<PER * (D >= 3 ? 2 : 0)>();
+    else if (D >= 2 && later >= 1) wait_vmcnt<PER * (D >= 2 ? 1 : 0)>();
+    else wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    const uint8_t* at = ring + slot * CF::SLOT;
+    const uint8_t* bt = at + CF::AROWS * BK;
+    const uint8_t* st = at + CF::ROWS * BK;
+    // the scale bytes of blocks that a short last K-block does not have may hold anything
+    const uint64_t mask = left && kb == nkb - 1 ? (1ull << (8 * left)) - 1 : ~0ull;
+    u32x4 fa[FM][2], fb[FN][2];
+    uint64_t sa[FM], sb[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      sb[j] = (*reinterpret_cast<const uint64_t*>(st + CF::AS_LOADS * 256 + (16 * j + fr) * 8) & mask) >> (8 * fg);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fb[j][h] = *reinterpret_cast<const u32x4*>(bt + swz(16 * j + fr, 4 * h + fg));
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = FUSED ? (fr < (int)p.M ? fr : 0) : 16 * i + fr;
+      sa[i] = (*reinterpret_cast<const uint64_t*>(FUSED ? scales + r * mx_scale_ld(nkb) + kb * 8 : st + r * 8) & mask) >> (8 * fg);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        fa[i][h] = *reinterpret_cast<const u32x4*>(FUSED ? codes + r * mx_code_ld(nkb) + kb * BK + 64 * h + 16 * fg
+                                                         : at + swz(r, 4 * h + fg));
+    }
+    // the slot is free once its fragments have arrived
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (kb + D * kSplitWaves < nkb) issue(kb + D * kSplitWaves, slot);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const v8i b8 = {(int)fb[j][h][0], (int)fb[j][h][1], (int)fb[j][h][2], (int)fb[j][h][3], 0, 0, 0, 0};
+          const v8i a8 = {(int)fa[i][h][0], (int)fa[i][h][1], (int)fa[i][h][2], (int)fa[i][h][3], 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b8, a8, acc[i][j], 4, 4, 0, (int)(sb[j] >> (32 * h)), 0,
+                                                                       (int)(sa[i] >> (32 * h)));
+        }
+    slot = slot + 1 == D ? 0 : slot + 1;
+  }
+  __syncthreads();
+  // the waves' sums, added in the order of the waves: sum[wave][subtile][lane]
+  v4f* sum = reinterpret_cast<v4f*>(smem);
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sum[(wave * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int q = threadIdx.x; q < FM * FN * 64; q += 64 * kSplitWaves) {
+    const int l = q & 63, i = (q >> 6) / FN, j = (q >> 6) % FN;
+    const int64_t row = t.m0 + 16 * i + (l & 15), col = t.n0 + 16 * j + 4 * (l >> 4);
+    if (row >= t.m1 || col >= p.N) continue;
+    v4f y = sum[q];
+#pragma unroll
+    for (int w = 1; w < kSplitWaves; ++w) y += sum[w * FM * FN * 64 + q];
+    const uint32_t w2[2] = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+    uint16_t* dst = p.C + row * p.ldc + col;
+    if (col + 4 <= p.N) {
+      *reinterpret_cast<u32x2u*>(dst) = u32x2u{w2[0], w2[1]};
+    } else {
+      for (int v = 0; v < 4 && col + v < p.N; ++v) dst[v] = (uint16_t)(w2[v >> 1] >> (16 * (v & 1)));
+    }
+  }
+}
+
 inline unsigned grid_of(uint32_t total, int units) {
   const uint64_t per = 256u * (uint64_t)units;
   uint64_t g = (total + per - 1) / per;
@@ -629,14 +844,95 @@ static hipError_t launch_mx_tiles(const MxGemmArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
-  if (a.M == 0 || a.N == 0) return hipSuccess;
-  const int64_t t256 = (a.M + 255) / 256 * ((a.N + 255) / 256);
-  if (t256 >= device_cu_count()) return launch_mx_tiles<MxCfg<256, 256, 2, 4, 2, 128>>(a, stream);
-  return launch_mx_tiles<MxCfg<64, 64, 2, 2, 4, 64>>(a, stream);
+template <int FM, int FN, int D, bool FUSED>
+static hipError_t launch_mx_split(const MxGemmArgs& a, const MxQuantArgs& x, hipStream_t stream) {
+  using CF = SplitCfg<FM, FN, D, FUSED>;
+  const int64_t tiles_n = (a.N + CF::TN - 1) / CF::TN;
+  const dim3 blk(64 * kSplitWaves);
+  if (a.offsets) {
+    if constexpr (!FUSED) {
+      const int64_t some = a.E < a.M ? a.E : a.M;
+      hipLaunchKernelGGL((mx_split_kernel<FM, FN, D, false, true>), dim3((unsigned)((some + (a.M - some) / CF::TM) * tiles_n)),
+                         blk, 0, stream, a, x);
+    }
+  } else {
+    const int64_t tiles_m = FUSED ? 1 : (a.M + CF::TM - 1) / CF::TM;
+    hipLaunchKernelGGL((mx_split_kernel<FM, FN, D, FUSED, false>), dim3((unsigned)(tiles_m * tiles_n)), blk, 0, stream, a, x);
+  }
+  return hipGetLastError();
 }
 
-bool linear_mx_fused(int64_t, int64_t, int64_t) { return false; }
-hipError_t launch_linear_mx_fused(const MxGemmArgs&, const MxQuantArgs&, hipStream_t) { return hipErrorInvalidValue; }
+// The variants and the cost of a product in each, in us:
+//   launch + rounds * (start + step * K-blocks) + traffic * MB
+// with rounds of workgroups over the CUs, K-blocks of 256 columns that one wave
+// walks (split: an eighth of them), and the MB that all tiles load (rows of both
+// operands).  Fitted to 120 dense and grouped products of 1 to 16384 rows in
+// 13 variants, weights past the caches; taking the least of these eight is within
+// 4.8% of the best of all 13 in the mean, 30% at most.
+struct MxVariant {
+  int rows, columns, per_cu;  // tile, workgroups that share a CU
+  bool split;
+  float launch, start, step, traffic;
+};
+constexpr MxVariant kMxVariants[] = {
+    {16, 16, 2, true, 1.761f, 0.782f, 0.462f, 0.0467f},    // 0
+    {16, 32, 3, true, 2.180f, 0.220f, 0.744f, 0.0636f},    // 1
+    {32, 32, 2, true, 2.004f, 0.476f, 1.008f, 0.0468f},    // 2
+    {64, 64, 2, false, 1.870f, 1.641f, 0.317f, 0.0468f},   // 3
+    {64, 128, 2, false, 0.774f, 2.647f, 0.506f, 0.0451f},  // 4
+    {128, 128, 1, false, 1.803f, 2.644f, 0.735f, 0.0f},    // 5
+    {128, 256, 1, false, 1.158f, 4.086f, 1.198f, 0.0017f}, // 6
+    {256, 256, 1, false, 5.285f, 0.0f, 1.781f, 0.0f},      // 7
+};
+
+static int mx_choose(const MxGemmArgs& a) {
+  const double cus = device_cu_count(), kbs = (double)((a.KB + 7) / 8);
+  int best = 0;
+  double least = 0;
+  for (int v = 0; v < (int)(sizeof kMxVariants / sizeof *kMxVariants); ++v) {
+    const MxVariant& m = kMxVariants[v];
+    // grouped: a short tile per expert that may have rows, and the rest in whole ones
+    const int64_t some = a.offsets ? (a.E < a.M ? a.E : a.M) : 0;
+    const int64_t tiles_m = a.offsets ? some + (a.M - some) / m.rows : (a.M + m.rows - 1) / m.rows;
+    const double tiles = (double)tiles_m * (double)((a.N + m.columns - 1) / m.columns), slots = cus * m.per_cu;
+    double rounds = tiles / slots;
+    rounds = a.offsets ? (rounds > 1 ? rounds : 1) : (double)(int64_t)(rounds + 1 - 1e-9);
+    const double deep = m.split ? (double)(((int64_t)kbs + kSplitWaves - 1) / kSplitWaves) : kbs;
+    const double cost =
+        m.launch + rounds * (m.start + m.step * deep) + m.traffic * tiles * (m.rows + m.columns) * kbs * BK * 1e-6;
+    if (v == 0 || cost < least) best = v, least = cost;
+  }
+  return best;
+}
+
+hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
+  if (a.M == 0 || a.N == 0) return hipSuccess;
+  const MxQuantArgs none{};
+  switch (mx_choose(a)) {
+    case 0: return launch_mx_split<1, 1, 2, false>(a, none, stream);
+    case 1: return launch_mx_split<1, 2, 1, false>(a, none, stream);
+    case 2: return launch_mx_split<2, 2, 1, false>(a, none, stream);
+    case 3: return launch_mx_tiles<MxCfg<64, 64, 2, 2, 4, 128>>(a, stream);
+    case 4: return launch_mx_tiles<MxCfg<64, 128, 1, 4, 3, 128>>(a, stream);
+    case 5: return launch_mx_tiles<MxCfg<128, 128, 2, 2, 4, 128>>(a, stream);
+    case 6: return launch_mx_tiles<MxCfg<128, 256, 1, 4, 3, 128>>(a, stream);
+    default: return launch_mx_tiles<MxCfg<256, 256, 2, 4, 2, 128>>(a, stream);
+  }
+}
+
+// The quantisation costs every workgroup a pass over all rows, 16384 elements at a time:
+// one launch takes 4.6 us against 6.4 in two for 1x7168x2048, 5.3 against
+// 6.6 for 8x7168x2048, and as long for 4x18432x7168.
+bool linear_mx_fused(int64_t M, int64_t, int64_t K) {
+  const int64_t nkb = (K + 255) / 256;
+  return M <= 16 && M * nkb * 256 <= 24576 && M * (mx_code_ld((int)nkb) + mx_scale_ld((int)nkb)) <= kFusedBytes;
+}
+
+// 16 columns a workgroup where those are one round over the CUs (1x1536x7168 5.0 us,
+// with 32 5.8), else 32, which quantise half as often (4x18432x7168 17.8 us, with 16 21.1).
+hipError_t launch_linear_mx_fused(const MxGemmArgs& g, const MxQuantArgs& q, hipStream_t stream) {
+  if (g.N <= 16 * (int64_t)device_cu_count()) return launch_mx_split<1, 1, 2, true>(g, q, stream);
+  return launch_mx_split<1, 2, 1, true>(g, q, stream);
+}
 
 }  // namespace dsfp8
