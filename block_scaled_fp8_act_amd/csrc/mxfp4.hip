@@ -265,7 +265,8 @@ struct MxCfg {
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole 1 KB segments per wave");
   static_assert(WM % 32 == 0 && WN % 32 == 0 && BM % 64 == 0 && BN % 64 == 0, "32x32 subtiles, scale loads of 64 rows");
   static_assert(STAGES >= 2 && (STAGES - 1) * LOADS + S_BUFS * S_INSTR < 64, "the waits of the K loop");
-  static_assert(LDS <= 160 * 1024, "LDS");
+  static constexpr int PER_CU = 160 * 1024 / LDS;  // workgroups that share a CU
+  static_assert(PER_CU >= 1, "LDS");
 };
 
 template <class CF, bool GROUPED>
@@ -452,29 +453,48 @@ __device__ __forceinline__ void mx_step(v16f (&acc)[CF::TM][CF::TN], u32x4 (&fa)
   }
 }
 
-// One workgroup per tile (grouped: per CU, walking the tiles of every expert).
+// Workgroups walk the tiles, a grid's width apart: the next tile's first stages
+// are on their way while the current one is stored, through the place of the
+// last stage.
 template <class CF, bool GROUPED>
 __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS];
   constexpr int S = CF::STAGES, L = CF::LOADS, PH = CF::PHASES;
-  const int64_t tiles_n = (p.N + CF::BN - 1) / CF::BN;
+  static_assert(CF::NW * CF::C_BYTES <= CF::STAGE_BYTES, "the output's staging");
+  const int64_t tiles_m = (p.M + CF::BM - 1) / CF::BM, tiles_n = (p.N + CF::BN - 1) / CF::BN;
   constexpr int SB = CF::ROW / 16;  // blocks of a stage
   const int ng = (int)((p.KB + SB - 1) / SB), left = (int)(p.KB % SB);
   const uint64_t tail = left ? (1ull << (8 * left)) - 1 : ~0ull;  // the blocks of the last stage
   const MxOperands<CF> op(smem);
-  for (int64_t pid = blockIdx.x;; pid += gridDim.x) {
-    MxTile t;
+  int64_t pid = blockIdx.x;
+  auto locate = [&](MxTile& t) __attribute__((always_inline)) {
     if constexpr (GROUPED) {
       const int64_t rt = div_u(pid, tiles_n);
-      if (!mx_find<CF::BM>(p, rt, t)) break;
+      if (!mx_find<CF::BM>(p, rt, t)) return false;
       t.n0 = (pid - rt * tiles_n) * CF::BN;
     } else {
+      if (pid >= tiles_m * tiles_n) return false;
       int64_t tm, tn;
-      tile_of(pid, (p.M + CF::BM - 1) / CF::BM, tiles_n, tm, tn);
+      tile_of(pid, tiles_m, tiles_n, tm, tn);
       t = MxTile{tm * CF::BM, p.M, tn * CF::BN, p.B, p.b_s};
     }
-    MxLoader<CF, GROUPED> ld;
-    ld.init(p, t, smem);
+    return true;
+  };
+  MxTile t;
+  if (!locate(t)) return;
+  MxLoader<CF, GROUPED> ld;
+  auto begin = [&](int from, int to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < S; ++g) {
+      if (g < from || g >= to) continue;
+#pragma unroll
+      for (int n = 0; n < L; ++n) ld.issue(n, g, g);
+      if (g % PH == 0) ld.issue_scales(g);
+    }
+  };
+  ld.init(p, t, smem);
+  begin(0, S - 1);
+  for (;;) {
     v16f acc[CF::TM][CF::TN];
 #pragma unroll
     for (int i = 0; i < CF::TM; ++i)
@@ -488,12 +508,7 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
     if (ng > 0) {
       u32x4 fa[CF::TM], fb[2][CF::TN];
       uint32_t sa[2][CF::TM], sb[2][CF::TN];
-#pragma unroll
-      for (int g = 0; g < S; ++g) {
-#pragma unroll
-        for (int n = 0; n < L; ++n) ld.issue(n, g, g);
-        if (g % PH == 0) ld.issue_scales(g);
-      }
+      begin(S - 1, S);
       // stage 0 has arrived when only the S - 1 later ones may be missing
       wait_vmcnt<(S - 1) * L + CF::scales_in(1, S - 1)>();
       __syncthreads();
@@ -554,11 +569,20 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
           }
         }
       }
-      wait_vmcnt<0>();
     }
+    // what has been loaded past the row's end is no longer on its way
+    wait_vmcnt<0>();
     __syncthreads();
-    mx_store<CF>(p, t, acc, smem);
-    if constexpr (!GROUPED) break;
+    MxTile u;
+    pid += gridDim.x;
+    const bool more = locate(u);
+    if (more) {
+      ld.init(p, u, smem);
+      begin(0, S - 1);
+    }
+    mx_store<CF>(p, t, acc, smem + (S - 1) * CF::STAGE_BYTES);
+    if (!more) break;
+    t = u;
     __syncthreads();
   }
 }
@@ -831,16 +855,12 @@ hipError_t launch_mx_dequant(const MxDequantArgs& args, hipStream_t stream) {
 
 template <class CF>
 static hipError_t launch_mx_tiles(const MxGemmArgs& a, hipStream_t stream) {
-  const int64_t tiles_n = (a.N + CF::BN - 1) / CF::BN;
-  if (a.offsets) {
-    const int64_t some = a.E < a.M ? a.E : a.M;  // at most one short tile per expert that has rows
-    const int64_t most = (some + (a.M - some) / CF::BM) * tiles_n, cus = device_cu_count();
-    hipLaunchKernelGGL((mx_gemm_kernel<CF, true>), dim3((unsigned)(most < cus ? most : cus)), dim3(CF::kThreads), 0,
-                       stream, a);
-  } else {
-    hipLaunchKernelGGL((mx_gemm_kernel<CF, false>), dim3((unsigned)((a.M + CF::BM - 1) / CF::BM * tiles_n)),
-                       dim3(CF::kThreads), 0, stream, a);
-  }
+  const int64_t tiles_n = (a.N + CF::BN - 1) / CF::BN, slots = (int64_t)device_cu_count() * CF::PER_CU;
+  const int64_t some = a.E < a.M ? a.E : a.M;  // at most one short tile per expert that has rows
+  const int64_t tiles = (a.offsets ? some + (a.M - some) / CF::BM : (a.M + CF::BM - 1) / CF::BM) * tiles_n;
+  const dim3 grid((unsigned)(tiles < slots ? tiles : slots)), blk(CF::kThreads);
+  if (a.offsets) hipLaunchKernelGGL((mx_gemm_kernel<CF, true>), grid, blk, 0, stream, a);
+  else hipLaunchKernelGGL((mx_gemm_kernel<CF, false>), grid, blk, 0, stream, a);
   return hipGetLastError();
 }
 
