@@ -653,8 +653,24 @@ def mxfp4_empty(M, K, device, lead=()):
     return q, (s if kb % 16 == 0 else s[..., :kb])
 
 
-def _mx(q, s, what, dim=2):
+def _mx(q, s, what):
     """Checked codes and scales of MXFP4 rows: ``(q, row stride, s, row stride)``."""
+    if (isinstance(q, torch.Tensor) and isinstance(s, torch.Tensor) and q.dtype == torch.uint8 and s.dtype == torch.uint8
+            and q.is_cuda and s.is_cuda and s.dim() == 2):
+        rows, kb = s.shape      # the usual case, as one condition: what _mx_slow asks for
+        if rows > 1 and kb > 0 and q.shape == (rows, 16 * kb):
+            (ldq, qc), (lds, sc) = q.stride(), s.stride()
+            if (qc == 1 and sc == 1 and not (ldq | lds) & 15 and lds >= kb
+                    and (lds == kb or _mx_room(s, rows, lds, (kb + 15) & ~15))):
+                return q, ldq, s, lds
+    return _mx_slow(q, s, what, 2)
+
+
+def _mx_room(s, rows, lds, pad):
+    return s.untyped_storage().nbytes() >= s.storage_offset() + (rows - 1) * lds + pad
+
+
+def _mx_slow(q, s, what, dim):
     if isinstance(q, torch.Tensor) and q.dtype in _MX_VIEWS:
         q = q.view(torch.uint8)
     if isinstance(s, torch.Tensor) and s.dtype in _MX_VIEWS:
@@ -670,7 +686,7 @@ def _mx(q, s, what, dim=2):
         return q, ldq, s, pad
     rows = s.numel() // kb
     lds = pad if rows == 1 else _mx_ld(s, what + "_s")
-    if lds % 16 or s.untyped_storage().nbytes() < s.storage_offset() + (rows - 1) * lds + pad:
+    if lds % 16 or not _mx_room(s, rows, lds, pad):
         raise Dsfp8Error(f"{what}_s: rows of scales must be a multiple of 16 bytes apart, with room for {pad} bytes "
                          "each (mxfp4_empty allocates them so)")
     if ldq % 16:
@@ -682,17 +698,20 @@ def _mx_ld(t, what):
     return _row(t, t.shape[-1]) if t.dim() == 2 else _expert_ld(t, what)
 
 
-def _mx_out(out, M, K, device):
+def _mx_out(out, M, K, t):
+    """Codes and scales for M rows of K columns, the caller's or new ones on t's device, with their row strides."""
+    kb = (K + 31) >> 5
     if out is None:
-        return mxfp4_empty(M, K, device)
+        pad = (kb + 15) & ~15
+        s = t.new_empty((M, pad), dtype=torch.uint8)
+        return t.new_empty((M, 16 * kb), dtype=torch.uint8), 16 * kb, s if pad == kb else s.as_strided((M, kb), (pad, 1)), pad
     q, s = out
-    kb = mxblocks(K)
     _mat(q, "y", (torch.uint8,))
     _mat(s, "s", (torch.uint8,))
-    if q.shape != (M, 16 * kb) or s.shape != (M, kb) or q.device != device or s.device != device:
-        raise Dsfp8Error(f"out must be uint8 {(M, 16 * kb)} and {(M, kb)} on {device}, got {tuple(q.shape)} on "
+    if q.shape != (M, 16 * kb) or s.shape != (M, kb) or q.device != t.device or s.device != t.device:
+        raise Dsfp8Error(f"out must be uint8 {(M, 16 * kb)} and {(M, kb)} on {t.device}, got {tuple(q.shape)} on "
                          f"{q.device} and {tuple(s.shape)} on {s.device}")
-    return q, s
+    return _mx(q, s, "y")
 
 
 def mxfp4_quant(x, out=None):
@@ -702,10 +721,10 @@ def mxfp4_quant(x, out=None):
     codes a byte, the lower column in the low half (columns past K hold 0), and a
     scale byte per block, for x ~= code * 2^(s - 127).  ``out`` may supply ``(q,
     s)`` as :func:`mxfp4_empty` gives them."""
-    _mat(x, "x", (torch.float32, torch.bfloat16))
+    if not _is_mat(x, torch.bfloat16):
+        _mat(x, "x", (torch.float32, torch.bfloat16))
     M, K = x.shape
-    q, s = _mx_out(out, M, K, x.device)
-    _, ldq, _, lds = _mx(q, s, "y")
+    q, ldq, s, lds = _mx_out(out, M, K, x)
     _launch("mxfp4_quant", _lib.load().dsfp8_mxfp4_quant, x.get_device(), x.data_ptr(),
             0 if x.dtype == torch.float32 else 1, M, K, _row(x, K), q.data_ptr(), ldq, s.data_ptr(), lds)
     return q, s
@@ -716,8 +735,7 @@ def silu_mul_mxfp4_quant(g, u, out=None):
     evaluated in fp32 and not rounded before the quantisation)."""
     _gate_pair(g, u)
     M, K = g.shape
-    q, s = _mx_out(out, M, K, g.device)
-    _, ldq, _, lds = _mx(q, s, "y")
+    q, ldq, s, lds = _mx_out(out, M, K, g)
     _launch("silu_mul_mxfp4_quant", _lib.load().dsfp8_silu_mul_mxfp4_quant, g.get_device(), g.data_ptr(), _row(g, K),
             u.data_ptr(), _row(u, K), M, K, q.data_ptr(), ldq, s.data_ptr(), lds)
     return q, s
@@ -730,10 +748,11 @@ def mxfp4_dequant(q, s, K=None, out=None):
     K = MX_BLOCK * kb if K is None else int(K)
     if mxblocks(K) != kb:
         raise Dsfp8Error(f"{kb} blocks hold {MX_BLOCK * (kb - 1) + 1} to {MX_BLOCK * kb} columns, not {K}")
-    _same_device(q.get_device(), s=s)
-    out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device) if out is None else _out(
-        out, (M, K), torch.bfloat16, q.device, "out")
-    _launch("mxfp4_dequant", _lib.load().dsfp8_mxfp4_dequant, q.get_device(), q.data_ptr(), ldq, s.data_ptr(), lds, M, K,
+    dev = q.get_device()
+    if s.get_device() != dev:
+        _same_device(dev, s=s)
+    out = q.new_empty((M, K), dtype=torch.bfloat16) if out is None else _out(out, (M, K), torch.bfloat16, q.device, "out")
+    _launch("mxfp4_dequant", _lib.load().dsfp8_mxfp4_dequant, dev, q.data_ptr(), ldq, s.data_ptr(), lds, M, K,
             out.data_ptr(), _row(out, K))
     return out
 
@@ -748,9 +767,9 @@ def gemm_mxfp4(a, a_s, b, b_s, out=None):
     if b_s.shape[1] != kb:
         raise Dsfp8Error(f"a and b disagree on K: {kb} vs {b_s.shape[1]} blocks")
     dev = a.get_device()
-    _same_device(dev, a_s=a_s, b=b, b_s=b_s)
-    c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device) if out is None else _out(
-        out, (M, N), torch.bfloat16, a.device, "out")
+    if not (a_s.get_device() == b.get_device() == b_s.get_device() == dev):
+        _same_device(dev, a_s=a_s, b=b, b_s=b_s)
+    c = a.new_empty((M, N), dtype=torch.bfloat16) if out is None else _out(out, (M, N), torch.bfloat16, a.device, "out")
     _launch("gemm_mxfp4", _lib.load().dsfp8_gemm_mxfp4, dev, a.data_ptr(), lda, a_s.data_ptr(), ldas, b.data_ptr(), ldb,
             b_s.data_ptr(), ldbs, c.data_ptr(), _row(c, N), M, N, MX_BLOCK * kb)
     return c
@@ -795,7 +814,7 @@ def grouped_gemm_mxfp4(a, a_s, b, b_s, offsets, rows=None, out=None):
     tokens' quantised rows feed the experts without a gathered copy.  Returns bf16 ``[M_total, N]``; rows past
     ``offsets[E]`` are left as they were (unspecified in a new output)."""
     a, lda, a_s, ldas = _mx(a, a_s, "a")
-    b, ldb, b_s, ldbs = _mx(b, b_s, "b", dim=3)
+    b, ldb, b_s, ldbs = _mx_slow(b, b_s, "b", 3)
     E, N, kb = b_s.shape
     if a_s.shape[1] != kb:
         raise Dsfp8Error(f"a and b disagree on K: {a_s.shape[1]} vs {kb} blocks")
@@ -807,8 +826,7 @@ def grouped_gemm_mxfp4(a, a_s, b, b_s, offsets, rows=None, out=None):
         _int32_vec(rows, None, "rows")
         _same_device(dev, rows=rows)
         M = rows.numel()
-    c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device) if out is None else _out(
-        out, (M, N), torch.bfloat16, a.device, "out")
+    c = a.new_empty((M, N), dtype=torch.bfloat16) if out is None else _out(out, (M, N), torch.bfloat16, a.device, "out")
     _launch("grouped_gemm_mxfp4", _lib.load().dsfp8_grouped_gemm_mxfp4, dev, a.data_ptr(), a.shape[0], lda,
             a_s.data_ptr(), ldas, rows.data_ptr() if rows is not None else None, b.data_ptr(), ldb, b_s.data_ptr(), ldbs,
             offsets.data_ptr(), E, M, N, MX_BLOCK * kb, c.data_ptr(), _row(c, N))
@@ -837,7 +855,8 @@ def moe_gate(logits, k, bias=None, score="sigmoid", groups=1, top_groups=None, r
     dev = logits.get_device()
     if bias is not None:
         _vec_f32(bias, E, "bias")
-        _same_device(dev, bias=bias)
+        if bias.get_device() != dev:
+            _same_device(dev, bias=bias)
     if out is None:
         indices, weights = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.bfloat16)
     else:
@@ -856,7 +875,8 @@ _NORM_FMT = {None: 0, "e4m3": 1, "e4m3_ue8m0": 2, "mxfp4": 3}
 
 
 def _norm_weight(w, D, name, dtype):
-    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != dtype or w.shape != (D,) or (D > 1 and w.stride(0) != 1):
+    if (not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != dtype or w.shape != (D,)
+            or not (D <= 1 or w.is_contiguous())):
         raise Dsfp8Error(f"{name} must be a {dtype} CUDA tensor of shape ({D},) with stride 1")
 
 
@@ -877,18 +897,21 @@ def add_rms_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.
     if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
         raise Dsfp8Error("weight must be a bfloat16 or float32 tensor")
     _norm_weight(weight, D, "weight", weight.dtype)
-    _same_device(dev, weight=weight)
+    if weight.get_device() != dev:
+        _same_device(dev, weight=weight)
     rp = gp = pp = None
     ldr = ldg = 0
     if post_weight is not None:
         _norm_weight(post_weight, D, "post_weight", weight.dtype)
-        _same_device(dev, post_weight=post_weight)
+        if post_weight.get_device() != dev:
+            _same_device(dev, post_weight=post_weight)
         pp = post_weight.data_ptr()
     if residual is not None:
         _need(residual, "residual", torch.bfloat16)
         if residual.shape != x.shape:
             raise Dsfp8Error(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
-        _same_device(dev, residual=residual)
+        if residual.get_device() != dev:
+            _same_device(dev, residual=residual)
         rp, ldr = residual.data_ptr(), _row(residual, D)
     if gate is not None:
         g = gate[None] if isinstance(gate, torch.Tensor) and gate.dim() == 1 else gate
@@ -907,14 +930,18 @@ def add_rms_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.
         y = x.new_empty((T, D)) if o[0] is None else _out(o[0], (T, D), torch.bfloat16, x.device, "y")
         ldy = _row(y, D)
     elif quant == "mxfp4":
-        y, s = _mx_out(None if o[0] is None else o[:2], T, D, x.device)
-        _, ldy, _, srs = _mx(y, s, "y")
+        y, ldy, s, srs = _mx_out(None if o[0] is None else o[:2], T, D, x)
         sp, sks = s.data_ptr(), 1
     else:
-        y = _out(o[0], (T, D), torch.uint8, x.device, "y")
-        s = _scales_out(o[1], T, kblocks(D), x.device)
+        y = x.new_empty((T, D), dtype=torch.uint8) if o[0] is None else _out(o[0], (T, D), torch.uint8, x.device, "y")
         ldy = _row(y, D)
-        sp, (srs, sks) = s.data_ptr(), _scale_strides(s)
+        if o[1] is None:        # K-block-major, as new_scales
+            srs, sks = 1, T
+            s = x.new_empty_strided((T, kblocks(D)), (1, T), dtype=torch.float32)
+        else:
+            s = _scales_out(o[1], T, kblocks(D), x.device)
+            srs, sks = _scale_strides(s)
+        sp = s.data_ptr()
     hp, h, ldh = None, None, 0
     if residual is not None:
         h = x.new_empty((T, D)) if o[-1] is None else _out(o[-1], (T, D), torch.bfloat16, x.device, "h")
