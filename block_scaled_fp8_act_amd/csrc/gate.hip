@@ -1,28 +1,36 @@
 // Choice of a token's experts from its router logits on gfx950.
 //
-// A wavefront per token; lane l holds VPT consecutive experts from l * VPT, so
-// that among equal keys the lowest lane, and in it the first, is the lowest
-// expert.  The scores are evaluated in 64 bits and rounded once, so that the
-// choice does not depend on how an exponential is computed: an expert's key is
-// the same fp32 value wherever it is evaluated.  Keys are compared as unsigned
-// integers of the same order, 0 for an expert that is not available.  The
-// maximum over the wave is six DPP steps, and each of the k rounds takes the first
-// lane that holds it.
+// LPT lanes per token, the whole wavefront or a quarter of it; each holds VPT
+// consecutive experts, so that among equal keys the lowest lane, and in it the first,
+// is the lowest expert.  The scores are evaluated in 64 bits and rounded once, so
+// that the choice does not depend on how an exponential is computed: an expert's
+// key is the same fp32 value wherever it is evaluated.  Keys are compared as unsigned
+// integers of the same order, 0 for an expert that is not available.  Each of the k
+// rounds takes the maximum over the token's lanes (DPP steps) and its first
+// holder, which puts itself into the round's slot in LDS.
 #include "device.h"
 #include "launch.h"
 
 namespace dsfp8 {
 namespace {
 
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));  // an access at any address
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+
 constexpr int kGateWaves = 4;
+constexpr int kMaxGateK = 16, kMaxGateGroups = 64;
+constexpr float kNone = -__builtin_inff();  // logit or key of an expert that is not available
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
 
-// Maximum over the wavefront, as a scalar.  Lanes without a source get 0, the least.
-__device__ __forceinline__ uint32_t max_u32_wave(uint32_t v) {
+// Maximum over a token's lanes, in every one of them.  Lanes without a source
+// get 0, the least.
+template <int LPT>
+__device__ __forceinline__ uint32_t max_token(uint32_t v) {
+  if constexpr (LPT == 16) return max_row16_u32(v);
   auto up = [&](uint32_t o) __attribute__((always_inline)) { v = o > v ? o : v; };
   up(dpp_u32<0x111>(v));  // row_shr 1
   up(dpp_u32<0x112>(v));  // row_shr 2
@@ -36,35 +44,73 @@ __device__ __forceinline__ uint32_t max_u32_wave(uint32_t v) {
 // Unsigned integer in the order of the fp32 value (-0 and +0 alike); 0 for -inf.
 __device__ __forceinline__ uint32_t order_u32(float key) {
   const uint32_t b = __float_as_uint(key + 0.0f);
-  return key == -__builtin_inff() ? 0u : ((b >> 31) ? ~b : b | 0x80000000u);
+  return key == kNone ? 0u : ((b >> 31) ? ~b : b | 0x80000000u);
 }
 
-template <int VPT, bool SOFTMAX>
-__global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastDiv per_group) {
-  __shared__ float keys[kGateWaves][64 * VPT];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
-  if (t >= a.T) return;
-  const float kNone = -__builtin_inff();
-  float l[VPT];
+// 1 / v for v >= 1 in 64 bits, within a few units in the last place: the hardware's
+// reciprocal and two Newton steps; 0 for infinity.
+__device__ __forceinline__ double reciprocal(double v) {
+  double r = __builtin_amdgcn_rcp(v);
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int e = lane * VPT + j;
-    l[j] = kNone;
-    if (e < a.E)
-      l[j] = a.bf16_in ? bf16_lo(static_cast<const uint16_t*>(a.logits)[t * a.ldl + e])
-                       : static_cast<const float*>(a.logits)[t * a.ldl + e];
+  for (int i = 0; i < 2; ++i) {
+    const double s = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+    r = r == 0.0 ? r : s;
   }
-  // scores, rounded once to fp32; 0 for an expert whose logit is -inf
-  float score[VPT];
+  return r;
+}
+
+// The two largest of two pairs, each in order.
+__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
+  const float lo = fminf(a1, b1);
+  a1 = fmaxf(a1, b1);
+  a2 = fmaxf(lo, fmaxf(a2, b2));
+}
+
+template <int VPT, int LPT, bool SOFTMAX>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastDiv per_group) {
+  constexpr int TPW = 64 / LPT;  // tokens of a wave
+  __shared__ float keys[kGateWaves][TPW][LPT * VPT];
+  __shared__ float group_score[kGateWaves][TPW][kMaxGateGroups];
+  __shared__ float2 best2[kGateWaves][TPW][LPT];
+  __shared__ int2 slots[kGateWaves][TPW][kMaxGateK];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int sub = (threadIdx.x & 63) / LPT, lane = threadIdx.x % LPT;  // token of the wave, lane of the token
+  const int64_t at = ((int64_t)blockIdx.x * kGateWaves + wave) * TPW + sub;
+  const int64_t t = at < a.T ? at : a.T - 1;  // a row past the last repeats it and stores nothing
+  float l[VPT];
+  const int e0 = lane * VPT;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) l[j] = kNone;
+#pragma unroll
+  for (int j = 0; j < VPT; j += 4) {
+    const int64_t from = t * a.ldl + e0 + j;
+    if (VPT >= 4 && e0 + j + 4 <= a.E) {
+      if (a.bf16_in) {
+        const u32x2u w = *reinterpret_cast<const u32x2u*>(static_cast<const uint16_t*>(a.logits) + from);
+#pragma unroll
+        for (int i = 0; i < 4 && j + i < VPT; ++i) l[j + i] = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+      } else {
+        const u32x4u w = *reinterpret_cast<const u32x4u*>(static_cast<const float*>(a.logits) + from);
+#pragma unroll
+        for (int i = 0; i < 4 && j + i < VPT; ++i) l[j + i] = __uint_as_float(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 && j + i < VPT; ++i)
+        if (e0 + j + i < a.E)
+          l[j + i] = a.bf16_in ? bf16_lo(static_cast<const uint16_t*>(a.logits)[from + i])
+                               : static_cast<const float*>(a.logits)[from + i];
+    }
+  }
+  // keys, of scores rounded once to fp32 (0 for an expert whose logit is -inf)
+  float key[VPT];
   bool bad = false;
   if constexpr (SOFTMAX) {
     float m = kNone;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) m = fmaxf(m, l[j]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    for (int d = 1; d < LPT; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
     double p[VPT], sum = 0.0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -72,75 +118,139 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
       sum += p[j];
     }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    for (int d = 1; d < LPT; d <<= 1) sum += __shfl_xor(sum, d);
+    const double r = reciprocal(sum);  // the largest is 1, so the sum is, unless no expert is available
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) score[j] = l[j] == kNone ? 0.0f : (float)(p[j] / sum);
+    for (int j = 0; j < VPT; ++j) key[j] = l[j] == kNone ? 0.0f : (float)(p[j] * r);
   } else {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) score[j] = l[j] == kNone ? 0.0f : (float)(1.0 / (1.0 + exp(-(double)l[j])));
+    for (int j = 0; j < VPT; ++j) key[j] = l[j] == kNone ? 0.0f : (float)reciprocal(1.0 + exp(-(double)l[j]));
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) keys[wave][sub][e0 + j] = key[j];  // the scores, for the weights
+  float b[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) b[j] = 0.0f;
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < VPT; j += 4) {
+      if (VPT >= 4 && e0 + j + 4 <= a.E) {
+        const u32x4u w = *reinterpret_cast<const u32x4u*>(a.bias + e0 + j);
+#pragma unroll
+        for (int i = 0; i < 4 && j + i < VPT; ++i) b[j + i] = __uint_as_float(w[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 && j + i < VPT; ++i)
+          if (e0 + j + i < a.E) b[j + i] = a.bias[e0 + j + i];
+      }
+    }
   }
   uint32_t u[VPT];
-  float key[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int e = lane * VPT + j;
-    key[j] = score[j];
-    if (a.bias && e < a.E) key[j] += a.bias[e];
+    if (a.bias) key[j] += b[j];
     if (l[j] == kNone) key[j] = kNone;
     bad |= key[j] != key[j];
     u[j] = key[j] != key[j] ? 1u : order_u32(key[j]);  // NaN: available, after every number
   }
   if (a.groups > 1) {
-    // Group g's score on lane g, from the keys in LDS; a group stays if fewer
-    // than top_groups come before it.
+    // A group's score, then its rank: a group stays if fewer than top_groups
+    // come before it.
+    const int gs = (int)per_group.d, gl = gs / VPT;
+    float* gsc = group_score[wave][sub];
+    const bool lanes = gs % VPT == 0;  // gl lanes hold a group
+    if (lanes && (gl & (gl - 1)) == 0) {
+      float t1 = kNone, t2 = kNone;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) keys[wave][lane * VPT + j] = key[j];
-    __builtin_amdgcn_wave_barrier();
-    float t1 = kNone, t2 = kNone;
-    const int gs = (int)per_group.d;
-    if (lane < a.groups) {
-      for (int i = 0; i < gs; ++i) {
-        const float v = keys[wave][lane * gs + i];
-        t2 = v > t1 ? t1 : (v > t2 ? v : t2);
-        t1 = v > t1 ? v : t1;
+      for (int j = 0; j < VPT; ++j) merge2(t1, t2, key[j], kNone);
+      for (int d = 1; d < gl; d <<= 1) merge2(t1, t2, __shfl_xor(t1, d), __shfl_xor(t2, d));
+      if (lane % gl == 0 && e0 < a.E) gsc[lane / gl] = a.bias && t2 != kNone ? t1 + t2 : t1;
+    } else if (lanes) {
+      float t1 = kNone, t2 = kNone;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) merge2(t1, t2, key[j], kNone);
+      best2[wave][sub][lane] = make_float2(t1, t2);
+      __builtin_amdgcn_wave_barrier();
+      for (int g = lane; g < a.groups; g += LPT) {
+        t1 = t2 = kNone;
+        for (int i = 0; i < gl; ++i) {
+          const float2 o = best2[wave][sub][g * gl + i];
+          merge2(t1, t2, o.x, o.y);
+        }
+        gsc[g] = a.bias && t2 != kNone ? t1 + t2 : t1;
+      }
+    } else {
+      for (int g = lane; g < a.groups; g += LPT) {
+        float t1 = kNone, t2 = kNone;
+        for (int i = 0; i < gs; ++i) {
+          // the group's keys again, from the scores
+          const int e = g * gs + i;
+          const float x = a.bf16_in ? bf16_lo(static_cast<const uint16_t*>(a.logits)[t * a.ldl + e])
+                                    : static_cast<const float*>(a.logits)[t * a.ldl + e];
+          const float v = x == kNone ? kNone : keys[wave][sub][e] + (a.bias ? a.bias[e] : 0.0f);
+          merge2(t1, t2, v, kNone);
+        }
+        gsc[g] = a.bias && t2 != kNone ? t1 + t2 : t1;
       }
     }
-    const float gsc = a.bias && t2 != kNone ? t1 + t2 : t1;
-    int ahead = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const float o = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(gsc), g));
-      ahead += o > gsc || (o == gsc && g < lane);
+    __builtin_amdgcn_wave_barrier();
+    uint64_t keep = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += LPT) {
+      const int mine = g0 + lane;
+      const float v = mine < a.groups ? gsc[mine] : kNone;
+      int ahead = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const float o = gsc[g];
+        ahead += o > v || (o == v && g < mine);
+      }
+      const uint64_t stay = __ballot(mine < a.groups && ahead < a.top_groups) >> (LPT * sub);
+      keep |= (LPT == 64 ? stay : stay & 0xffffu) << g0;
     }
-    const uint64_t keep = __ballot(lane < a.groups && ahead < a.top_groups);
+    if (lanes) {
+      const bool out = e0 < a.E && !(keep >> (lane / gl) & 1);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const uint32_t g = fastdiv((uint32_t)(lane * VPT + j), per_group);
-      if (g < 64 && !(keep >> g & 1)) u[j] = 0;
+      for (int j = 0; j < VPT; ++j) u[j] = out ? 0u : u[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const uint32_t g = fastdiv((uint32_t)(e0 + j), per_group);
+        if (g < 64 && !(keep >> g & 1)) u[j] = 0;
+      }
     }
   }
-  bad = __ballot(bad) != 0;
+  {
+    const uint64_t b = __ballot(bad) >> (LPT * sub);
+    bad = (LPT == 64 ? b : b & 0xffffu) != 0;
+  }
 
-  float sum = 0.0f, w = 0.0f;
-  int idx = -1;
+  int2* slot = slots[wave][sub];
+  if (lane < kMaxGateK) slot[lane] = make_int2(-1, 0);
+  __builtin_amdgcn_wave_barrier();
   for (int i = 0; i < a.k; ++i) {
-    uint32_t bu = u[0];
-    int bj = 0;
-    float bs = score[0];
+    uint32_t best = u[0];
 #pragma unroll
-    for (int j = 1; j < VPT; ++j)
-      if (u[j] > bu) bu = u[j], bj = j, bs = score[j];
-    const uint32_t top = max_u32_wave(bu);
-    if (top == 0) break;  // no expert left
-    const int from = __ffsll((unsigned long long)__ballot(bu == top)) - 1;
-    const int e = __builtin_amdgcn_readlane(lane * VPT + bj, from);
-    const float s = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bs), from));
-    sum += s;
-    if (lane == i) idx = e, w = s;
+    for (int j = 1; j < VPT; ++j) best = u[j] > best ? u[j] : best;
+    const uint32_t top = max_token<LPT>(best);
+    const uint64_t have = __ballot(best == top && top != 0) >> (LPT * sub);
+    const int from = __ffsll((unsigned long long)(LPT == 64 ? have : have & 0xffffu)) - 1;  // -1: no expert left
+    if (lane == from) {
+      int first = 0;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (lane == from && j == bj) u[j] = 0;
+      for (int j = VPT - 1; j >= 0; --j) first = u[j] == best ? j : first;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) u[j] = j == first ? 0u : u[j];
+      slot[i] = make_int2(e0 + first, __float_as_int(keys[wave][sub][e0 + first]));
+    }
   }
-  if (lane < a.k) {
+  __builtin_amdgcn_wave_barrier();
+  // Slot i on lane i; the sum over a row of 16 lanes, in a fixed order.
+  const int2 s = slot[lane < kMaxGateK ? lane : kMaxGateK - 1];
+  const int idx = s.x;
+  float w = lane < a.k ? __int_as_float(s.y) : 0.0f;
+  float sum = w;
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d);
+  if (lane < a.k && at < a.T) {
     if (a.renormalize) w = sum > 0.0f ? w / sum : 0.0f;
     w *= a.scale;
     if (bad) w = __uint_as_float(0x7fc00000u);
@@ -149,12 +259,13 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
   }
 }
 
-template <int VPT>
+template <int VPT, int LPT>
 hipError_t launch_gate_of(const GateArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.T + kGateWaves - 1) / kGateWaves)), blk(64 * kGateWaves);
+  constexpr int TPB = kGateWaves * 64 / LPT;
+  const dim3 grid((unsigned)((a.T + TPB - 1) / TPB)), blk(64 * kGateWaves);
   const FastDiv d = make_fastdiv((uint32_t)(a.E / a.groups));
-  if (a.softmax) hipLaunchKernelGGL((gate_kernel<VPT, true>), grid, blk, 0, stream, a, d);
-  else hipLaunchKernelGGL((gate_kernel<VPT, false>), grid, blk, 0, stream, a, d);
+  if (a.softmax) hipLaunchKernelGGL((gate_kernel<VPT, LPT, true>), grid, blk, 0, stream, a, d);
+  else hipLaunchKernelGGL((gate_kernel<VPT, LPT, false>), grid, blk, 0, stream, a, d);
   return hipGetLastError();
 }
 
@@ -162,12 +273,20 @@ hipError_t launch_gate_of(const GateArgs& a, hipStream_t stream) {
 
 hipError_t launch_gate(const GateArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  if (a.E <= 64) return launch_gate_of<1>(a, stream);
-  if (a.E <= 128) return launch_gate_of<2>(a, stream);
-  if (a.E <= 256) return launch_gate_of<4>(a, stream);
-  if (a.E <= 512) return launch_gate_of<8>(a, stream);
-  if (a.E <= 1024) return launch_gate_of<16>(a, stream);
-  return launch_gate_of<64>(a, stream);
+  // A quarter of a wave per token issues less for a token but takes longer for it:
+  // 16384x256 in groups 18.0 us against 20.9, 16384x64 5.9 against 9.5, 4096x128 4.7
+  // against 4.4.
+  if (a.T >= 8192 && a.E <= 256) {
+    if (a.E <= 64) return launch_gate_of<4, 16>(a, stream);
+    if (a.E <= 128) return launch_gate_of<8, 16>(a, stream);
+    return launch_gate_of<16, 16>(a, stream);
+  }
+  if (a.E <= 64) return launch_gate_of<1, 64>(a, stream);
+  if (a.E <= 128) return launch_gate_of<2, 64>(a, stream);
+  if (a.E <= 256) return launch_gate_of<4, 64>(a, stream);
+  if (a.E <= 512) return launch_gate_of<8, 64>(a, stream);
+  if (a.E <= 1024) return launch_gate_of<16, 64>(a, stream);
+  return launch_gate_of<64, 64>(a, stream);
 }
 
 }  // namespace dsfp8
