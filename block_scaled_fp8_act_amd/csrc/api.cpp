@@ -30,6 +30,8 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;  // rows, columns and K below 2^31
 constexpr int64_t kMoeFewMaxDim = (int64_t)1 << 26;  // grids and task numbers of its kernels within 32 bits
 constexpr int64_t kMaxExperts = 65536;
 
+constexpr int64_t kMaxGateTokens = (int64_t)1 << 26;  // a wave each: a launch holds fewer than 2^32 threads
+
 inline int64_t nblk(int64_t n) { return (n + DSFP8_BLOCK - 1) / DSFP8_BLOCK; }
 inline bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 inline bool dim_ok(int64_t v) { return v >= 0 && v < kMaxDim; }
@@ -897,7 +899,7 @@ dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const fl
                             int32_t* indices, int64_t ldi, void* weights, int64_t ldw, hipStream_t stream) {
   if (dtype != DSFP8_DTYPE_F32 && dtype != DSFP8_DTYPE_BF16) return DSFP8_ERR_DTYPE;
   if (score != DSFP8_SCORE_SIGMOID && score != DSFP8_SCORE_SOFTMAX) return DSFP8_ERR_SCORE;
-  if (!dim_ok(T) || E < 1 || E > dsfp8::kMaxRouteExperts || k < 1 || k > 16) return DSFP8_ERR_SHAPE;
+  if (T < 0 || T >= kMaxGateTokens || E < 1 || E > dsfp8::kMaxRouteExperts || k < 1 || k > 16) return DSFP8_ERR_SHAPE;
   if (groups < 1 || groups > 64 || E % groups != 0 || top_groups < 1 || top_groups > groups) return DSFP8_ERR_SHAPE;
   if (k > top_groups * (E / groups)) return DSFP8_ERR_SHAPE;
   DSFP8_TRY(check_mat(logits, T, E, ldl, dtype == DSFP8_DTYPE_F32 ? 4 : 2));

@@ -217,55 +217,46 @@ __device__ __forceinline__ bool mx_find(const MxGemmArgs& p, int64_t want, MxTil
 // bytes, the 32 columns of one block of row fr, and that block's scale byte, which
 // the instruction applies.
 //
-// The operands go through a ring of LDS stages, filled by buffer_load ... lds.
-// A stage holds 64 bytes of a row, 128 columns, two matrix instructions deep:
-// four of them take the room of two of 128 bytes, but three are in flight when
-// the fourth is used.  What bounds the large products is how soon the operands
-// arrive (a 256x256 tile without its matrix instructions took 86% of its time
-// with two stages of 128 bytes), so bytes in flight count.  The scale bytes of four
-// stages (16 bytes a row) are loaded together, one load per 64 rows, into a
-// ring of two buffers behind the stages.
+// The operands go through the same ring of LDS stages as the other tiled
+// products', filled by buffer_load ... lds; a stage is a K-block of 128 bytes a row,
+// 256 columns, four matrix instructions deep, read without bank conflicts through
+// the XOR swizzle.  The scale bytes of two K-blocks (16 bytes a row) are loaded
+// together, one load per 64 rows, into buffers of their own behind the stages.
 //
 // A matrix instruction of this format takes half as long as one of 8 bits, so
 // its operands are read one step (64 columns) ahead into registers, and over the
-// stages' border too: the barrier that hands over the next stage comes before
-// the second step of the current one, whose operands are in registers by then.
+// K-blocks' border too: the barrier that hands over the next K-block comes before
+// the last step of the current one, whose operands are in registers by then.
 // The stage it leaves is refilled behind that step's instructions.
+//
+// 256x256 tiles, 4096x7168x18432: 269 us (4.0 PFLOP/s; 4096x18432x7168 292).  Two
+// things bound it, close together: without the loads the rest takes 228 us (the matrix
+// cores at the clock that the power allows: 6.1-7.1 PFLOP/s from registers alone),
+// without the matrix instructions 230 us (of which the scales' loads, a line per
+// row, are 27; LDS reads alone take 116).  Stages of 64 bytes a row, four of
+// them or three, took 294 us; waves of 128x128, four a workgroup, 290.
 
-// Where 16-byte chunk c of row r lies, for rows of 64 or 128 bytes: chunk c ^ key.
-// The 8 rows of an aligned group of 8 lie in distinct 16-byte slots of 128 bytes of
-// banks, the 16 rows of an aligned group of 16 in distinct slots of 256 bytes.
-template <int ROW>
-__device__ __forceinline__ int mx_key(int r) {
-  return ROW == 128 ? swz_key(r) : ((r >> 1) & 3) ^ ((r >> 3) & 1);
-}
-
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int ROW_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
 struct MxCfg {
-  static constexpr int ROW = ROW_;              // bytes of a row in a stage
-  static constexpr int STEPS = ROW / 32;        // matrix instructions deep
-  static constexpr int PHASES = 256 / ROW;      // stages of one load of scales
-  static constexpr int RPI = 1024 / ROW;        // rows of one load instruction
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
   static constexpr int NW = WAVES_M * WAVES_N;
   static constexpr int kThreads = 64 * NW;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int TM = WM / 32, TN = WN / 32;
-  static constexpr int A_BYTES = BM * ROW, B_BYTES = BN * ROW, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int A_INSTR = A_BYTES / 1024 / NW, B_INSTR = B_BYTES / 1024 / NW, LOADS = A_INSTR + B_INSTR;
   static constexpr int S_ROWS = BM + BN, S_INSTR = (S_ROWS / 64 + NW - 1) / NW;  // scale loads of a wave
-  static constexpr int S_BYTES = S_INSTR * NW * 1024, S_BUFS = (STAGES + PHASES - 2) / PHASES + 1;
+  static constexpr int S_BYTES = S_INSTR * NW * 1024, S_BUFS = STAGES / 2 + 1;
   static constexpr int C_BYTES = 32 * WN * 2;  // 32 rows of a wave's output
-  static constexpr int RING = STAGES * STAGE_BYTES + S_BUFS * S_BYTES;
-  static constexpr int LDS = RING > NW * C_BYTES ? RING : NW * C_BYTES;
-  // Scale loads that go with stages a .. b.
-  static constexpr int scales_in(int a, int b) {
-    return b < a ? 0 : (b / PHASES - (a + PHASES - 1) / PHASES + 1) * S_INSTR;
-  }
+  static constexpr int LDS = STAGES * STAGE_BYTES + S_BUFS * S_BYTES;
+  static constexpr int PER_CU = 160 * 1024 / LDS;  // workgroups that share a CU
+  // Scale loads that go with K-blocks a .. b (every second one).
+  static constexpr int scales_in(int a, int b) { return b < a ? 0 : (b / 2 - (a + 1) / 2 + 1) * S_INSTR; }
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole 1 KB segments per wave");
   static_assert(WM % 32 == 0 && WN % 32 == 0 && BM % 64 == 0 && BN % 64 == 0, "32x32 subtiles, scale loads of 64 rows");
+  static_assert(NW % 2 == 0, "a wave's segments start at rows that agree modulo 16");
   static_assert(STAGES >= 2 && (STAGES - 1) * LOADS + S_BUFS * S_INSTR < 64, "the waits of the K loop");
-  static constexpr int PER_CU = 160 * 1024 / LDS;  // workgroups that share a CU
+  static_assert(NW * C_BYTES <= STAGE_BYTES, "the output's staging");
   static_assert(PER_CU >= 1, "LDS");
 };
 
@@ -276,7 +267,7 @@ struct MxLoader {
   // past the matrix lies past the descriptor's end by itself); grouped rows may
   // be anywhere.
   uint32_t offA[GROUPED ? CF::A_INSTR : 1], offB, stepA, stepB, soff[CF::S_INSTR];
-  uint32_t kc;  // byte within the stage's row of every load's chunk (a wave's rows agree modulo 16)
+  uint32_t kc;  // byte within the K-block of every load's chunk (a wave's rows agree modulo 16)
   uint32_t lds0, sds0;
   uint32_t KR;  // bytes of a row's codes
   int wave;
@@ -298,21 +289,20 @@ struct MxLoader {
       const int32_t v = p.rows[t.m0 + r];
       return (uint32_t)(v < 0 ? 0 : (v < p.a_rows ? v : p.a_rows - 1));
     };
-    constexpr int C = CF::ROW / 16;  // chunks of a row
-    const int r0 = wave * CF::RPI + lane / C;
-    kc = (uint32_t)((lane % C) ^ mx_key<CF::ROW>(r0)) * 16;
+    const int r0 = wave * 8 + (lane >> 3);
+    kc = (uint32_t)((lane & 7) ^ swz_key(r0)) * 16;
     if constexpr (GROUPED) {
 #pragma unroll
       for (int n = 0; n < CF::A_INSTR; ++n) {
-        const int r = r0 + CF::NW * CF::RPI * n;
+        const int r = r0 + CF::NW * 8 * n;
         offA[n] = r < ra ? a_row(r) * (uint32_t)p.lda + kc : kOob;
       }
     } else {
       offA[0] = (uint32_t)(r0 * p.lda) + kc;
     }
     offB = (uint32_t)(r0 * p.ldb) + kc;
-    stepA = (uint32_t)(CF::NW * CF::RPI * p.lda);
-    stepB = (uint32_t)(CF::NW * CF::RPI * p.ldb);
+    stepA = (uint32_t)(CF::NW * 8 * p.lda);
+    stepB = (uint32_t)(CF::NW * 8 * p.ldb);
 #pragma unroll
     for (int n = 0; n < CF::S_INSTR; ++n) {
       const int g = (wave + CF::NW * n) * 64 + lane, r = g < CF::BM ? g : g - CF::BM;
@@ -324,20 +314,20 @@ struct MxLoader {
     sds0 = lds0 + (uint32_t)(CF::STAGES * CF::STAGE_BYTES + wave * 1024);
   }
 
-  // Load n of stage g of the row (g counts along K) into ring place `at`; one
-  // past the row's end fetches nothing (its lanes are out of range and read as zero).
-  __device__ __forceinline__ void issue(int n, int g, int place) const {
+  // Load n of K-block kb into ring place `place`; one past the row's end fetches
+  // nothing (its lanes are out of range and read as zero).
+  __device__ __forceinline__ void issue(int n, int kb, int place) const {
     const bool a = n < CF::A_INSTR;
     const int i = a ? n : n - CF::A_INSTR;
-    const uint32_t kbyte = (uint32_t)g * CF::ROW;
+    const uint32_t kbyte = (uint32_t)kb * BK;
     const uint32_t at = lds0 + (uint32_t)(place * CF::STAGE_BYTES + (a ? 0 : CF::A_BYTES) + (wave + CF::NW * i) * 1024);
     const uint32_t off = !a ? offB + (uint32_t)i * stepB : (GROUPED ? offA[GROUPED ? i : 0] : offA[0] + (uint32_t)i * stepA);
     dma_b128(a ? rsA : rsB, at, kbyte + kc < KR ? off : kOob, kbyte);
   }
-  // The scales of the PHASES stages from g, a multiple of that.
-  __device__ __forceinline__ void issue_scales(int g) const {
-    const bool in = (uint32_t)g * CF::ROW < KR;
-    const int q = g / CF::PHASES;
+  // The scales of K-blocks kb and kb + 1 (kb even).
+  __device__ __forceinline__ void issue_scales(int kb) const {
+    const bool in = (uint32_t)kb * BK < KR;
+    const int q = kb / 2;
 #pragma unroll
     for (int n = 0; n < CF::S_INSTR; ++n)
       dma_b128((wave + CF::NW * n) * 64 < CF::BM ? rsAS : rsBS,
@@ -345,12 +335,12 @@ struct MxLoader {
   }
 };
 
-// A wave's operands: fragments of one step, and the scale bytes of a stage's two.
+// A wave's operands: fragments of one step, and the scale bytes of two.
 template <class CF>
 struct MxOperands {
   const uint8_t* smem;
   int at, bt, sat, sbt;  // in a stage, and in a buffer of scales
-  int lf[CF::STEPS];
+  int lf[4];
   int shift;
 
   __device__ __forceinline__ explicit MxOperands(const uint8_t* smem) : smem(smem) {
@@ -358,26 +348,27 @@ struct MxOperands {
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int fr = lane & 31, fg = lane >> 5;
     const int wm = wave / CF::WAVES_N * CF::WM, wn = wave % CF::WAVES_N * CF::WN;
-    at = wm * CF::ROW;
-    bt = CF::A_BYTES + wn * CF::ROW;
+    at = wm * BK;
+    bt = CF::A_BYTES + wn * BK;
     sat = CF::STAGES * CF::STAGE_BYTES + (wm + fr) * 16;
     sbt = CF::STAGES * CF::STAGE_BYTES + (CF::BM + wn + fr) * 16;
     shift = 8 * fg;
 #pragma unroll
-    for (int h = 0; h < CF::STEPS; ++h) lf[h] = fr * CF::ROW + (((2 * h + fg) ^ mx_key<CF::ROW>(fr)) << 4);
+    for (int h = 0; h < 4; ++h) lf[h] = fr * BK + (((2 * h + fg) ^ swz_key(fr)) << 4);
   }
   __device__ __forceinline__ u32x4 a(int place, int h, int i) const {
-    return *reinterpret_cast<const u32x4*>(smem + place * CF::STAGE_BYTES + lf[h] + at + 32 * i * CF::ROW);
+    return *reinterpret_cast<const u32x4*>(smem + place * CF::STAGE_BYTES + lf[h] + at + 32 * i * BK);
   }
   __device__ __forceinline__ u32x4 b(int place, int h, int j) const {
-    return *reinterpret_cast<const u32x4*>(smem + place * CF::STAGE_BYTES + lf[h] + bt + 32 * j * CF::ROW);
+    return *reinterpret_cast<const u32x4*>(smem + place * CF::STAGE_BYTES + lf[h] + bt + 32 * j * BK);
   }
-  // Dword d of the rows' scales in stage g, for steps 2d and 2d + 1: step h uses
-  // byte 2h + fg of a row's, byte 0 or 2 of the dword shifted by fg bytes.  `mask`
-  // clears the blocks that a short last stage does not have: their codes read as
-  // zero, but their scale bytes may hold anything, and 255 would make NaN of them.
-  __device__ __forceinline__ void scales(int g, int d, uint32_t mask, uint32_t (&sa)[CF::TM], uint32_t (&sb)[CF::TN]) const {
-    const uint8_t* b = smem + g / CF::PHASES % CF::S_BUFS * CF::S_BYTES + g % CF::PHASES * (CF::ROW / 16) + 4 * d;
+  // Dword d of the rows' scales in K-block kb, for steps 2d and 2d + 1: step h uses
+  // byte 2h + fg of a row's eight, byte 0 or 2 of the dword shifted by fg bytes.
+  // `mask` clears the blocks that a short last K-block does not have: their codes
+  // read as zero, but their scale bytes may hold anything, and 255 would make NaN
+  // of them.
+  __device__ __forceinline__ void scales(int kb, int d, uint32_t mask, uint32_t (&sa)[CF::TM], uint32_t (&sb)[CF::TN]) const {
+    const uint8_t* b = smem + kb / 2 % CF::S_BUFS * CF::S_BYTES + kb % 2 * 8 + 4 * d;
 #pragma unroll
     for (int i = 0; i < CF::TM; ++i) sa[i] = (*reinterpret_cast<const uint32_t*>(b + sat + 32 * i * 16) & mask) >> shift;
 #pragma unroll
@@ -439,7 +430,7 @@ __device__ __forceinline__ void mx_store(const MxGemmArgs& p, const MxTile& t, c
   }
 }
 
-// Step H of a stage; follow(i) is called behind the instructions of each
+// Step H of a K-block; follow(i) is called behind the instructions of each
 // subtile row i, whose operand is then free.
 template <class CF, int H, class Follow>
 __device__ __forceinline__ void mx_step(v16f (&acc)[CF::TM][CF::TN], u32x4 (&fa)[CF::TM], const u32x4 (&fb)[CF::TN],
@@ -459,12 +450,10 @@ __device__ __forceinline__ void mx_step(v16f (&acc)[CF::TM][CF::TN], u32x4 (&fa)
 template <class CF, bool GROUPED>
 __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::LDS];
-  constexpr int S = CF::STAGES, L = CF::LOADS, PH = CF::PHASES;
-  static_assert(CF::NW * CF::C_BYTES <= CF::STAGE_BYTES, "the output's staging");
+  constexpr int S = CF::STAGES, L = CF::LOADS;
   const int64_t tiles_m = (p.M + CF::BM - 1) / CF::BM, tiles_n = (p.N + CF::BN - 1) / CF::BN;
-  constexpr int SB = CF::ROW / 16;  // blocks of a stage
-  const int ng = (int)((p.KB + SB - 1) / SB), left = (int)(p.KB % SB);
-  const uint64_t tail = left ? (1ull << (8 * left)) - 1 : ~0ull;  // the blocks of the last stage
+  const int nkb = (int)((p.KB + 7) / 8), left = (int)(p.KB & 7);
+  const uint64_t tail = left ? (1ull << (8 * left)) - 1 : ~0ull;  // the blocks of the last K-block
   const MxOperands<CF> op(smem);
   int64_t pid = blockIdx.x;
   auto locate = [&](MxTile& t) __attribute__((always_inline)) {
@@ -485,11 +474,11 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
   MxLoader<CF, GROUPED> ld;
   auto begin = [&](int from, int to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int g = 0; g < S; ++g) {
-      if (g < from || g >= to) continue;
+    for (int kb = 0; kb < S; ++kb) {
+      if (kb < from || kb >= to) continue;
 #pragma unroll
-      for (int n = 0; n < L; ++n) ld.issue(n, g, g);
-      if (g % PH == 0) ld.issue_scales(g);
+      for (int n = 0; n < L; ++n) ld.issue(n, kb, kb);
+      if (kb % 2 == 0) ld.issue_scales(kb);
     }
   };
   ld.init(p, t, smem);
@@ -502,73 +491,57 @@ __global__ __launch_bounds__(CF::kThreads) void mx_gemm_kernel(MxGemmArgs p) {
       for (int j = 0; j < CF::TN; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    // The loop over the stages has no branch inside, since the compiler would
+    // The loop over the K-blocks has no branch inside, since the compiler would
     // move matrix instructions across it: loads past the row's end fetch nothing,
     // and the same numbers of them are in flight at every wait.
-    if (ng > 0) {
+    if (nkb > 0) {
       u32x4 fa[CF::TM], fb[2][CF::TN];
       uint32_t sa[2][CF::TM], sb[2][CF::TN];
       begin(S - 1, S);
-      // stage 0 has arrived when only the S - 1 later ones may be missing
+      // K-block 0 has arrived when only the S - 1 later ones may be missing
       wait_vmcnt<(S - 1) * L + CF::scales_in(1, S - 1)>();
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < CF::TN; ++j) fb[0][j] = op.b(0, 0, j);
 #pragma unroll
       for (int i = 0; i < CF::TM; ++i) fa[i] = op.a(0, 0, i);
-      op.scales(0, 0, ng == 1 ? (uint32_t)tail : ~0u, sa[0], sb[0]);
+      op.scales(0, 0, nkb == 1 ? (uint32_t)tail : ~0u, sa[0], sb[0]);
       constexpr int PER = (L + CF::TM - 1) / CF::TM;
       int place = 0;
-      auto run = [&](int g, auto phase) __attribute__((always_inline)) {  // phase: g % PHASES
-        constexpr int X = decltype(phase)::value;
-        // registers of the scales of the stage's first and last steps, and of the next stage's first
-        constexpr int C0 = CF::STEPS == 4 ? 0 : X & 1, C1 = CF::STEPS == 4 ? 1 : C0, C2 = CF::STEPS == 4 ? 0 : 1 - C0;
+      auto run = [&](int kb, auto odd) __attribute__((always_inline)) {
+        constexpr int X = decltype(odd)::value;
         const int next = place + 1 == S ? 0 : place + 1;
         auto ahead = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
           for (int j = 0; j < CF::TN; ++j) fb[h & 1][j] = op.b(place, h, j);
         };
-        if constexpr (CF::STEPS == 4) {
-          op.scales(g, 1, g + 1 >= ng ? (uint32_t)(tail >> 32) : ~0u, sa[1], sb[1]);
-          ahead(1);
-          mx_step<CF, 0>(acc, fa, fb[0], sa[0], sb[0], [&](int i) { fa[i] = op.a(place, 1, i); });
-          ahead(2);
-          mx_step<CF, 1>(acc, fa, fb[1], sa[0], sb[0], [&](int i) { fa[i] = op.a(place, 2, i); });
-        }
-        ahead(CF::STEPS - 1);
-        mx_step<CF, 0>(acc, fa, fb[0], sa[C1], sb[C1], [&](int i) { fa[i] = op.a(place, CF::STEPS - 1, i); });
-        // stage g + 1, when g + 2 .. g + S - 1 are missing
+        op.scales(kb, 1, kb + 1 >= nkb ? (uint32_t)(tail >> 32) : ~0u, sa[1], sb[1]);
+        ahead(1);
+        mx_step<CF, 0>(acc, fa, fb[0], sa[0], sb[0], [&](int i) { fa[i] = op.a(place, 1, i); });
+        ahead(2);
+        mx_step<CF, 1>(acc, fa, fb[1], sa[0], sb[0], [&](int i) { fa[i] = op.a(place, 2, i); });
+        ahead(3);
+        mx_step<CF, 2>(acc, fa, fb[0], sa[1], sb[1], [&](int i) { fa[i] = op.a(place, 3, i); });
+        // K-block kb + 1, when kb + 2 .. kb + S - 1 are missing
         wait_vmcnt<(S - 2) * L + CF::scales_in(X + 2, X + S - 1)>();
         __syncthreads();
-        op.scales(g + 1, 0, g + 2 >= ng ? (uint32_t)tail : ~0u, sa[C2], sb[C2]);
+        op.scales(kb + 1, 0, kb + 2 >= nkb ? (uint32_t)tail : ~0u, sa[0], sb[0]);
 #pragma unroll
         for (int j = 0; j < CF::TN; ++j) fb[0][j] = op.b(next, 0, j);
-        mx_step<CF, 1>(acc, fa, fb[1], sa[C1], sb[C1], [&](int i) __attribute__((always_inline)) {
+        mx_step<CF, 3>(acc, fa, fb[1], sa[1], sb[1], [&](int i) __attribute__((always_inline)) {
           fa[i] = op.a(next, 0, i);
 #pragma unroll
-          for (int n = i * PER; n < (i + 1) * PER && n < L; ++n) ld.issue(n, g + S, place);
-          if (i == CF::TM - 1 && (X + S) % PH == 0) ld.issue_scales(g + S);
+          for (int n = i * PER; n < (i + 1) * PER && n < L; ++n) ld.issue(n, kb + S, place);
+          if (i == CF::TM - 1 && (X + S) % 2 == 0) ld.issue_scales(kb + S);
         });
         place = next;
       };
-      int g = 0;
-      for (; g + PH <= ng; g += PH) {
-        run(g, std::integral_constant<int, 0>{});
-        run(g + 1, std::integral_constant<int, 1>{});
-        if constexpr (PH == 4) {
-          run(g + 2, std::integral_constant<int, 2>{});
-          run(g + 3, std::integral_constant<int, 3>{});
-        }
+      int kb = 0;
+      for (; kb + 1 < nkb; kb += 2) {
+        run(kb, std::integral_constant<int, 0>{});
+        run(kb + 1, std::integral_constant<int, 1>{});
       }
-      if (g < ng) {
-        run(g, std::integral_constant<int, 0>{});
-        if constexpr (PH == 4) {
-          if (g + 1 < ng) {
-            run(g + 1, std::integral_constant<int, 1>{});
-            if (g + 2 < ng) run(g + 2, std::integral_constant<int, 2>{});
-          }
-        }
-      }
+      if (kb < nkb) run(kb, std::integral_constant<int, 0>{});
     }
     // what has been loaded past the row's end is no longer on its way
     wait_vmcnt<0>();
@@ -853,76 +826,91 @@ hipError_t launch_mx_dequant(const MxDequantArgs& args, hipStream_t stream) {
   });
 }
 
+// The variants and the cost of a product in each, in us:
+//   launch + rounds * (start + step * K-blocks) + traffic * MB
+// with rounds of workgroups over the CUs, K-blocks of 256 columns that one wave
+// walks (split: an eighth of them), and the MB that all tiles load (rows of both
+// operands).  Fitted to 108 dense products of 1 to 4096 rows and 93 grouped ones of
+// 0.3 to 1500 rows an expert, weights past the caches: taking the least is within
+// 5.3% (grouped 2.8%) of the best of thirteen variants in the mean, 32% (19%) at
+// most.  Grouped products take five of the seven.
+struct MxCost {
+  float launch, start, step, traffic;
+};
+struct MxVariant {
+  int rows, columns, per_cu;  // tile, workgroups that share a CU
+  bool split;
+  MxCost dense, grouped;
+};
+constexpr MxCost kNever = {1e30f, 0.0f, 0.0f, 0.0f};
+constexpr MxVariant kMxVariants[] = {
+    {16, 16, 2, true, {1.899f, 0.838f, 0.430f, 0.0479f}, kNever},
+    {16, 32, 3, true, {2.277f, 0.307f, 0.706f, 0.0642f}, {2.777f, 1.567f, 0.0f, 0.0690f}},
+    {32, 32, 2, true, {2.125f, 0.598f, 0.911f, 0.0491f}, {2.877f, 1.822f, 0.0f, 0.0588f}},
+    {64, 64, 2, false, {2.009f, 1.881f, 0.313f, 0.0382f}, kNever},
+    {64, 128, 2, false, {1.935f, 1.786f, 0.467f, 0.0457f}, {5.626f, 0.817f, 0.262f, 0.0711f}},
+    {128, 128, 2, false, {3.529f, 0.0f, 0.845f, 0.0327f}, {6.981f, 0.026f, 0.533f, 0.0530f}},
+    {256, 256, 1, false, {5.583f, 0.0f, 1.745f, 0.0f}, {12.626f, 0.243f, 0.892f, 0.0492f}},
+};
+
+// Row tiles of a grouped product: a short one for every expert that may have
+// rows, and the rest in whole ones; never fewer than there are.
+static int64_t grouped_tiles(const MxGemmArgs& a, int rows) {
+  const int64_t some = a.E < a.M ? a.E : a.M;
+  return some + (a.M - some) / rows;
+}
+
+constexpr double kMaxSplitTiles = 1 << 22;  // a workgroup each: a launch holds fewer than 2^32 threads
+
+static int mx_choose(const MxGemmArgs& a) {
+  const bool grouped = a.offsets != nullptr;
+  const int64_t kbs = (a.KB + 7) / 8;
+  int best = 0;
+  double least = 1e30;
+  for (int v = 0; v < (int)(sizeof kMxVariants / sizeof *kMxVariants); ++v) {
+    const MxVariant& m = kMxVariants[v];
+    const MxCost& c = grouped ? m.grouped : m.dense;
+    const double tiles = (double)(grouped ? grouped_tiles(a, m.rows) : (a.M + m.rows - 1) / m.rows) *
+                         (double)((a.N + m.columns - 1) / m.columns);
+    if (m.split && tiles > kMaxSplitTiles) continue;
+    const double part = tiles / ((double)device_cu_count() * m.per_cu);
+    const double rounds = grouped ? (part > 1 ? part : 1) : __builtin_ceil(part);
+    const double deep = (double)(m.split ? (kbs + kSplitWaves - 1) / kSplitWaves : kbs);
+    const double cost =
+        c.launch + rounds * (c.start + c.step * deep) + c.traffic * tiles * (m.rows + m.columns) * (double)kbs * BK * 1e-6;
+    if (cost < least) best = v, least = cost;
+  }
+  return best;
+}
+
 template <class CF>
 static hipError_t launch_mx_tiles(const MxGemmArgs& a, hipStream_t stream) {
-  const int64_t tiles_n = (a.N + CF::BN - 1) / CF::BN, slots = (int64_t)device_cu_count() * CF::PER_CU;
-  const int64_t some = a.E < a.M ? a.E : a.M;  // at most one short tile per expert that has rows
-  const int64_t tiles = (a.offsets ? some + (a.M - some) / CF::BM : (a.M + CF::BM - 1) / CF::BM) * tiles_n;
+  const int64_t tiles_m = a.offsets ? grouped_tiles(a, CF::BM) : (a.M + CF::BM - 1) / CF::BM;
+  const int64_t tiles = tiles_m * ((a.N + CF::BN - 1) / CF::BN), slots = (int64_t)device_cu_count() * CF::PER_CU;
   const dim3 grid((unsigned)(tiles < slots ? tiles : slots)), blk(CF::kThreads);
-  if (a.offsets) hipLaunchKernelGGL((mx_gemm_kernel<CF, true>), grid, blk, 0, stream, a);
-  else hipLaunchKernelGGL((mx_gemm_kernel<CF, false>), grid, blk, 0, stream, a);
+  if constexpr (CF::BN > 64) {
+    if (a.offsets) {
+      hipLaunchKernelGGL((mx_gemm_kernel<CF, true>), grid, blk, 0, stream, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((mx_gemm_kernel<CF, false>), grid, blk, 0, stream, a);
   return hipGetLastError();
 }
 
 template <int FM, int FN, int D, bool FUSED>
 static hipError_t launch_mx_split(const MxGemmArgs& a, const MxQuantArgs& x, hipStream_t stream) {
   using CF = SplitCfg<FM, FN, D, FUSED>;
-  const int64_t tiles_n = (a.N + CF::TN - 1) / CF::TN;
-  const dim3 blk(64 * kSplitWaves);
-  if (a.offsets) {
-    if constexpr (!FUSED) {
-      const int64_t some = a.E < a.M ? a.E : a.M;
-      hipLaunchKernelGGL((mx_split_kernel<FM, FN, D, false, true>), dim3((unsigned)((some + (a.M - some) / CF::TM) * tiles_n)),
-                         blk, 0, stream, a, x);
+  const int64_t tiles_m = a.offsets ? grouped_tiles(a, CF::TM) : (FUSED ? 1 : (a.M + CF::TM - 1) / CF::TM);
+  const dim3 grid((unsigned)(tiles_m * ((a.N + CF::TN - 1) / CF::TN))), blk(64 * kSplitWaves);
+  if constexpr (FN > 1 && !FUSED) {
+    if (a.offsets) {
+      hipLaunchKernelGGL((mx_split_kernel<FM, FN, D, false, true>), grid, blk, 0, stream, a, x);
+      return hipGetLastError();
     }
-  } else {
-    const int64_t tiles_m = FUSED ? 1 : (a.M + CF::TM - 1) / CF::TM;
-    hipLaunchKernelGGL((mx_split_kernel<FM, FN, D, FUSED, false>), dim3((unsigned)(tiles_m * tiles_n)), blk, 0, stream, a, x);
   }
+  hipLaunchKernelGGL((mx_split_kernel<FM, FN, D, FUSED, false>), grid, blk, 0, stream, a, x);
   return hipGetLastError();
-}
-
-// The variants and the cost of a product in each, in us:
-//   launch + rounds * (start + step * K-blocks) + traffic * MB
-// with rounds of workgroups over the CUs, K-blocks of 256 columns that one wave
-// walks (split: an eighth of them), and the MB that all tiles load (rows of both
-// operands).  Fitted to 120 dense and grouped products of 1 to 16384 rows in
-// 13 variants, weights past the caches; taking the least of these eight is within
-// 4.8% of the best of all 13 in the mean, 30% at most.
-struct MxVariant {
-  int rows, columns, per_cu;  // tile, workgroups that share a CU
-  bool split;
-  float launch, start, step, traffic;
-};
-constexpr MxVariant kMxVariants[] = {
-    {16, 16, 2, true, 1.761f, 0.782f, 0.462f, 0.0467f},    // 0
-    {16, 32, 3, true, 2.180f, 0.220f, 0.744f, 0.0636f},    // 1
-    {32, 32, 2, true, 2.004f, 0.476f, 1.008f, 0.0468f},    // 2
-    {64, 64, 2, false, 1.870f, 1.641f, 0.317f, 0.0468f},   // 3
-    {64, 128, 2, false, 0.774f, 2.647f, 0.506f, 0.0451f},  // 4
-    {128, 128, 1, false, 1.803f, 2.644f, 0.735f, 0.0f},    // 5
-    {128, 256, 1, false, 1.158f, 4.086f, 1.198f, 0.0017f}, // 6
-    {256, 256, 1, false, 5.285f, 0.0f, 1.781f, 0.0f},      // 7
-};
-
-static int mx_choose(const MxGemmArgs& a) {
-  const double cus = device_cu_count(), kbs = (double)((a.KB + 7) / 8);
-  int best = 0;
-  double least = 0;
-  for (int v = 0; v < (int)(sizeof kMxVariants / sizeof *kMxVariants); ++v) {
-    const MxVariant& m = kMxVariants[v];
-    // grouped: a short tile per expert that may have rows, and the rest in whole ones
-    const int64_t some = a.offsets ? (a.E < a.M ? a.E : a.M) : 0;
-    const int64_t tiles_m = a.offsets ? some + (a.M - some) / m.rows : (a.M + m.rows - 1) / m.rows;
-    const double tiles = (double)tiles_m * (double)((a.N + m.columns - 1) / m.columns), slots = cus * m.per_cu;
-    double rounds = tiles / slots;
-    rounds = a.offsets ? (rounds > 1 ? rounds : 1) : (double)(int64_t)(rounds + 1 - 1e-9);
-    const double deep = m.split ? (double)(((int64_t)kbs + kSplitWaves - 1) / kSplitWaves) : kbs;
-    const double cost =
-        m.launch + rounds * (m.start + m.step * deep) + m.traffic * tiles * (m.rows + m.columns) * kbs * BK * 1e-6;
-    if (v == 0 || cost < least) best = v, least = cost;
-  }
-  return best;
 }
 
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
@@ -932,20 +920,19 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
     case 0: return launch_mx_split<1, 1, 2, false>(a, none, stream);
     case 1: return launch_mx_split<1, 2, 1, false>(a, none, stream);
     case 2: return launch_mx_split<2, 2, 1, false>(a, none, stream);
-    case 3: return launch_mx_tiles<MxCfg<64, 64, 2, 2, 4, 128>>(a, stream);
-    case 4: return launch_mx_tiles<MxCfg<64, 128, 1, 4, 3, 128>>(a, stream);
-    case 5: return launch_mx_tiles<MxCfg<128, 128, 2, 2, 4, 128>>(a, stream);
-    case 6: return launch_mx_tiles<MxCfg<128, 256, 1, 4, 3, 128>>(a, stream);
-    default: return launch_mx_tiles<MxCfg<256, 256, 2, 4, 2, 128>>(a, stream);
+    case 3: return launch_mx_tiles<MxCfg<64, 64, 2, 2, 4>>(a, stream);
+    case 4: return launch_mx_tiles<MxCfg<64, 128, 1, 4, 3>>(a, stream);
+    case 5: return launch_mx_tiles<MxCfg<128, 128, 2, 2, 2>>(a, stream);
+    default: return launch_mx_tiles<MxCfg<256, 256, 2, 4, 2>>(a, stream);
   }
 }
 
 // The quantisation costs every workgroup a pass over all rows, 16384 elements at a time:
 // one launch takes 4.6 us against 6.4 in two for 1x7168x2048, 5.3 against
 // 6.6 for 8x7168x2048, and as long for 4x18432x7168.
-bool linear_mx_fused(int64_t M, int64_t, int64_t K) {
+bool linear_mx_fused(int64_t M, int64_t N, int64_t K) {
   const int64_t nkb = (K + 255) / 256;
-  return M <= 16 && M * nkb * 256 <= 24576 && M * (mx_code_ld((int)nkb) + mx_scale_ld((int)nkb)) <= kFusedBytes;
+  return M <= 16 && N <= 16 * (int64_t)kMaxSplitTiles && M * nkb * 256 <= 24576 && M * (mx_code_ld((int)nkb) + mx_scale_ld((int)nkb)) <= kFusedBytes;
 }
 
 // 16 columns a workgroup where those are one round over the CUs (1x1536x7168 5.0 us,

@@ -730,7 +730,7 @@ dsfp8_status dsfp8_grouped_gemm_mxfp4(const void* A, int64_t a_rows, int64_t lda
  *   indices  int32 [T, k], row stride ldi                 (device, written)
  *   weights  bf16 [T, k], row stride ldw                  (device, written)
  * Limits: 1 <= k <= 16, 1 <= E <= 4096, 1 <= groups <= 64 and a divisor of E,
- * 1 <= top_groups <= groups, k <= top_groups * (E / groups), T < 2^31.
+ * 1 <= top_groups <= groups, k <= top_groups * (E / groups), T < 2^26.
  * Errors: DTYPE, SHAPE (the limits), NULL, LD, ALIGN, SCORE (unknown score),
  * LAUNCH.
  */
