@@ -58,6 +58,7 @@ SIGNATURES = {
     "dsfp8_linear_mxfp4_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "dsfp8_grouped_gemm_mxfp4": (_i, [_p, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64,
                                       _p, _i64, _p]),
+    "dsfp8_mxfp4_variant": (_i, [_i64, _i64, _i64, _i64, _p]),
     "dsfp8_moe_gate": (_i, [_p, _i, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i, _i, _f, _p, _i64, _p, _i64, _p]),
     "dsfp8_add_rms_norm": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i, _f, _f, _i64, _i64, _p, _i64, _p, _i64, _i,
                                 _p, _i64, _i64, _p]),

@@ -892,6 +892,21 @@ dsfp8_status dsfp8_grouped_gemm_mxfp4(const void* A, int64_t a_rows, int64_t lda
   return launched(dsfp8::launch_mx_gemm(a, stream));
 }
 
+dsfp8_status dsfp8_mxfp4_variant(int64_t E, int64_t M, int64_t N, int64_t K, int32_t* variant) {
+  if (variant == nullptr) return DSFP8_ERR_NULL;
+  if (E < 0 || E > kMaxExperts || !dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
+  dsfp8::MxGemmArgs a{};
+  a.M = M;
+  a.N = N;
+  a.KB = mx_blocks(K);
+  a.E = E;
+  a.offsets = E > 0 ? variant : nullptr;  // only whether there are any matters here
+  const dsfp8::MxTileSize t = M > 0 && N > 0 ? dsfp8::mx_gemm_tile(a) : dsfp8::MxTileSize{0, 0};
+  variant[0] = t.rows;
+  variant[1] = t.columns;
+  return DSFP8_OK;
+}
+
 // ---- gate -------------------------------------------------------------------------------
 
 dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const float* bias, int64_t T, int64_t E,

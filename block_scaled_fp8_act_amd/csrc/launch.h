@@ -262,6 +262,10 @@ struct NormArgs {
 
 hipError_t launch_mx_quant(const MxQuantArgs& a, hipStream_t stream);
 hipError_t launch_mx_dequant(const MxDequantArgs& a, hipStream_t stream);
+struct MxTileSize {
+  int rows, columns;
+};
+MxTileSize mx_gemm_tile(const MxGemmArgs& a);  // of the variant that serves a product
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 // Quantisation and product in one launch, where linear_mx_fused says so; the
 // product's A and a_s are then not used.

@@ -913,6 +913,11 @@ static hipError_t launch_mx_split(const MxGemmArgs& a, const MxQuantArgs& x, hip
   return hipGetLastError();
 }
 
+MxTileSize mx_gemm_tile(const MxGemmArgs& a) {
+  const MxVariant& v = kMxVariants[mx_choose(a)];
+  return {v.rows, v.columns};
+}
+
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const MxQuantArgs none{};

@@ -705,6 +705,17 @@ dsfp8_status dsfp8_grouped_gemm_mxfp4(const void* A, int64_t a_rows, int64_t lda
                                       void* C, int64_t ldc, hipStream_t stream);
 
 /*
+ * Rows and columns of a workgroup's output tile in the variant that serves an
+ * MXFP4 product, for tests and profiles (a host call; nothing is launched).  E:
+ * experts of a grouped product, 0 for dsfp8_gemm_mxfp4 (and dsfp8_linear_mxfp4
+ * where it needs a workspace).  Tiles of 16 and 32 rows split K over the waves of a
+ * workgroup.  0, 0 where there is nothing to do.  The choice follows the current
+ * device's number of CUs.
+ * Errors: NULL, SHAPE.
+ */
+dsfp8_status dsfp8_mxfp4_variant(int64_t E, int64_t M, int64_t N, int64_t K, int32_t* variant);
+
+/*
  * The gate of a routed-expert layer ([AG] 6.4, Gate): which k of E experts a token
  * goes to, and with what weights, from the router's logits.
  *   score[t,e] = sigmoid(logits[t,e])  or  softmax(logits[t])[e], evaluated

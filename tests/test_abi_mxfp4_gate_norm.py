@@ -94,11 +94,24 @@ def test_grouped(lib):
     assert c(M=0) == OK and c(N=0) == OK
 
 
+def test_variant(lib):
+    import ctypes
+    v = (ctypes.c_int32 * 2)()
+    c = caller(lib.dsfp8_mxfp4_variant, E=0, M=4, N=8, K=64, v=ctypes.addressof(v))
+    assert c(v=None) == NULL and c(E=-1) == SHAPE and c(E=65537) == SHAPE
+    assert c(M=-1) == SHAPE and c(N=-1) == SHAPE and c(K=-1) == SHAPE
+    assert c() == OK and tuple(v) == (16, 16)
+    assert c(M=0) == OK and tuple(v) == (0, 0)
+    # more tiles of 16 rows than one launch holds threads for
+    assert c(M=1, N=(1 << 31) - 1, K=32) == OK and v[0] > 32
+    assert lib.dsfp8_linear_mxfp4_workspace_bytes(1, (1 << 31) - 1, 32) > 0
+
+
 def test_gate(lib):
     c = caller(lib.dsfp8_moe_gate, logits=P, dtype=0, ldl=64, bias=None, T=4, E=64, k=8, groups=8, top=4, score=0, renorm=1,
                scale=1.0, indices=P, ldi=8, weights=P, ldw=8, stream=None)
     assert c(dtype=2) == DTYPE and c(score=2) == SCORE
-    assert c(T=-1) == SHAPE and c(E=0) == SHAPE and c(E=4097, ldl=4097, groups=1, top=1) == SHAPE
+    assert c(T=-1) == SHAPE and c(T=1 << 26) == SHAPE and c(E=0) == SHAPE and c(E=4097, ldl=4097, groups=1, top=1) == SHAPE
     assert c(k=0) == SHAPE and c(k=17, ldi=17, ldw=17) == SHAPE and c(groups=0) == SHAPE and c(groups=7) == SHAPE
     assert c(E=128, ldl=128, groups=128) == SHAPE and c(top=0) == SHAPE and c(top=9) == SHAPE
     assert c(top=1, k=9, ldi=9, ldw=9) == SHAPE             # 8 experts in the groups kept

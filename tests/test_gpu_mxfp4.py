@@ -4,11 +4,14 @@ Codes and scale bytes are compared bit for bit.  A product's bf16 output is with
 bf16, 2^-8 of the value, and of the bound that oracle/mxfp4.py states for an fp32 sum.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import block_scaled_fp8_act_amd as ds
+from block_scaled_fp8_act_amd import _lib
 from block_scaled_fp8_act_amd import inputs as I
 from oracle import int8 as Q8
 from oracle import mxfp4 as MX
@@ -154,6 +157,20 @@ def test_quant_strides_and_untouched_padding():
     assert torch.equal(out[:, 1:301], ds.mxfp4_dequant(q2, s2, 300)) and (out[:, 301:] == 5).all() and (out[:, 0] == 5).all()
 
 
+def test_quant_of_more_rows_than_one_launch_takes():
+    """2^28 + 5 rows of one block: two launches; the rows on both sides of the cut, and the last."""
+    M = 2 ** 28 + 5
+    x = torch.zeros((M, 1), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 7, 2 ** 28 - 1, 2 ** 28, M - 1], device="cuda")
+    x[at, 0] = torch.tensor([1.0, -3.0, 0.5, 6.0, -40.0], dtype=torch.bfloat16, device="cuda")
+    q, s = ds.mxfp4_quant(x)
+    qr, sr = MX.quant(x[at].double().cpu().numpy())
+    assert np.array_equal(host_u8(q[at]), qr) and np.array_equal(host_u8(s[at]), sr)
+    assert int((q.view(M, 16)[:, 0] != 0).sum()) == 5
+    del q, s
+    torch.cuda.empty_cache()
+
+
 # ---- products ---------------------------------------------------------------------------------
 
 # one row or column, sizes around a block, around 256 columns of K (a K-block), 512 (two: one load of
@@ -182,6 +199,51 @@ def test_gemm_many_tiles(M, N, K):
     c = ds.gemm_mxfp4(*mx_dev(a, a_s), *mx_dev(b, b_s))
     pick = np.unique(np.concatenate([np.arange(0, M, 37), [M - 1, 255, 256]]))
     check_product(c[torch.from_numpy(pick).cuda()], a[pick], a_s[pick], b, b_s)
+
+
+def tile(E, M, N, K):
+    v = (ctypes.c_int32 * 2)()
+    assert _lib.load().dsfp8_mxfp4_variant(E, M, N, K, ctypes.addressof(v)) == 0
+    return tuple(v)
+
+
+# tile, M, N, K: ragged edges, more tiles than workgroups for the larger ones, K of one K-block of 256 columns, of odd
+# and even numbers of them, and ends inside one
+VARIANTS = [((16, 16), 9, 300, 1000), ((16, 32), 9, 9000, 1000), ((16, 32), 40, 3000, 1000), ((32, 32), 64, 7200, 700),
+            ((32, 32), 20, 9001, 1000), ((64, 64), 150, 9000, 700), ((64, 64), 300, 2100, 288), ((64, 64), 500, 3001, 1056),
+            ((64, 128), 800, 2700, 1120), ((128, 128), 2048, 7168, 288), ((128, 128), 900, 5003, 1312),
+            ((256, 256), 4000, 16300, 200), ((256, 256), 4000, 16300, 288), ((256, 256), 4090, 16201, 544),
+            ((256, 256), 3000, 12000, 800), ((256, 256), 700, 20000, 1300)]
+
+
+@pytest.mark.parametrize("want,M,N,K", VARIANTS)
+def test_every_variant(want, M, N, K):
+    assert tile(0, M, N, K) == want
+    a, a_s = rows_of(M, K, 4000)
+    b, b_s = rows_of(N, K, 4001)
+    c = ds.gemm_mxfp4(*mx_dev(a, a_s), *mx_dev(b, b_s))
+    pick = np.unique(np.concatenate([np.arange(0, M, max(1, M // 60)), [M - 1, M // 2]]))
+    check_product(c[torch.from_numpy(pick).cuda()], a[pick], a_s[pick], b, b_s, f"{M}x{N}x{K}")
+
+
+GROUPED = [((16, 32), [20, 0, 3, 60, 7], 1000, 1056), ((32, 32), [9, 14, 0, 33, 40, 1, 2, 29], 2100, 2336),
+           ((64, 128), [0, 100, 64, 3, 90, 1, 0, 42], 8200, 544), ((128, 128), [130, 0, 1800, 70], 2100, 288),
+           ((256, 256), [4000, 300, 4700], 8100, 288), ((256, 256), [257, 8743], 4101, 544),
+           ((256, 256), [4000, 0, 256, 744], 8200, 1056)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("want,counts,N,K", GROUPED)
+def test_every_grouped_variant(want, counts, N, K, gather):
+    assert tile(len(counts), sum(counts), N, K) == want
+    a, a_s, w, off, rows = grouped(counts, N, K, 600, 500 if gather else None)
+    c = ds.grouped_gemm_mxfp4(*grouped_dev(a, a_s, w), torch.from_numpy(off).cuda(),
+                              rows=None if rows is None else torch.from_numpy(rows).cuda())
+    for e, (b, b_s) in enumerate(w):
+        if counts[e]:
+            r = np.unique(np.concatenate([np.arange(off[e], off[e + 1], max(1, counts[e] // 25)), [off[e + 1] - 1]]))
+            src = r if rows is None else rows[r]
+            check_product(c[torch.from_numpy(r).cuda()], a[src], a_s[src], b, b_s, f"expert {e}")
 
 
 def test_gemm_small_whole_numbers_are_exact():

@@ -171,6 +171,21 @@ def test_no_rows():
     assert ds.add_rms_norm(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), w).shape == (0, 64)
 
 
+@pytest.mark.parametrize("quant", [None, "e4m3", "mxfp4"])
+def test_more_rows_than_one_launch_takes(quant):
+    """2^21 + 9 rows go in two launches; the rows around the cut as in a call of their own."""
+    T, D = 2 ** 21 + 9, 16
+    x = torch.randn((T, D), device="cuda").bfloat16()
+    r = torch.randn((T, D), device="cuda").bfloat16()
+    g = torch.rand((T, D), device="cuda").bfloat16()
+    w = torch.randn(D, device="cuda")
+    for gate in (g, g[0]):
+        whole = ds.add_rms_norm(x, w, residual=r, gate=gate, scale=0.5, quant=quant)
+        cut = slice(2 ** 21 - 5, T)
+        part = ds.add_rms_norm(x[cut], w, residual=r[cut], gate=gate if gate.dim() == 1 else gate[cut], scale=0.5, quant=quant)
+        assert all(torch.equal(a[cut], b) for a, b in zip(whole, part))
+
+
 def test_graph():
     T, D = 40, 2304
     op, w, pw = operands(T, D, 8)
