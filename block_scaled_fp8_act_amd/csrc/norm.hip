@@ -139,32 +139,48 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a)
     const int k = (t + c * TPR) * 8;
     float w[8];
     load_weight(a.w, a.w_f32, k, D, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * r * w[i];
     if (a.fmt == DSFP8_NORM_BF16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * r * w[i];
       store_bf16x8(static_cast<uint16_t*>(a.y) + m * a.ldy, k, D, v[c]);
       continue;
     }
     if (a.fmt == DSFP8_NORM_MXFP4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * r * w[i];
       const uint32_t s = mx_scale(mx_quad_top(v[c]));
       if (k < (D + 31) / 32 * 32) {
         reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + m * a.ldy)[k >> 3] = mx_codes8(v[c], mx_scale_f32(s));
         if ((k & 31) == 0) static_cast<uint8_t*>(a.s)[m * a.s_rs + (k >> 5)] = (uint8_t)s;
       }
     } else {
-      // over bit patterns, in which NaN > infinity > every finite value, so
-      // that a block that holds one gets a scale that shows it
-      uint32_t top = 0;
+      // From h on in 64 bits: h w is exact, 1 / rms is a factor of the scale and
+      // cancels in the code, and what is left is rounded to fp32 on its way to e4m3,
+      // which puts a value halfway between two codes exactly there again.  So a code is
+      // that of the exact y wherever h is exact (in 32 bits 5 in 10^6 codes, all halfway
+      // cases, go by chance; 8192x7168 101 us against 104).  The maximum is over
+      // bit patterns, in which NaN > infinity > every finite value, so that a block
+      // that holds one gets a scale that shows it.
+      double hw[8];
+      uint64_t top = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(v[c][i]) & 0x7fffffffu;
+        hw[i] = (double)v[c][i] * (double)w[i];
+        const uint64_t b = (uint64_t)__double_as_longlong(hw[i]) & 0x7fffffffffffffffull;
         top = b > top ? b : top;
       }
-      const float amax = __uint_as_float(max_row16_u32(top));
-      const float s = amax == amax ? block_scale(amax, a.fmt == DSFP8_NORM_E4M3_UE8M0) : amax;
+      const uint32_t hi32 = max_row16_u32((uint32_t)(top >> 32));
+      const uint32_t lo32 = max_row16_u32((uint32_t)(top >> 32) == hi32 ? (uint32_t)top : 0u);
+      const double amax = __longlong_as_double((long long)((uint64_t)hi32 << 32 | lo32)) * (double)r;
+      double scale = amax;
+      if (amax == amax)
+        scale = a.fmt == DSFP8_NORM_E4M3_UE8M0 ? (double)block_scale((float)amax, true)
+                                               : fmax(amax, (double)kScaleFloor) * (1.0 / (double)kE4m3Max);
+      const float s = (float)scale;
+      const double inv = (double)r / scale;
       float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = v[c][i] / s;
+      for (int i = 0; i < 8; ++i) q[i] = (float)(hw[i] * inv);
       const uint32_t lo = pack_e4m3x4(q[0], q[1], q[2], q[3]), hi = pack_e4m3x4(q[4], q[5], q[6], q[7]);
       uint8_t* dst = static_cast<uint8_t*>(a.y) + m * a.ldy + k;
       if (k + 8 <= D) {

@@ -770,8 +770,9 @@ dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const fl
  *                without a residual                        (device, written)
  *   y, s         y_fmt BF16: y bf16 [T, D], row stride ldy; s is not used
  *                E4M3, E4M3_UE8M0: y e4m3 [T, D], s fp32 [T, KB(D)] with strides
- *                s_row_stride, s_kb_stride: dsfp8_act_quant of the fp32 y
- *                (with IEEE divisions)
+ *                s_row_stride, s_kb_stride: the codes and scales that
+ *                dsfp8_act_quant defines, of y = h / rms(h) * weight held in 64
+ *                bits, a code dividing by its scale before that is rounded to fp32
  *                MXFP4: y codes [T, 16 KM(D)], s scales [T, KM(D)] with row
  *                stride s_row_stride: dsfp8_mxfp4_quant of the fp32 y
  *                                                          (device, written)
