@@ -1,8 +1,8 @@
 """RMS norms around a residual connection in fp64, with bounds on an fp32 evaluation.
 
-``u`` is half a step of fp32 (2^-24).  A row's sum of squares is added up in at most 64 + 6 + 16
-steps one after the other (a thread's columns, a wave, a workgroup), each squared term rounded once:
-90 u; its root halves that; the division by D, the addition of eps, the root and the reciprocal add
+``u`` is half a step of fp32 (2^-24).  A row's sum of squares is added up in fewer than 86 steps one
+after the other (8 columns, a wave, the waves' sums), each squared term rounded once: 90 u at most;
+its root halves that; the division by D, the addition of eps, the root and the reciprocal add
 4 u: 1 / rms errs by at most 50 u, relative.
 """
 

@@ -186,6 +186,17 @@ def test_more_rows_than_one_launch_takes(quant):
         assert all(torch.equal(a[cut], b) for a, b in zip(whole, part))
 
 
+@pytest.mark.parametrize("D", [520, 4000, 7168, 16000, 33000])
+@pytest.mark.parametrize("quant", [None, "e4m3", "mxfp4"])
+def test_a_row_does_not_depend_on_the_number_of_rows(D, quant):
+    op, w, pw = operands(4, D, 9)
+    op = {n: v if v is None else np.tile(v, (400, 1)) for n, v in op.items()}
+    whole = run(op, w, pw, scale=0.5, quant=quant)
+    few = run({n: v if v is None else v[:4] for n, v in op.items()}, w, pw, scale=0.5, quant=quant)
+    for a, b in zip(whole, few):
+        assert torch.equal(a[:4], b) and torch.equal(a[-4:], b)
+
+
 def test_graph():
     T, D = 40, 2304
     op, w, pw = operands(T, D, 8)
