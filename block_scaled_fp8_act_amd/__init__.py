@@ -936,8 +936,8 @@ def add_rms_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.
         y = x.new_empty((T, D), dtype=torch.uint8) if o[0] is None else _out(o[0], (T, D), torch.uint8, x.device, "y")
         ldy = _row(y, D)
         if o[1] is None:        # K-block-major, as new_scales
-            srs, sks = 1, T
-            s = x.new_empty_strided((T, kblocks(D)), (1, T), dtype=torch.float32)
+            srs, sks = 1, max(T, 1)
+            s = x.new_empty_strided((T, kblocks(D)), (1, sks), dtype=torch.float32)
         else:
             s = _scales_out(o[1], T, kblocks(D), x.device)
             srs, sks = _scale_strides(s)

@@ -171,6 +171,17 @@ def test_no_rows():
     assert ds.add_rms_norm(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), w).shape == (0, 64)
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("quant,shapes", [(None, [(0, 300)]), ("e4m3", [(0, 300), (0, 3)]), ("e4m3_ue8m0", [(0, 300), (0, 3)]),
+                                          ("mxfp4", [(0, 160), (0, 10)])])
+def test_no_rows_of_any_output(quant, shapes, residual):
+    w = torch.ones(300, dtype=torch.bfloat16, device="cuda")
+    x = torch.empty((0, 300), dtype=torch.bfloat16, device="cuda")
+    got = ds.add_rms_norm(x, w, residual=x if residual else None, quant=quant)
+    got = got if isinstance(got, tuple) else (got,)
+    assert [tuple(t.shape) for t in got] == shapes + ([(0, 300)] if residual else [])
+
+
 @pytest.mark.parametrize("quant", [None, "e4m3", "mxfp4"])
 def test_more_rows_than_one_launch_takes(quant):
     """2^21 + 9 rows go in two launches; the rows around the cut as in a call of their own."""
