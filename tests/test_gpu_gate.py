@@ -48,6 +48,20 @@ def test_choice(T, E, k, groups, top, bias, score):
     check(x, k, b, dtype=torch.bfloat16, score=score, groups=groups, top_groups=top, renormalize=False, scale=1.0)
 
 
+# groups that begin inside a lane's experts: larger than a lane holds, and smaller, for a wave and a quarter
+# of one per token and every number of experts a lane takes
+UNEVEN = [(300, 250, 6, 5, 2), (9000, 250, 6, 5, 2), (40, 130, 4, 13, 3), (8200, 60, 4, 20, 5), (8200, 126, 5, 7, 2),
+          (8195, 90, 3, 30, 9), (70, 500, 8, 20, 7), (30, 420, 8, 60, 11), (50, 1000, 8, 40, 7), (20, 3900, 8, 60, 5),
+          (12, 2016, 16, 63, 6), (9, 4090, 8, 5, 3)]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T,E,k,groups,top", UNEVEN)
+def test_groups_that_begin_inside_a_lane(T, E, k, groups, top, bias, score):
+    test_choice(T, E, k, groups, top, bias, score)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("E,groups", [(6, 1), (64, 8), (130, 13), (256, 4)])
 def test_ties_and_saturation(E, groups, score):
