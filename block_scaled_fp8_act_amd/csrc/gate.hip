@@ -41,10 +41,18 @@ __device__ __forceinline__ uint32_t max_token(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Unsigned integer in the order of the fp32 value (-0 and +0 alike); 0 for -inf.
-__device__ __forceinline__ uint32_t order_u32(float key) {
-  const uint32_t b = __float_as_uint(key + 0.0f);
-  return key == kNone ? 0u : ((b >> 31) ? ~b : b | 0x80000000u);
+// Unsigned integer, never 0, in the order of the fp32 value (-0 and +0 alike).
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b >> 31) ? ~b : b | 0x80000000u;
+}
+// The same of a key; 0 for -inf.
+__device__ __forceinline__ uint32_t order_u32(float key) { return key == kNone ? 0u : order_of(key); }
+
+// A group's score from its two best keys, in order; 0 for a group without an
+// expert, which comes after one whose two keys add up to -inf.
+__device__ __forceinline__ uint32_t order_group(float t1, float t2, bool sum) {
+  return t1 == kNone ? 0u : order_of(sum && t2 != kNone ? t1 + t2 : t1);
 }
 
 // 1 / v for finite v >= 1 in 64 bits, within a few units in the last place: the
@@ -81,7 +89,7 @@ template <int VPT, int LPT, bool SOFTMAX>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastDiv per_group) {
   constexpr int TPW = 64 / LPT;  // tokens of a wave
   __shared__ float keys[kGateWaves][TPW][LPT * VPT];
-  __shared__ float group_score[kGateWaves][TPW][kMaxGateGroups];
+  __shared__ uint32_t group_score[kGateWaves][TPW][kMaxGateGroups];
   __shared__ float4 best2[kGateWaves][TPW][LPT];
   __shared__ int2 slots[kGateWaves][TPW][kMaxGateK];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -174,7 +182,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
     // A group's score, then its rank: a group stays if fewer than top_groups
     // come before it.
     const int gs = (int)per_group.d, gl = gs / VPT;
-    float* gsc = group_score[wave][sub];
+    uint32_t* gsc = group_score[wave][sub];
     const bool lanes = gs % VPT == 0;  // gl lanes hold a group
     // else, where gs > VPT, a lane's experts belong to group g0 and, from `border` on, the next
     // (16384x250 in 5 groups 18.3 us; one lane per group over all of its experts 39.5)
@@ -185,7 +193,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
 #pragma unroll
       for (int j = 0; j < VPT; ++j) merge2(t1, t2, key[j], kNone);
       for (int d = 1; d < gl; d <<= 1) merge2(t1, t2, __shfl_xor(t1, d), __shfl_xor(t2, d));
-      if (lane % gl == 0 && e0 < a.E) gsc[lane / gl] = a.bias && t2 != kNone ? t1 + t2 : t1;
+      if (lane % gl == 0 && e0 < a.E) gsc[lane / gl] = order_group(t1, t2, a.bias != nullptr);
     } else if (lanes) {
       float t1 = kNone, t2 = kNone;
 #pragma unroll
@@ -198,7 +206,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
           const float4 o = best2[wave][sub][g * gl + i];
           merge2(t1, t2, o.x, o.y);
         }
-        gsc[g] = a.bias && t2 != kNone ? t1 + t2 : t1;
+        gsc[g] = order_group(t1, t2, a.bias != nullptr);
       }
     } else if (two) {
       float4 o = make_float4(kNone, kNone, kNone, kNone);
@@ -218,7 +226,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
           o = best2[wave][sub][i];
           merge2(t1, t2, o.x, o.y);
         }
-        gsc[g] = a.bias && t2 != kNone ? t1 + t2 : t1;
+        gsc[g] = order_group(t1, t2, a.bias != nullptr);
       }
     } else {
       // fewer experts in a group than a lane holds: their keys through LDS
@@ -228,17 +236,17 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
       for (int g = lane; g < a.groups; g += LPT) {
         float t1 = kNone, t2 = kNone;
         for (int i = 0; i < gs; ++i) merge2(t1, t2, keys[wave][sub][g * gs + i], kNone);
-        gsc[g] = a.bias && t2 != kNone ? t1 + t2 : t1;
+        gsc[g] = order_group(t1, t2, a.bias != nullptr);
       }
     }
     __builtin_amdgcn_wave_barrier();
     uint64_t keep = 0;
     for (int base = 0; base < a.groups; base += LPT) {
       const int mine = base + lane;
-      const float v = mine < a.groups ? gsc[mine] : kNone;
+      const uint32_t v = mine < a.groups ? gsc[mine] : 0u;
       int ahead = 0;
       for (int g = 0; g < a.groups; ++g) {
-        const float o = gsc[g];
+        const uint32_t o = gsc[g];
         ahead += o > v || (o == v && g < mine);
       }
       const uint64_t stay = __ballot(mine < a.groups && ahead < a.top_groups) >> (LPT * sub);

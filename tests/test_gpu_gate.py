@@ -98,6 +98,24 @@ def test_missing_experts(bias, score):
         assert torch.equal(rows < 0, idx < 0) and int(off[-1]) == int((idx >= 0).sum())
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,groups,top", [(40, 24, 6, 4), (40, 250, 5, 3), (8200, 60, 4, 3), (8193, 126, 7, 4), (30, 130, 13, 9)])
+def test_groups_masked_by_the_lowest_value(T, E, groups, top, score):
+    """Biases of the type's lowest value: a group's two best keys add up to -inf, and the group still comes before
+    those whose experts are all missing; tokens without whole groups."""
+    g = I.rng(CID, 9)
+    size = E // groups
+    x = g.standard_normal((T, E)).astype(np.float32)
+    b = (0.1 * g.standard_normal(E)).astype(np.float32)
+    b[(groups - 1) * size:] = np.finfo(np.float32).min
+    for t in range(T):
+        gone = g.permutation(groups - 1)[:int(g.integers(0, groups))]
+        for q in gone:
+            x[t, q * size:(q + 1) * size] = -np.inf
+    x[1, g.random(E) < 0.7] = -np.inf
+    check(x, 4, b, score=score, groups=groups, top_groups=top)
+
+
 def test_nan_shows_and_stays_in_its_row():
     g = I.rng(CID, 8)
     x = g.standard_normal((9, 40)).astype(np.float32)
