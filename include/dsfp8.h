@@ -734,7 +734,7 @@ dsfp8_status dsfp8_mxfp4_variant(int64_t E, int64_t M, int64_t N, int64_t K, int
  * in fp32.  Where fewer than k experts are available the last slots get index
  * -1, which the routed-expert calls take as no expert, and weight 0: a token
  * whose logits are all -infinity (padding) goes to none.  A token whose scores
- * or keys contain a NaN gets NaN weights and k distinct available experts.
+ * or keys contain a NaN gets NaN weights and distinct available experts.
  *
  *   logits   fp32 or bf16 (dtype) [T, E], row stride ldl  (device, read)
  *   bias     fp32 [E], or NULL                            (device, read)
@@ -777,7 +777,8 @@ dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const fl
  *                stride s_row_stride: dsfp8_mxfp4_quant of the fp32 y
  *                                                          (device, written)
  * A row with a NaN shows it in its outputs (a quantised y in its scales) and
- * changes no other row.  h may be residual or x, and a bf16 y may be x, with the
+ * changes no other row; a row of finite values whose squares add up past fp32's
+ * range gives zeros.  The bytes of a row do not depend on T.  h may be residual or x, and a bf16 y may be x, with the
  * same stride; otherwise outputs must not overlap inputs.  Without a residual,
  * post_weight and gate must be NULL and scale 1.
  * Limits: D <= 65536, eps >= 0.

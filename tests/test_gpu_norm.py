@@ -119,6 +119,18 @@ def test_rows_of_zeros_and_tiny_values():
     assert np.all(s[0].cpu().numpy() == np.float32(1e-4) / np.float32(448)) and not q[0].any()
 
 
+def test_squares_past_the_range_give_zeros():
+    w = torch.ones(700, dtype=torch.bfloat16, device="cuda")
+    x = torch.ones((3, 700), dtype=torch.bfloat16, device="cuda")
+    x[1] = 1e25
+    y = ds.add_rms_norm(x, w)
+    assert not y[1].any() and (y[0] == 1).all() and (y[2] == 1).all()
+    q, s = ds.add_rms_norm(x, w, quant="e4m3")
+    assert not q[1].any() and torch.isfinite(s).all()
+    q, s = ds.add_rms_norm(x, w, quant="mxfp4")
+    assert not ds.mxfp4_dequant(q, s, 700)[1].any()
+
+
 @pytest.mark.parametrize("bad", [0x7fc0, 0x7f80])
 def test_nan_and_infinity_stay_in_their_row(bad):
     op, w, pw = operands(5, 700, 6)
