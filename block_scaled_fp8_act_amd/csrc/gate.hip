@@ -2,12 +2,17 @@
 //
 // LPT lanes per token, the whole wavefront or a quarter of it; each holds VPT
 // consecutive experts, so that among equal keys the lowest lane, and in it the first,
-// is the lowest expert.  The scores are evaluated in 64 bits and rounded once, so
-// that the choice does not depend on how an exponential is computed: an expert's
-// key is the same fp32 value wherever it is evaluated.  Keys are compared as unsigned
+// is the lowest expert.  The scores are evaluated in 64 bits (within 2^-45) and rounded
+// once, so that the choice does not depend on how an exponential is computed: two
+// evaluations give the same fp32 key but for one in 10^6 that lie next to a
+// halfway case.  Keys are compared as unsigned
 // integers of the same order, 0 for an expert that is not available.  Each of the k
 // rounds takes the maximum over the token's lanes (DPP steps) and its first
 // holder, which puts itself into the round's slot in LDS.
+//
+// 16384x256 in 8 groups: 18.4 us, 1.0 TB/s; instructions bound it (scores, groups
+// and rounds in about equal parts), not its 17.6 MB.  One token: 4.3 us, a chain of
+// dependent steps.
 #include "device.h"
 #include "launch.h"
 
@@ -65,7 +70,7 @@ __device__ __forceinline__ double reciprocal(double v) {
 
 // e^x for |x| <= 800 within 2^-46: x = n ln 2 + r with |r| <= ln 2 / 2, and the series of
 // e^r up to r^11.  No branch, so that the chains of a lane's experts overlap (16384x256
-// in groups 19.7 us with the library's exponential, which has branches, and 17.8 with this).
+// in groups 19.7 us with the library's exponential, which has branches, 17.8 with this).
 __device__ __forceinline__ double exp64(double x) {
   const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
   double r = __builtin_fma(n, -0x1.62e42fefa38p-1, x);     // ln 2 to 42 bits, n times it is exact
@@ -328,8 +333,8 @@ hipError_t launch_gate_of(const GateArgs& a, hipStream_t stream) {
 hipError_t launch_gate(const GateArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   // A quarter of a wave per token issues less for a token but takes longer for it:
-  // 16384x256 in groups 18.0 us against 20.9, 16384x64 5.9 against 9.5, 4096x128 4.7
-  // against 4.4.
+  // 16384x256 in groups 18.4 us against 20.0, 8192x256 10.0 against 11.0, 16384x64 5.4
+  // against 7.8, but 4096x128 4.0 against 3.9.
   if (a.T >= 8192 && a.E <= 256) {
     if (a.E <= 64) return launch_gate_of<4, 16>(a, stream);
     if (a.E <= 128) return launch_gate_of<8, 16>(a, stream);
