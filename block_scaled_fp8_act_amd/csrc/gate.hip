@@ -10,9 +10,9 @@
 // rounds takes the maximum over the token's lanes (DPP steps) and its first
 // holder, which puts itself into the round's slot in LDS.
 //
-// 16384x256 in 8 groups: 18.4 us, 1.0 TB/s; instructions bound it (scores, groups
-// and rounds in about equal parts), not its 17.6 MB.  One token: 4.3 us, a chain of
-// dependent steps.
+// 16384x256 in 8 groups: 18.4 us (softmax without groups 16.1), 1.0 TB/s; the
+// instructions of the scores and of the k rounds bound it, not its 17.6 MB.  One
+// token: 4.3 us, a chain of dependent steps.
 #include "device.h"
 #include "launch.h"
 
