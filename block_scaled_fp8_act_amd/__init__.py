@@ -699,13 +699,17 @@ def _mx_ld(t, what):
 
 
 def _mx_out(out, M, K, t):
-    """Codes and scales for M rows of K columns, the caller's or new ones on t's device, with their row strides."""
+    """Codes and scales for M rows of K columns, each the caller's or new on t's device, with their row strides."""
     kb = (K + 31) >> 5
-    if out is None:
+    q, s = (None, None) if out is None else out
+    if s is None:
         pad = (kb + 15) & ~15
         s = t.new_empty((M, pad), dtype=torch.uint8)
-        return t.new_empty((M, 16 * kb), dtype=torch.uint8), 16 * kb, s if pad == kb else s.as_strided((M, kb), (pad, 1)), pad
-    q, s = out
+        s = s if pad == kb else s.as_strided((M, kb), (pad, 1))
+        if q is None:
+            return t.new_empty((M, 16 * kb), dtype=torch.uint8), 16 * kb, s, pad
+    if q is None:
+        q = t.new_empty((M, 16 * kb), dtype=torch.uint8)
     _mat(q, "y", (torch.uint8,))
     _mat(s, "s", (torch.uint8,))
     if q.shape != (M, 16 * kb) or s.shape != (M, kb) or q.device != t.device or s.device != t.device:
@@ -720,7 +724,7 @@ def mxfp4_quant(x, out=None):
     Returns ``(q uint8 [M, 16 * ceil(K/32)], s uint8 [M, ceil(K/32)])``: two e2m1
     codes a byte, the lower column in the low half (columns past K hold 0), and a
     scale byte per block, for x ~= code * 2^(s - 127).  ``out`` may supply ``(q,
-    s)`` as :func:`mxfp4_empty` gives them."""
+    s)`` as :func:`mxfp4_empty` gives them (None for one that is to be new)."""
     if not _is_mat(x, torch.bfloat16):
         _mat(x, "x", (torch.float32, torch.bfloat16))
     M, K = x.shape
@@ -888,7 +892,8 @@ def add_rms_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.
     ``x``, ``residual`` bf16 ``[T, D]``; ``gate`` bf16 ``[T, D]`` or ``[D]``; the weights ``[D]``, both bf16 or both
     fp32.  ``quant``: None for a bf16 y, "e4m3" or "e4m3_ue8m0" for :func:`act_quant`'s codes and scales of y, "mxfp4"
     for :func:`mxfp4_quant`'s.  Returns ``y`` or ``(y, s)``, followed by the new residual stream h (bf16) if there is
-    a ``residual``.  ``out`` may supply the same tuple (``(y,)`` for y alone); its h may be ``residual`` itself."""
+    a ``residual``.  ``out`` may supply the same tuple (``(y,)`` for y alone; None for one that is to be new); its h may
+    be ``residual`` itself."""
     _need(x, "x", torch.bfloat16)
     T, D = x.shape
     dev = x.get_device()
@@ -930,7 +935,7 @@ def add_rms_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.
         y = x.new_empty((T, D)) if o[0] is None else _out(o[0], (T, D), torch.bfloat16, x.device, "y")
         ldy = _row(y, D)
     elif quant == "mxfp4":
-        y, ldy, s, srs = _mx_out(None if o[0] is None else o[:2], T, D, x)
+        y, ldy, s, srs = _mx_out(o[:2], T, D, x)
         sp, sks = s.data_ptr(), 1
     else:
         y = x.new_empty((T, D), dtype=torch.uint8) if o[0] is None else _out(o[0], (T, D), torch.uint8, x.device, "y")

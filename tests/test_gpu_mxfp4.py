@@ -157,6 +157,18 @@ def test_quant_strides_and_untouched_padding():
     assert torch.equal(out[:, 1:301], ds.mxfp4_dequant(q2, s2, 300)) and (out[:, 301:] == 5).all() and (out[:, 0] == 5).all()
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_quant_into_one_given_output(gated):
+    x = dev_bf16(I.activations((9, 300), CID, 8))
+    call = (lambda **kw: ds.silu_mul_mxfp4_quant(x, x, **kw)) if gated else (lambda **kw: ds.mxfp4_quant(x, **kw))
+    ref = call()
+    q, s = (t.fill_(9) for t in ds.mxfp4_empty(9, 300, "cuda"))
+    got = call(out=(None, s))
+    assert got[1].data_ptr() == s.data_ptr() and torch.equal(s, ref[1]) and torch.equal(got[0], ref[0])
+    got = call(out=(q, None))
+    assert got[0].data_ptr() == q.data_ptr() and torch.equal(q, ref[0]) and torch.equal(got[1], ref[1])
+
+
 def test_quant_of_more_rows_than_one_launch_takes():
     """2^28 + 5 rows of one block: two launches; the rows on both sides of the cut, and the last."""
     M = 2 ** 28 + 5

@@ -260,3 +260,23 @@ def test_refusals():
                                         torch.zeros(65537, dtype=torch.bfloat16, device="cuda"))):
         with pytest.raises(ds.Dsfp8Error):
             bad()
+
+
+@pytest.mark.parametrize("quant", ["e4m3", "e4m3_ue8m0", "mxfp4"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("given", [(True, False), (False, True), (True, True)])
+def test_some_outputs_given(quant, residual, given):
+    """Whichever of y, s and h the caller supplies is what is written and returned."""
+    T, D = 7, 333
+    op, w, _ = operands(T, D, 11, post=False, gate="none", residual=residual)
+    ref = run(op, w, None, quant=quant)
+    buf = list(ds.mxfp4_empty(T, D, "cuda")) if quant == "mxfp4" else [
+        torch.empty((T, D), dtype=torch.uint8, device="cuda"), torch.empty((T, 3), device="cuda")]
+    for b in buf:
+        b.fill_(9)
+    out = [b if g else None for b, g in zip(buf, given)]
+    h = [torch.empty((T, D), dtype=torch.bfloat16, device="cuda")] if residual else []
+    got = run(op, w, None, quant=quant, out=(*out, *h))
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    for g, b in zip(got, [*out, *h]):
+        assert b is None or (g.data_ptr() == b.data_ptr() and g.stride() == b.stride())
