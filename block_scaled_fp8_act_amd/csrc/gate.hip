@@ -186,6 +186,11 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_kernel(GateArgs a, FastD
   if (a.groups > 1) {
     // A group's score, then its rank: a group stays if fewer than top_groups
     // come before it.
+    if (__ballot(bad)) {
+      // an expert whose key is NaN is available: in its group's score, the least number
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) key[j] = key[j] != key[j] ? -0x1.fffffep127f : key[j];
+    }
     const int gs = (int)per_group.d, gl = gs / VPT;
     uint32_t* gsc = group_score[wave][sub];
     const bool lanes = gs % VPT == 0;  // gl lanes hold a group

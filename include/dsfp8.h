@@ -734,7 +734,8 @@ dsfp8_status dsfp8_mxfp4_variant(int64_t E, int64_t M, int64_t N, int64_t K, int
  * in fp32.  Where fewer than k experts are available the last slots get index
  * -1, which the routed-expert calls take as no expert, and weight 0: a token
  * whose logits are all -infinity (padding) goes to none.  A token whose scores
- * or keys contain a NaN gets NaN weights and distinct available experts.
+ * or keys contain a NaN gets NaN weights and distinct available experts, those
+ * of a NaN key after the others and, in a group's score, as the least number.
  *
  *   logits   fp32 or bf16 (dtype) [T, E], row stride ldl  (device, read)
  *   bias     fp32 [E], or NULL                            (device, read)

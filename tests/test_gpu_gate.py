@@ -132,6 +132,34 @@ def test_nan_shows_and_stays_in_its_row():
     assert torch.equal(idx[keep], clean[0][keep]) and torch.equal(w[keep], clean[1][keep])
 
 
+# a group's keys in several lanes, in one, and in parts of lanes; a wave and a quarter of one per token
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T,E,groups", [(3, 64, 2), (3, 256, 8), (3, 384, 6), (3, 250, 5), (3, 1000, 40), (3, 2048, 64),
+                                        (8195, 256, 8), (8195, 250, 5), (8195, 60, 20), (8195, 96, 2)])
+def test_group_of_nan_comes_before_a_masked_one(T, E, groups, bias):
+    """Experts whose keys are NaN are available: a group of them is kept before groups whose experts are all missing,
+    and after one with a number."""
+    size = E // groups
+    x = torch.full((T, E), -float("inf"))
+    x[0, size:2 * size] = float("nan")                  # the only group with experts
+    x[1, -size:] = float("nan")
+    x[2, :size] = float("nan")                          # one NaN group, one of numbers
+    x[2, size:2 * size] = 0.25
+    b = torch.zeros(E, device="cuda") if bias else None
+    idx, w = (v.cpu() for v in ds.moe_gate(x.cuda(), 2, bias=b, groups=groups, top_groups=1))
+    for row, first in ((0, size), (1, E - size), (2, size)):
+        assert idx[row].tolist() == [first, first + 1], row
+        assert torch.isnan(w[row]).all()
+    assert (idx[3:] == -1).all() and not w[3:].any()
+    # a bias of NaN does the same to an expert of every token
+    if bias:
+        b[size:2 * size] = float("nan")
+        x[:] = -float("inf")
+        x[:, size:2 * size] = 0.5
+        idx, w = (v.cpu() for v in ds.moe_gate(x.cuda(), 2, bias=b, groups=groups, top_groups=1))
+        assert (idx == torch.tensor([size, size + 1], dtype=torch.int32)).all() and torch.isnan(w).all()
+
+
 def test_strides_and_out():
     g = I.rng(CID, 9)
     x = g.standard_normal((13, 100)).astype(np.float32)
