@@ -855,6 +855,8 @@ def moe_gate(logits, k, bias=None, score="sigmoid", groups=1, top_groups=None, r
         _mat(logits, "logits", (torch.float32, torch.bfloat16))
     if score not in _SCORES:
         raise Dsfp8Error(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if not hasattr(k, "__index__") or k < 1:
+        raise Dsfp8Error(f"k must be a number of experts from 1 on, got {k!r}")
     T, E = logits.shape
     dev = logits.get_device()
     if bias is not None:

@@ -211,3 +211,11 @@ def test_refusals():
                 lambda: ds.moe_gate(x, 2, out=(torch.zeros((4, 2), device="cuda"), torch.zeros((4, 2), device="cuda")))):
         with pytest.raises(ds.Dsfp8Error):
             bad()
+
+
+@pytest.mark.parametrize("k", [-1, 0, 17, 2.0, None, "2"])
+def test_refused_numbers_of_experts(k):
+    with pytest.raises(ds.Dsfp8Error):
+        ds.moe_gate(torch.zeros((4, 64), device="cuda"), k)
+    with pytest.raises(ds.Dsfp8Error):
+        ds.moe_gate(torch.zeros((4, 64), device="cuda"), k, out=(torch.zeros((4, 2), dtype=torch.int32, device="cuda"), None))
