@@ -855,6 +855,7 @@ dsfp8_status dsfp8_linear_mxfp4(const void* x, int64_t ldx, const void* B, int64
                                 size_t workspace_bytes, hipStream_t stream) {
   if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return DSFP8_ERR_SHAPE;
   DSFP8_TRY(check_mat(x, M, K, ldx, 2));
+  if (16 * mx_blocks(K) >= kMxMaxLd) return DSFP8_ERR_UNSUPPORTED;  // no workspace is asked for either
   const bool fused = dsfp8::linear_mx_fused(M, N, K);
   const size_t need = dsfp8_linear_mxfp4_workspace_bytes(M, N, K);
   if (workspace_bytes < need) return DSFP8_ERR_WORKSPACE;

@@ -674,7 +674,8 @@ dsfp8_status dsfp8_gemm_mxfp4(const void* A, int64_t lda, const void* a_s, int64
  *              aligned (scratch: the codes and scales of x; needs no
  *              initialisation); 0 bytes, and NULL, for few rows, whose
  *              quantisation is part of the product's launch
- * Errors: NULL, SHAPE, LD, ALIGN, UNSUPPORTED, WORKSPACE, LAUNCH.
+ * Limits: K <= 2^24 - 32, ldb < 2^23.
+ * Errors: NULL, SHAPE, LD, ALIGN, UNSUPPORTED (the limits), WORKSPACE, LAUNCH.
  */
 dsfp8_status dsfp8_linear_mxfp4(const void* x, int64_t ldx, const void* B, int64_t ldb, const void* b_s, int64_t ldbs,
                                 void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,

@@ -82,6 +82,19 @@ def test_linear(lib):
     assert c(M=0, x=None, C=None, ws=None, wsb=0) == OK and c(N=0, B=None, b_s=None, C=None) == OK
 
 
+def test_linear_past_its_limit(lib):
+    """K from 2^24 - 31 on, whose rows of codes the product does not take: UNSUPPORTED, with the workspace that the
+    query asks for (none) and with any other."""
+    c = caller(lib.dsfp8_linear_mxfp4, x=P, ldx=1 << 25, B=P, ldb=1 << 23, b_s=P, ldbs=1 << 19, C=P, ldc=8, M=4, N=8,
+               K=1 << 24, ws=None, wsb=0, stream=None)
+    for M in (1, 4, 400):
+        for K in ((1 << 24) - 31, 1 << 24, (1 << 24) + 5):
+            assert lib.dsfp8_linear_mxfp4_workspace_bytes(M, 8, K) == 0
+            assert c(M=M, K=K) == UNSUP and c(M=M, K=K, ws=P, wsb=1 << 40) == UNSUP and c(M=M, K=K, ws=P, wsb=16) == UNSUP
+        assert lib.dsfp8_linear_mxfp4_workspace_bytes(M, 8, (1 << 24) - 32) > 0
+        assert c(M=M, K=(1 << 24) - 32, ldb=(1 << 23) - 16) == WS
+
+
 def test_grouped(lib):
     c = caller(lib.dsfp8_grouped_gemm_mxfp4, A=P, a_rows=10, lda=32, a_s=P, ldas=16, rows=None, B=P, ldb=32, b_s=P,
                ldbs=16, offsets=P, E=3, M=10, N=8, K=64, C=P, ldc=8, stream=None)
