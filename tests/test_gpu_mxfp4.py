@@ -336,6 +336,25 @@ def test_linear_equals_its_steps(M, N, K):
     assert torch.equal(c, ds.linear_mxfp4(wide[:, 3:K + 3], *B))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 4100, 2048), (1, 4097, 7168), (2, 9001, 1000), (3, 18433, 1031), (5, 4500, 4800),
+                                   (16, 5000, 1500)])
+def test_linear_in_one_launch_with_many_columns(M, N, K):
+    """Few rows and more than 16 columns for every CU: 32 columns a workgroup, the last tile ragged, K ending inside a
+    K-block of 256 or with one."""
+    assert ds.linear_mxfp4_workspace_bytes(M, N, K) == 0
+    assert N > 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    xb = I.activations((M, K), CID, 170 + M, outlier_frac=0.02)
+    b, b_s = rows_of(N, K, 171)
+    B = mx_dev(b, b_s)
+    a, a_s = MX.quant(bf16_to_f32(xb))
+    C = torch.full((M + 2, N + 9), 5.0, dtype=torch.bfloat16, device="cuda")
+    c = ds.linear_mxfp4(dev_bf16(xb), *B, out=C[1:M + 1, 5:N + 5])
+    check_product(c, a, a_s, b, b_s)
+    assert torch.equal(c, ds.linear_mxfp4(dev_bf16(xb), *B))
+    c.fill_(5)
+    assert (C == 5).all()
+
+
 def test_linear_nan_row():
     for M in (3, 40):
         x = I.activations((M, 700), CID, 80)
