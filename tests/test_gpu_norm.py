@@ -280,3 +280,20 @@ def test_some_outputs_given(quant, residual, given):
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
     for g, b in zip(got, [*out, *h]):
         assert b is None or (g.data_ptr() == b.data_ptr() and g.stride() == b.stride())
+
+
+# each number of threads and chunks that fp32 weights of more than 2048 columns take, for few rows and, where that
+# is another kernel, for more than two a CU
+@pytest.mark.parametrize("quant", [None, "e4m3", "mxfp4"])
+@pytest.mark.parametrize("T,D", [(3, 2051), (3, 4100), (3, 7171), (3, 16003), (2, 20001), (2, 33001), (1, 65529), (600, 2051),
+                                 (600, 4100), (530, 7171), (520, 16003)])
+def test_wide_rows_with_fp32_weights(T, D, quant):
+    assert T < 4 or T > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    # the sandwich for a few rows, many times over where there are more: the oracle's time is that of seven
+    n = min(T, 7)
+    op, w, pw = operands(n, D, 13 + D, wtype=torch.float32)
+    many = {k: v if v is None else np.resize(v, (T, D)) for k, v in op.items()}
+    got = run(many, w, pw, scale=0.5, quant=quant)
+    for r in range(0, T - n + 1, max(1, (T - n) // 3)):
+        r -= r % n
+        check(tuple(t[r:r + n] for t in got), op, w, pw, quant, D, scale=0.5)
