@@ -197,11 +197,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a)
     } else {
       // From h on in 64 bits: h w is exact, 1 / rms is a factor of the scale and
       // cancels in the code, and what is left is rounded to fp32 on its way to e4m3,
-      // which puts a value halfway between two codes exactly there again.  So a code is
-      // that of the exact y wherever h is exact (in 32 bits 5 in 10^6 codes, all halfway
-      // cases, go by chance; 8192x7168 101 us against 104).  The maximum is over
-      // bit patterns, in which NaN > infinity > every finite value, so that a block
-      // that holds one gets a scale that shows it.
+      // which puts a value halfway between two codes exactly there again (its 64-bit
+      // error is some 2^-50).  Where h and w have 8 significant bits each (no residual,
+      // bf16 weights) nothing else gets there: with hw = a 2^i and the largest b 2^j, a
+      // and b below 2^16, and a halfway point c of 5 bits, 448 hw / top and c differ by
+      // 2^-21 or more, relative, or not at all, so the code is that of the exact y.  With
+      // more bits a quotient within 2^-24 of a halfway point counts as one.  In 32 bits 5
+      // in 10^6 codes, all halfway cases, go by chance (8192x7168 101 us against 104).
+      // With a power-of-two scale, and where the clamp makes the scale, r does not cancel
+      // and its error stays in the quotient.
+      // The maximum is over bit patterns, in which NaN > infinity > every finite value, so
+      // that a block that holds one gets a scale that shows it.
       double hw[8];
       uint64_t top = 0;
 #pragma unroll

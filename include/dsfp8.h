@@ -773,8 +773,15 @@ dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const fl
  *   y, s         y_fmt BF16: y bf16 [T, D], row stride ldy; s is not used
  *                E4M3, E4M3_UE8M0: y e4m3 [T, D], s fp32 [T, KB(D)] with strides
  *                s_row_stride, s_kb_stride: the codes and scales that
- *                dsfp8_act_quant defines, of y = h / rms(h) * weight held in 64
- *                bits, a code dividing by its scale before that is rounded to fp32
+ *                dsfp8_act_quant defines, of y = h / rms(h) * weight in 64 bits
+ *                from fp32 h and 1 / rms(h).  A code divides y by its scale before
+ *                that is rounded to fp32, and rounds the quotient to fp32 and then
+ *                to e4m3.  In E4M3, where max |y| is above the clamp, 1 / rms cancels:
+ *                without a residual and with bf16 weights a code is that of the
+ *                exact quotient, halfway cases included; with more bits in h or
+ *                weight a quotient within 2^-24 of a halfway case (relative) counts
+ *                as one.  In E4M3_UE8M0, and at the clamp, the error of 1 / rms in
+ *                fp32 (50 * 2^-24 at most) stays in the quotient.
  *                MXFP4: y codes [T, 16 KM(D)], s scales [T, KM(D)] with row
  *                stride s_row_stride: dsfp8_mxfp4_quant of the fp32 y
  *                                                          (device, written)

@@ -297,3 +297,17 @@ def test_wide_rows_with_fp32_weights(T, D, quant):
     for r in range(0, T - n + 1, max(1, (T - n) // 3)):
         r -= r % n
         check(tuple(t[r:r + n] for t in got), op, w, pw, quant, D, scale=0.5)
+
+
+@pytest.mark.parametrize("T,D", [(5, 100), (600, 128), (7, 300), (700, 513), (5, 2100), (530, 2100), (3, 4000), (9, 7168), (520, 7001),
+                                 (2, 16000), (2, 20000), (2, 40000)])
+def test_e4m3_codes_of_halfway_cases(T, D):
+    """Without a residual and with bf16 weights a code is that of the exact quotient, halfway cases included, and a row's
+    codes do not change with a power of two."""
+    x, w = NM.halfway_rows(T, D, I.rng(CID, 60 + D))
+    want = NM.e4m3_codes(x, w)
+    x[1::3] *= 2.0 ** -5
+    x[2::3] *= 2.0 ** 20
+    q, s = ds.add_rms_norm(torch.from_numpy(x).bfloat16().cuda(), torch.from_numpy(w).bfloat16().cuda(), eps=0.0, quant="e4m3")
+    assert (s > 1e-4 / 448).all()
+    assert np.array_equal(host_u8(q), want)

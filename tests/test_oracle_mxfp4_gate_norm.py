@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import formats as F
 from oracle import gate as GT
 from oracle import mxfp4 as MX
 from oracle import norm as NM
@@ -102,3 +103,29 @@ def test_norm_invariants():
     np.testing.assert_allclose(h2, r + 0.5 * gate * (x / np.sqrt((x * x).mean(1, keepdims=True)) * w), rtol=1e-12)
     ref = torch.nn.functional.rms_norm(torch.from_numpy(x), (33,), torch.from_numpy(w), 1e-6).numpy()
     np.testing.assert_allclose(NM.forward(x, w)[2], ref, rtol=1e-12)
+
+
+def test_norm_codes_against_fractions():
+    """Codes of the exact quotient, and that a 32-bit evaluation gives others on the same rows: what a kernel is
+    compared with on them tells the two apart."""
+    x, w = NM.halfway_rows(3, 300, np.random.default_rng(3))
+    codes = NM.e4m3_codes(x, w)
+    values = [Fraction(float(v)) for v in F.e4m3_decode(np.arange(127, dtype=np.uint8))]
+    ties = 0
+    for t in range(3):
+        for b in range(0, 300, 128):
+            hw = [Fraction(float(x[t, k])) * Fraction(float(w[k])) for k in range(b, min(300, b + 128))]
+            top = max(abs(v) for v in hw)
+            for k, v in enumerate(hw):
+                q = 448 * abs(v) / top
+                best = min(range(127), key=lambda c: (abs(values[c] - q), c % 2))
+                assert codes[t, b + k] == best | (128 if v < 0 else 0)
+                near = sorted(abs(c - q) for c in values)
+                ties += near[0] == near[1]
+    assert ties > 45                    # one in twenty
+    x, w = NM.halfway_rows(64, 1024, np.random.default_rng(4))
+    y = x * np.float32(NM.inverse_rms(x.astype(np.float64), 1e-6)).astype(np.float32) * w
+    b = y.reshape(64, 8, 128)
+    s = np.abs(b).max(axis=2, keepdims=True) / np.float32(448)
+    off = F.e4m3_encode((b / s).reshape(64, 1024)) != NM.e4m3_codes(x, w)
+    assert off.sum() > 100
