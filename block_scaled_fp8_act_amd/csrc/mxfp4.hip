@@ -7,9 +7,9 @@
 // nearest-even, |q| <= 6; the scale byte is e + 127.  floor(log2) of an fp32
 // value is its exponent field, so the scale byte is that field minus 2, and
 // the division is part of the hardware's conversion, which rounds exactly
-// (checked over every bf16 value and every scale).  A block that holds a NaN
-// or an infinity has the field 255 and gets the scale byte 255, the format's
-// NaN.
+// (its tests hold every bf16 value against every scale it can have).  A block that
+// holds a NaN or an infinity has the field 255 and gets the scale byte 255, the
+// format's NaN.
 #include <type_traits>
 
 #include "device.h"

@@ -86,6 +86,22 @@ def test_every_bf16_value_against_every_top():
     assert np.array_equal(host_u8(s), sr) and np.array_equal(host_u8(q), qr)
 
 
+def test_every_bf16_value_of_every_scale():
+    """For each scale (the largest value of each of bf16's binades, and of its subnormals, at the head of every block) all
+    bf16 values of either sign up to that largest one."""
+    for first in range(0, 255, 15):
+        rows = []
+        for f in range(first, first + 15):
+            v = np.arange((f + 1) << 7, dtype=np.uint16)
+            v = np.concatenate([v, v | 0x8000])
+            v = np.concatenate([v, np.zeros(-len(v) % 31, np.uint16)]).reshape(-1, 31)
+            rows.append(np.concatenate([np.full((len(v), 1), (f << 7) | 0x7f, np.uint16), v], 1))
+        x = np.concatenate(rows)
+        q, s = ds.mxfp4_quant(dev_bf16(x))
+        qr, sr = MX.quant(bf16_to_f32(x))
+        assert np.array_equal(host_u8(s), sr) and np.array_equal(host_u8(q), qr), first
+
+
 def test_halfway_cases_and_subnormals():
     steps = np.concatenate([MX.HALFWAY, np.nextafter(MX.HALFWAY.astype(np.float32), np.float32(0)),
                             np.nextafter(MX.HALFWAY.astype(np.float32), np.float32(9)), [0, 6, 7, 7.9, 0.1]])
