@@ -787,7 +787,9 @@ dsfp8_status dsfp8_moe_gate(const void* logits, int dtype, int64_t ldl, const fl
  *                                                          (device, written)
  * A row with a NaN shows it in its outputs (a quantised y in its scales) and
  * changes no other row; a row of finite values whose squares add up past fp32's
- * range gives zeros.  The bytes of a row do not depend on T.  h may be residual or x, and a bf16 y may be x, with the
+ * range gives zeros.  With eps = 0 a row of zeros gives NaN and one whose squares
+ * all vanish in fp32 infinities, as 1 / rms is infinite there.  The bytes of a row do
+ * not depend on T.  h may be residual or x, and a bf16 y may be x, with the
  * same stride; otherwise outputs must not overlap inputs.  Without a residual,
  * post_weight and gate must be NULL and scale 1.
  * Limits: D <= 65536, eps >= 0.

@@ -311,3 +311,18 @@ def test_e4m3_codes_of_halfway_cases(T, D):
     q, s = ds.add_rms_norm(torch.from_numpy(x).bfloat16().cuda(), torch.from_numpy(w).bfloat16().cuda(), eps=0.0, quant="e4m3")
     assert (s > 1e-4 / 448).all()
     assert np.array_equal(host_u8(q), want)
+
+
+def test_eps_zero():
+    """eps = 0 is taken: a row of zeros, or of values whose squares vanish in fp32, shows it and changes no other row."""
+    x = torch.ones((5, 300), dtype=torch.bfloat16, device="cuda")
+    x[1], x[3] = 0, 1e-30
+    w = torch.ones(300, device="cuda")
+    y = ds.add_rms_norm(x, w, eps=0.0)
+    assert torch.isnan(y[1]).all() and torch.isinf(y[3]).all() and (y[[0, 2, 4]] == 1).all()
+    for quant in ("e4m3", "e4m3_ue8m0", "mxfp4"):
+        q, s = ds.add_rms_norm(x, w, eps=0.0, quant=quant)
+        shown = s == 255 if quant == "mxfp4" else ~torch.isfinite(s)
+        assert shown[[1, 3]].all() and not shown[[0, 2, 4]].any()
+    y, h = ds.add_rms_norm(x, w, residual=x, post_weight=w, eps=0.0)
+    assert torch.isnan(h[1]).all() and torch.isinf(h[3]).all() and (h[[0, 2, 4]] == 2).all() and (y[[0, 2, 4]] == 1).all()
