@@ -6,6 +6,10 @@ follow, then the experts: the up-projection of the tokens' rows, read through th
 (``grouped_gemm_mxfp4``), the gate and the next quantisation (``silu_mul_mxfp4_quant``), the down-projection and the
 weighted sum (``moe_combine``).  Nothing is synchronised, so the block is captured into a HIP graph and replayed.
 
+The router is an MXFP4 weight here, since the norm hands its result out in that format alone, and its logits are bf16.
+The choice of experts hangs on them: a model trained with its router in bf16 or fp32 keeps it so, takes the router's input
+from the residual stream through a norm of its own, and gives ``moe_gate`` fp32 logits.
+
     python examples/mxfp4_moe_block.py --tokens 64 [--experts 64 --topk 6 --groups 8 --top-groups 3 --dim 2048 --inter 1024]
 
 prints the block's time, eager and as a graph.
