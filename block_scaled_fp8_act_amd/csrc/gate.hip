@@ -10,9 +10,10 @@
 // rounds takes the maximum over the token's lanes (DPP steps) and its first
 // holder, which puts itself into the round's slot in LDS.
 //
-// 16384x256 in 8 groups: 18.4 us (softmax without groups 16.1), 1.0 TB/s; the
-// instructions of the scores and of the k rounds bound it, not its 17.6 MB.  One
-// token: 4.3 us, a chain of dependent steps.
+// 16384x256 in 8 groups: 18.2 us (softmax without groups 16.4), 1.0 TB/s; its
+// instructions bound it, not its 17.6 MB: the last seven of eight rounds are 5.1 us, the
+// scores 4.7 (the logits in their place), the groups 2.1 (one group), the rest 5.3.  One
+// token: 4.3 to 4.8 us, a chain of dependent steps.
 #include "device.h"
 #include "launch.h"
 
@@ -339,7 +340,9 @@ hipError_t launch_gate(const GateArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   // A quarter of a wave per token issues less for a token but takes longer for it:
   // 16384x256 in groups 18.4 us against 20.0, 8192x256 10.0 against 11.0, 16384x64 5.4
-  // against 7.8, but 4096x128 4.0 against 3.9.
+  // against 7.8, but 4096x128 4.0 against 3.9.  Past 256 experts it has not been
+  // made: 24 a lane would take 16384x384 in 19.6 us against 25.2 (8192x384 12.7
+  // against 14.5), 32 a lane 16384x512 in 28.5 against 24.2.
   if (a.T >= 8192 && a.E <= 256) {
     if (a.E <= 64) return launch_gate_of<4, 16>(a, stream);
     if (a.E <= 128) return launch_gate_of<8, 16>(a, stream);

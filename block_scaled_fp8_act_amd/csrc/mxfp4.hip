@@ -229,11 +229,15 @@ __device__ __forceinline__ bool mx_find(const MxGemmArgs& p, int64_t want, MxTil
 // the last step of the current one, whose operands are in registers by then.
 // The stage it leaves is refilled behind that step's instructions.
 //
-// 256x256 tiles, 4096x7168x18432: 269 us (4.0 PFLOP/s; 4096x18432x7168 292).  Two
+// 256x256 tiles, 4096x7168x18432: 269 us (4.0 PFLOP/s; 4096x18432x7168 297-301).  Two
 // things bound it, close together: without the loads the rest takes 228 us (the matrix
 // cores at the clock that the power allows: 6.1-7.1 PFLOP/s from registers alone),
 // without the matrix instructions 230 us (of which the scales' loads, a line per
-// row, are 27; LDS reads alone take 116).  Stages of 64 bytes a row, four of
+// row, are 27; LDS reads alone take 116).  Two more add to both: the last round of
+// workgroups (1.75 rounds over the CUs run as two, an eighth of their time idle;
+// 4096x18432x7168 4.5 as five, a tenth), and reading the scales from LDS, dwords at a
+// stride of 16 bytes: without these reads 254 us (283), and of the bank conflicts, 14% of
+// the cycles, 1% stay.  Stages of 64 bytes a row, four of
 // them or three, took 294 us; waves of 128x128, four a workgroup, 290.
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
@@ -932,16 +936,19 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   }
 }
 
-// The quantisation costs every workgroup a pass over all rows, 16384 elements at a time:
-// one launch takes 4.6 us against 6.4 in two for 1x7168x2048, 5.3 against
-// 6.6 for 8x7168x2048, and as long for 4x18432x7168.
+// The quantisation costs every workgroup a pass over all rows, 16384 elements at a time.
+// One launch takes 4.6 us against 6.1 in two for 1x1536x7168, 5.3 against 7.1 for
+// 8x7168x2048, 17.4 against 19.2 for 3x18432x7168, 87 against 90 for 3x129280x7168.  The
+// bounds on M and K do not weigh N, and with many rows and very many columns two
+// launches are faster: 16x18432x1536 8.9 us against 11.0, 8x129280x2048 29 against 36.
 bool linear_mx_fused(int64_t M, int64_t N, int64_t K) {
   const int64_t nkb = (K + 255) / 256;
   return M <= 16 && N <= 16 * (int64_t)kMaxSplitTiles && M * nkb * 256 <= 24576 && M * (mx_code_ld((int)nkb) + mx_scale_ld((int)nkb)) <= kFusedBytes;
 }
 
-// 16 columns a workgroup where those are one round over the CUs (1x1536x7168 5.0 us,
-// with 32 5.8), else 32, which quantise half as often (4x18432x7168 17.8 us, with 16 21.1).
+// 16 columns a workgroup where those are one round over the CUs (1x1536x7168 5.4 us,
+// with 32 6.9; 1x4096x7168 6.3 and 7.3), else 32, which quantise half as often
+// (3x18432x7168 16.9 us, with 16 19.2; 1x18432x7168 15.6 and 15.3).
 hipError_t launch_linear_mx_fused(const MxGemmArgs& g, const MxQuantArgs& q, hipStream_t stream) {
   if (g.N <= 16 * (int64_t)device_cu_count()) return launch_mx_split<1, 1, 2, true>(g, q, stream);
   return launch_mx_split<1, 2, 1, true>(g, q, stream);

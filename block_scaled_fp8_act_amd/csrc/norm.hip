@@ -12,8 +12,10 @@
 // block in a quad.
 //
 // Bytes bound it: 8192x7168 with both norms and a gate 106 us, 5.5 TB/s; residual
-// to e4m3 84 us, 4.9 TB/s (a copy reaches 4.96).  32x7168 4.1 us: one trip to memory
-// and one sum over the workgroup.
+// to e4m3 80-84 us, 4.9-5.2 TB/s, to MXFP4 71 us (a copy reaches 4.96).  32x7168 4.1 us:
+// one trip to memory and one sum over the workgroup.  Rows that do not start at
+// multiples of 16 bytes are read and written at their own addresses, 16 bytes a lane,
+// which touch more lines: 8192x7167 with both norms and a gate 178 us, 3.3 TB/s.
 #include "device.h"
 #include "launch.h"
 
