@@ -317,6 +317,31 @@ def test_gemm_nan_scales():
         assert np.array_equal(np.isnan(c), nan)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 40, 320), (40, 50, 600), (300, 300, 320), (900, 5003, 320), (3000, 12000, 288)])
+def test_gemm_scales_at_the_ends_of_their_range(M, N, K):
+    """A block's two scales meet as one power of two, whatever they are alone.  Below 2^-126 bf16's values are 2^-133
+    apart, so the output's rounding is off by up to 2^-134 there."""
+    a, _ = rows_of(M, K, 65)
+    b, _ = rows_of(N, K, 66)
+    for ea, eb in [(0, 254), (254, 0), (1, 253), (0, 150), (254, 60), (20, 100), (60, 60), (0, 0)]:
+        a_s, b_s = np.full((M, MX.blocks(K)), ea, np.uint8), np.full((N, MX.blocks(K)), eb, np.uint8)
+        c = bf16_to_f64(host_bits16(ds.gemm_mxfp4(*mx_dev(a, a_s), *mx_dev(b, b_s))[-50:, -50:]))
+        ref, bound = MX.gemm(a[-50:], a_s[-50:], b[-50:], b_s[-50:])
+        assert np.all(np.abs(c - ref) <= (np.abs(ref) + bound) * 2.0 ** -8 + bound + 2.0 ** -134), (ea, eb)
+
+
+def test_torch_types_of_codes_and_scales():
+    """torch's own types for two e2m1 codes a byte and for powers of two are taken as bytes."""
+    f4, e8 = torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+    (a, a_s), (b, b_s) = (mx_dev(*rows_of(r, 320, 67)) for r in (70, 48))
+    ref = ds.gemm_mxfp4(a, a_s, b, b_s)
+    assert torch.equal(ref, ds.gemm_mxfp4(a.view(f4), a_s.view(e8), b.view(f4), b_s.view(e8)))
+    assert torch.equal(ref, ds.gemm_mxfp4(a, a_s, b.view(f4), b_s))
+    assert torch.equal(ds.mxfp4_dequant(a, a_s, 300), ds.mxfp4_dequant(a.view(f4), a_s.view(e8), 300))
+    x = torch.randn((2, 320), device="cuda").bfloat16()
+    assert torch.equal(ds.linear_mxfp4(x, b, b_s), ds.linear_mxfp4(x, b.view(f4), b_s.view(e8)))
+
+
 def test_empty_products():
     for M, N in [(0, 5), (5, 0)]:
         assert ds.gemm_mxfp4(*ds.mxfp4_empty(M, 64, "cuda"), *ds.mxfp4_empty(N, 64, "cuda")).shape == (M, N)
